@@ -381,6 +381,83 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
                                      const float* w2_global_scales, int64_t E, int64_t I, void* workspace,
                                      void* out, uint32_t* invalid_pairs, void* stream);
 
+/*
+ * Log probabilities of given tokens, from the logits a GEMM above wrote (or
+ * any other logits).
+ *
+ * Row i holds V logits of type `dtype` at logits + i * row_stride elements
+ * (row_stride >= V; rows need only the element's own alignment).  With
+ * z[i, j] = logits[i, j] / temperature[i] over the allowed tokens of the row:
+ *   lse[i]            = log sum_j exp(z[i, j])
+ *   token_logprobs[i] = z[i, id] - lse[i],  id = token_ids[i]
+ *   token_ranks[i]    = 1 + (how many allowed logits of the row are larger than the token's)
+ *   entropy[i]        = -sum_j p[i, j] log p[i, j],  p = exp(z - lse)
+ *   top_ids[i, 0..topk), top_logprobs: the largest allowed logits in falling
+ *                       order, equal ones in the order of their index
+ * All sums are float32 (per lane, then joined pairwise); selection and ranks
+ * compare the logits themselves, exactly (-0 equals 0).  The outputs do not
+ * depend on timing: the same call gives the same bits.
+ */
+typedef enum {
+  NVFP4_BF16 = 0,
+  NVFP4_F16 = 1,
+  NVFP4_F32 = 2
+} nvfp4_dtype;
+
+/*
+ * nvfp4_logprobs_workspace_bytes -- workspace of nvfp4_logprobs (host helper;
+ * at least 16; 0 for sizes the call rejects).
+ *
+ * nvfp4_logprobs
+ *   logits         in  dtype [M, V] rows of row_stride elements, aligned to the element
+ *   M, V           in  0 <= M <= 2^23 (M == 0 enqueues nothing), 1 <= V <= 2^30
+ *   token_ids      in  optional int32 [M] (NULL = none); a row whose id is outside [0, V)
+ *                      has no given token: logprob 0, rank 0
+ *   temperatures   in  optional float [M] (NULL = 1); 1 / temperature must be finite; one that
+ *                      is not > 0 (a greedy row) counts as 1
+ *   allowed        in  optional uint32 [M, ceil(V / 32)]: token j is allowed if bit j % 32 of
+ *                      word j / 32 is set; logits of the others are not looked at, whatever
+ *                      they hold (NULL = all allowed)
+ *   topk           in  0 .. 64 alternatives
+ *   workspace      tmp nvfp4_logprobs_workspace_bytes(M, V, topk) bytes, 16-byte aligned
+ *   token_logprobs, token_ranks, lse, entropy   out  float / int32 [M], each optional (NULL)
+ *   top_logprobs, top_ids   out  float / int32 [M, topk] (NULL only if topk == 0)
+ *
+ * A logit of -inf has probability 0: a given token there has logprob -inf, and
+ * it is never an alternative.  Where fewer than topk alternatives exist the
+ * rest are id -1, logprob -inf.  A row with nothing allowed, or only -inf, has
+ * lse -inf, entropy 0, logprob -inf and no alternatives.  An allowed NaN or
+ * +inf makes the row's lse, entropy and logprobs NaN; a NaN is never an
+ * alternative.
+ */
+int64_t nvfp4_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk);
+nvfp4_status nvfp4_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride,
+                            const int32_t* token_ids, const float* temperatures, const uint32_t* allowed,
+                            int64_t topk, void* workspace, float* token_logprobs, int32_t* token_ranks, float* lse,
+                            float* entropy, float* top_logprobs, int32_t* top_ids, void* stream);
+
+/*
+ * nvfp4_logprobs_backward -- the gradient of a loss through token_logprobs,
+ * entropy and lse to the logits:
+ *   dlogits[i, j] = (1 / T) * ( dlogprob[i] * 1[j = id] + p * (dlse[i] - dlogprob[i]
+ *                               - dentropy[i] * (log p + entropy[i])) ),   log p = z[i, j] - lse[i]
+ * in float32, rounded once to dtype.  Tokens that are not allowed, logits of
+ * -inf and rows with lse -inf get 0.
+ *
+ *   logits, token_ids, temperatures, allowed   in  as given to nvfp4_logprobs
+ *   lse, entropy   in  float [M] as nvfp4_logprobs wrote them (entropy only with dentropy)
+ *   dlogprob, dentropy, dlse   in  float [M], each optional (NULL = 0); a row without a given
+ *                                  token takes dlogprob as 0
+ *   dlogits        out dtype [M, V] rows of dlogits_stride elements; it may be logits itself
+ *                      (same pointer and stride: the gradient replaces the logits) and
+ *                      otherwise overlaps no input
+ */
+nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride,
+                                     const int32_t* token_ids, const float* temperatures, const uint32_t* allowed,
+                                     const float* lse, const float* entropy, const float* dlogprob,
+                                     const float* dentropy, const float* dlse, void* dlogits,
+                                     int64_t dlogits_stride, void* stream);
+
 /* Host-side helpers (no device work). */
 const char* nvfp4_status_string(int status);   /* static string for a status code        */
 const char* nvfp4_last_hip_error(void);        /* last HIP error text of this thread, or "" */

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -43,6 +44,7 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_refresh_inplace", "nvfp4_w4a16_gemm",
             "nvfp4_w4a4_gemm_noalloc",
             "nvfp4_moe_gemm_workspace_bytes", "nvfp4_moe_w4a16_gemm", "nvfp4_moe_silu_and_mul",
             "nvfp4_moe_combine", "nvfp4_moe_workspace_bytes", "nvfp4_moe_w4a16_forward",
+            "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "nvfp4_logprobs_backward",
             "nvfp4_status_string", "nvfp4_last_hip_error", "nvfp4_abi_version")
 
 
@@ -111,6 +113,13 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_moe_w4a16_forward.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp,
                                             vp, vp]
     lib.nvfp4_moe_w4a16_forward.restype = ctypes.c_int
+    lib.nvfp4_logprobs_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.nvfp4_logprobs_workspace_bytes.restype = i64
+    lib.nvfp4_logprobs.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.nvfp4_logprobs.restype = ctypes.c_int
+    lib.nvfp4_logprobs_backward.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64,
+                                            vp]
+    lib.nvfp4_logprobs_backward.restype = ctypes.c_int
     lib.nvfp4_status_string.argtypes = [ctypes.c_int]
     lib.nvfp4_status_string.restype = ctypes.c_char_p
     lib.nvfp4_last_hip_error.argtypes = []
@@ -553,4 +562,127 @@ def nvfp4_moe_w4a16_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weight
            lib.nvfp4_moe_w4a16_forward(_ptr(x), t, hdim, _ptr(ids), _ptr(w), topk, _ptr(w13[0]), _ptr(w13[1]),
                                        _ptr(w13[2]), _ptr(w2[0]), _ptr(w2[1]), _ptr(w2[2]), e, i,
                                        _ptr(workspace), _ptr(out), _ptr(invalid_pairs), _stream_of(x, stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Log probabilities of given tokens
+# ---------------------------------------------------------------------------
+
+#: Logit types of the log-probability calls (nvfp4_dtype).
+LOGIT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+#: Most alternatives nvfp4_logprobs reports for a row.
+LOGPROBS_MAX_TOPK = 64
+
+
+class Logprobs(NamedTuple):
+    """Outputs of nvfp4_logprobs, and the workspace that goes with them."""
+    token_logprobs: torch.Tensor      # float32 [M]
+    token_ranks: torch.Tensor         # int32 [M]
+    lse: torch.Tensor                 # float32 [M]
+    entropy: torch.Tensor             # float32 [M]
+    top_logprobs: torch.Tensor        # float32 [M, topk]
+    top_ids: torch.Tensor             # int32 [M, topk]
+    workspace: torch.Tensor           # uint8, free again once the stream is past the call
+
+
+def logprobs_buffers(m: int, v: int, topk: int, device) -> Logprobs:
+    """Output buffers and workspace of nvfp4_logprobs for [m, v] logits, to be
+    kept and passed as ``out``."""
+    need = int(load_library().nvfp4_logprobs_workspace_bytes(m, v, topk))
+    if need == 0:
+        raise NVFP4ShapeError("nvfp4_logprobs", 2, f"M={m}, V={v}, topk={topk}")
+    f = dict(dtype=torch.float32, device=device)
+    i = dict(dtype=torch.int32, device=device)
+    return Logprobs(torch.empty((m,), **f), torch.empty((m,), **i), torch.empty((m,), **f), torch.empty((m,), **f),
+                    torch.empty((m, topk), **f), torch.empty((m, topk), **i),
+                    torch.empty((need,), dtype=torch.uint8, device=device))
+
+
+def _check_logits(t: torch.Tensor, what: str) -> tuple:
+    """(dtype code, M, V, row stride) of 2-D logits whose rows are dense."""
+    code = LOGIT_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what} must be a 2-D device tensor, got shape {tuple(t.shape)} on {t.device}")
+    m, v = t.shape
+    stride = t.stride(0) if m > 1 else v
+    if (v > 1 and t.stride(1) != 1) or stride < v:
+        raise ValueError(f"{what} rows must be dense and not overlap, got strides {t.stride()}")
+    return code, m, v, stride
+
+
+def _check_vec(t, m: int, dtype, dev, what: str):
+    if t is not None and (t.dtype != dtype or t.dim() != 1 or t.shape[0] != m or t.device != dev
+                          or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected contiguous ({m},) {dtype} on {dev}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _check_allowed(t, m: int, v: int, dev):
+    if t is not None:
+        _check_out(t, (m, (v + 31) // 32), (torch.int32, torch.uint32), dev, "allowed")
+
+
+def nvfp4_logprobs(logits: torch.Tensor, token_ids: torch.Tensor | None = None, topk: int = 0,
+                   temperatures: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
+                   out: Logprobs | None = None, stream=None) -> Logprobs:
+    """Log probability and rank of the given token of each row of ``logits``
+    [M, V] (bfloat16, float16 or float32; rows dense, any row stride), with the
+    row's lse and entropy and its ``topk`` best alternatives.  ``token_ids``
+    int32 [M], ``temperatures`` float32 [M], ``allowed`` int32 or uint32 [M, ceil(V / 32)]
+    (bit j % 32 of word j / 32 allows token j).  ``out`` = kept logprobs_buffers(M, V, topk)."""
+    code, m, v, stride = _check_logits(logits, "logits")
+    dev = logits.device
+    _check_vec(token_ids, m, torch.int32, dev, "token_ids")
+    _check_vec(temperatures, m, torch.float32, dev, "temperatures")
+    _check_allowed(allowed, m, v, dev)
+    lib = load_library()
+    if out is None:
+        out = logprobs_buffers(m, v, topk, dev)
+    else:
+        for t, what in ((out.token_logprobs, "token_logprobs"), (out.lse, "lse"), (out.entropy, "entropy")):
+            _check_vec(t, m, torch.float32, dev, what)
+        _check_vec(out.token_ranks, m, torch.int32, dev, "token_ranks")
+        _check_out(out.top_logprobs, (m, topk), (torch.float32,), dev, "top_logprobs")
+        _check_out(out.top_ids, (m, topk), (torch.int32,), dev, "top_ids")
+        need = int(lib.nvfp4_logprobs_workspace_bytes(m, v, topk))
+        if out.workspace.numel() * out.workspace.element_size() < need or out.workspace.device != dev:
+            raise ValueError(f"workspace needs {need} bytes on {dev}")
+    _check("nvfp4_logprobs",
+           lib.nvfp4_logprobs(_ptr(logits), code, m, v, stride, _ptr(token_ids), _ptr(temperatures), _ptr(allowed),
+                              topk, _ptr(out.workspace), _ptr(out.token_logprobs), _ptr(out.token_ranks),
+                              _ptr(out.lse), _ptr(out.entropy), _ptr(out.top_logprobs), _ptr(out.top_ids),
+                              _stream_of(logits, stream)))
+    return out
+
+
+def nvfp4_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor | None, lse: torch.Tensor,
+                            entropy: torch.Tensor | None = None, dlogprob: torch.Tensor | None = None,
+                            dentropy: torch.Tensor | None = None, dlse: torch.Tensor | None = None,
+                            temperatures: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient with respect to ``logits`` from the gradients of nvfp4_logprobs'
+    token_logprobs, entropy and lse (each float32 [M] or None).  ``out`` may be
+    ``logits`` itself."""
+    code, m, v, stride = _check_logits(logits, "logits")
+    dev = logits.device
+    _check_vec(token_ids, m, torch.int32, dev, "token_ids")
+    for t, what in ((lse, "lse"), (entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy"),
+                    (dlse, "dlse"), (temperatures, "temperatures")):
+        _check_vec(t, m, torch.float32, dev, what)
+    _check_allowed(allowed, m, v, dev)
+    if out is None:
+        out = torch.empty((m, v), dtype=logits.dtype, device=dev)
+    ocode, om, ov, ostride = _check_logits(out, "out")
+    if (ocode, om, ov) != (code, m, v) or out.device != dev:
+        raise ValueError(f"out: expected {(m, v)} {logits.dtype} on {dev}, got {tuple(out.shape)} {out.dtype} "
+                         f"on {out.device}")
+    lib = load_library()
+    _check("nvfp4_logprobs_backward",
+           lib.nvfp4_logprobs_backward(_ptr(logits), code, m, v, stride, _ptr(token_ids), _ptr(temperatures),
+                                       _ptr(allowed), _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy),
+                                       _ptr(dlse), _ptr(out), ostride, _stream_of(logits, stream)))
     return out

@@ -1,0 +1,646 @@
+// Log probabilities of given tokens, with their rank, the entropy and the top
+// alternatives, from the logits that the lm_head produced, and the gradient
+// (gfx950).
+//
+// Forward.  For a row x[0..V) with temperature T, z = x / T, over the allowed
+// tokens: lse = log sum_j exp(z_j), logprob = z_id - lse, H = -sum_j p_j log p_j.
+// One pass over the row keeps, per lane, the running maximum and the two sums
+//   s = sum 2^(y_j),  t = sum 2^(y_j) y_j,   y_j = z_j log2(e) - m2,
+// rescaled when the maximum m2 grows (s' = s a, t' = (t + s (m2 - m2')) a with
+// a = 2^(m2 - m2')); then lse = m2 ln 2 + log s and H = log s - (t / s) ln 2.
+// The rank is a count of larger logits in the same pass.
+//
+// Top alternatives: each wavefront keeps its best 64 as one 64-bit key per
+// lane, sorted, key = (order-preserving image of the logit, ~index), so equal
+// logits order by the lower index and every comparison is exact.  A group of
+// 16 logits per lane is only looked at when some lane's maximum reaches the
+// k-th best so far.  Lists of two wavefronts or segments merge by a bitonic
+// step: max(a[i], b[63 - i]), then six compare-exchanges.
+//
+// With few rows a row is split into segments, one workgroup each; a second
+// kernel joins the segments' sums, counts and lists in segment order (no
+// atomics, so results do not depend on timing).
+//
+// Backward.  d logprob / dz_j = 1[j = id] - p_j, dH / dz_j = -p_j (log p_j + H),
+// dlse / dz_j = p_j: one read and one write per logit, p_j recomputed from lse.
+//
+// Rows start at any element (2-byte or 4-byte) alignment: the 16-byte accesses
+// below are declared with the element's alignment.
+#include <algorithm>
+
+#include "nvfp4_device.hpp"
+#include "nvfp4_launch.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kLpThreads = 256;
+constexpr int kLpWaves = kLpThreads / 64;
+constexpr int kGroup16 = 16;                 // logits per lane and step
+constexpr int kJoinWaves = 8;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLowest = -3.40282346638528859812e38f;
+constexpr float kM2Init = -3.0e38f;          // below every finite scaled maximum that matters, itself finite
+
+constexpr int kBf16 = 0, kF16 = 1, kF32 = 2;
+
+struct __attribute__((packed, aligned(2))) Vec16A2 { u32x4 v; };
+struct __attribute__((packed, aligned(4))) Vec16A4 { u32x4 v; };
+
+template <int DT> struct Elem;
+template <> struct Elem<kBf16> {
+  static constexpr int kBytes = 2, kPerVec = 8;
+  static constexpr uint32_t kNegInf = 0xFF80FF80u;
+  static __device__ __forceinline__ u32x4 load(const uint8_t* p) { return reinterpret_cast<const Vec16A2*>(p)->v; }
+  static __device__ __forceinline__ void store(uint8_t* p, u32x4 v) { reinterpret_cast<Vec16A2*>(p)->v = v; }
+  static __device__ __forceinline__ uint32_t bits(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b << 16); }
+  static __device__ __forceinline__ void unpack(u32x4 v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(v[i]);
+      f[2 * i + 1] = bf16_hi(v[i]);
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float* f) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)f[2 * i], (__bf16)f[2 * i + 1]});
+    return o;
+  }
+};
+template <> struct Elem<kF16> {
+  static constexpr int kBytes = 2, kPerVec = 8;
+  static constexpr uint32_t kNegInf = 0xFC00FC00u;
+  static __device__ __forceinline__ u32x4 load(const uint8_t* p) { return reinterpret_cast<const Vec16A2*>(p)->v; }
+  static __device__ __forceinline__ void store(uint8_t* p, u32x4 v) { reinterpret_cast<Vec16A2*>(p)->v = v; }
+  static __device__ __forceinline__ uint32_t bits(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
+  static __device__ __forceinline__ float value(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
+  static __device__ __forceinline__ void unpack(u32x4 v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = v[i];                 // a value: bit_cast of a vector's element takes element 0
+      const f16x2 h = __builtin_bit_cast(f16x2, w);
+      f[2 * i] = (float)h[0];
+      f[2 * i + 1] = (float)h[1];
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float* f) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)f[2 * i], (_Float16)f[2 * i + 1]});
+    return o;
+  }
+};
+template <> struct Elem<kF32> {
+  static constexpr int kBytes = 4, kPerVec = 4;
+  static constexpr uint32_t kNegInf = 0xFF800000u;
+  static __device__ __forceinline__ u32x4 load(const uint8_t* p) { return reinterpret_cast<const Vec16A4*>(p)->v; }
+  static __device__ __forceinline__ void store(uint8_t* p, u32x4 v) { reinterpret_cast<Vec16A4*>(p)->v = v; }
+  static __device__ __forceinline__ uint32_t bits(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
+  static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
+  static __device__ __forceinline__ void unpack(u32x4 v, float* f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float* f) {
+    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
+};
+
+// Elements [j, V) of a row whose last vector is cut: the missing ones are -inf.
+template <int DT>
+__device__ __forceinline__ u32x4 load_tail(const uint8_t* row, int j, int V) {
+  u32x4 v = {Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf, Elem<DT>::kNegInf};
+#pragma unroll
+  for (int e = 0; e < Elem<DT>::kPerVec; ++e) {
+    if (j + e < V) {
+      const uint32_t b = Elem<DT>::bits(row + (int64_t)(j + e) * Elem<DT>::kBytes);
+      if (DT == kF32) {
+        v[e & 3] = b;
+      } else {
+        const int w = (e >> 1) & 3;
+        v[w] = (e & 1) ? ((v[w] & 0xFFFFu) | (b << 16)) : ((v[w] & 0xFFFF0000u) | b);
+      }
+    }
+  }
+  return v;
+}
+
+// A row's temperature as 1 / T; a temperature that is not greater than 0
+// (greedy rows) counts as 1.
+__device__ __forceinline__ float inv_temperature(const float* temps, int64_t row) {
+  if (!temps) return 1.0f;
+  const float t = temps[row];
+  return t > 0.0f ? 1.0f / t : 1.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Sorted lists of 64 keys, one per lane, best first; 0 = empty.
+// ---------------------------------------------------------------------------
+struct Key {
+  uint32_t hi, lo;                           // order-preserving image of the logit; ~index
+};
+
+__device__ __forceinline__ bool key_gt(Key a, Key b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+__device__ __forceinline__ uint32_t key_image(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);          // -0 compares equal to +0
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t h) {
+  return __uint_as_float((h >> 31) ? (h & 0x7FFFFFFFu) : ~h);
+}
+
+// Insert the (wavefront-uniform) key c; the last lane's key falls out.
+__device__ __forceinline__ void list_insert(Key& k, Key c, int lane) {
+  const bool ahead = key_gt(k, c);
+  const int pos = __popcll(__ballot(ahead));
+  Key up;
+  up.hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)k.hi, 0x138, 0xF, 0xF, false);   // wave_shr:1
+  up.lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)k.lo, 0x138, 0xF, 0xF, false);
+  if (!ahead) {
+    k.hi = lane == pos ? c.hi : up.hi;
+    k.lo = lane == pos ? c.lo : up.lo;
+  }
+}
+
+// Best 64 of two sorted lists, sorted.
+__device__ __forceinline__ Key list_merge(Key a, Key b, int lane) {
+  Key r;
+  r.hi = (uint32_t)__shfl((int)b.hi, 63 - lane, 64);
+  r.lo = (uint32_t)__shfl((int)b.lo, 63 - lane, 64);
+  Key k = key_gt(a, r) ? a : r;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    Key o;
+    o.hi = (uint32_t)__shfl_xor((int)k.hi, d, 64);
+    o.lo = (uint32_t)__shfl_xor((int)k.lo, d, 64);
+    const bool keep_max = (lane & d) == 0;
+    if (key_gt(o, k) == keep_max) k = o;
+  }
+  return k;
+}
+
+// Softmax sums of a set of logits.
+struct Sums {
+  float m2, s, t;                            // scaled maximum, sum 2^y, sum 2^y y
+  float raw;                                 // largest logit
+};
+
+__device__ __forceinline__ void rescale(float& m2, float& s, float& t, float to) {
+  const float d = m2 - to;                   // <= 0
+  const float a = __builtin_amdgcn_exp2f(d);
+  t = __builtin_fmaf(s, d, t) * a;
+  s *= a;
+  m2 = to;
+}
+
+__device__ __forceinline__ Sums combine(Sums a, Sums b) {
+  const float to = fmaxf(a.m2, b.m2);
+  rescale(a.m2, a.s, a.t, to);
+  rescale(b.m2, b.s, b.t, to);
+  return Sums{to, a.s + b.s, a.t + b.t, fmaxf(a.raw, b.raw)};
+}
+
+__device__ __forceinline__ Sums wave_combine(Sums a) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    Sums b;
+    b.m2 = __shfl_xor(a.m2, d, 64);
+    b.s = __shfl_xor(a.s, d, 64);
+    b.t = __shfl_xor(a.t, d, 64);
+    b.raw = __shfl_xor(a.raw, d, 64);
+    a = combine(a, b);
+  }
+  return a;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Forward.
+// ---------------------------------------------------------------------------
+namespace {
+
+// The given token's logit of a row: NaN-free flag `given` tells whether there
+// is one; a token that is not allowed counts as -inf.
+template <int DT>
+__device__ __forceinline__ float token_logit(const LogprobsArgs& a, const uint8_t* row, int64_t i, bool* given) {
+  *given = false;
+  if (!a.tok) return 0.0f;
+  const int id = a.tok[i];
+  if (id < 0 || id >= a.V) return 0.0f;
+  *given = true;
+  const float x = Elem<DT>::value(Elem<DT>::bits(row + (int64_t)id * Elem<DT>::kBytes));
+  if (a.allowed && !((a.allowed[i * a.mask_words + (id >> 5)] >> (id & 31)) & 1u)) return -INFINITY;
+  return x;
+}
+
+// A row whose scaled maximum overflows although its logits are finite (only
+// logits of about the type's largest magnitude): the differences to the
+// maximum are taken before the scaling, and z in the units of raw / T.
+// One wavefront walks the row; rare, so it is plain.
+template <int DT>
+__device__ void extreme_row(const LogprobsArgs& a, const uint8_t* row, int64_t i, float raw, float c, int lane,
+                            float* s_out, float* t_out) {
+  float s = 0.0f, t = 0.0f;
+  for (int j = lane; j < a.V; j += 64) {
+    const float x = Elem<DT>::value(Elem<DT>::bits(row + (int64_t)j * Elem<DT>::kBytes));
+    if (a.allowed && !((a.allowed[i * a.mask_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
+    const float y = (x - raw) * c;
+    const float e = __builtin_amdgcn_exp2f(y);
+    s += e;
+    t = __builtin_fmaf(e, fmaxf(y, -1000.0f), t);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    s += __shfl_xor(s, d, 64);
+    t += __shfl_xor(t, d, 64);
+  }
+  *s_out = s;
+  *t_out = t;
+}
+
+// The row's outputs from its sums, count and list (one wavefront).
+template <int DT>
+__device__ __forceinline__ void finish_row(const LogprobsArgs& a, int64_t i, Sums q, int larger, Key k, int lane) {
+  const uint8_t* const row = a.x + i * a.row_stride * Elem<DT>::kBytes;
+  const float invt = inv_temperature(a.temps, i), c = invt * kLog2e;
+  bool given;
+  const float xt = token_logit<DT>(a, row, i, &given);
+  const bool empty = q.raw == -INFINITY && !(q.s != q.s);     // nothing allowed or finite, and no NaN
+  float m = q.m2 * kLn2;                                       // the maximum of z
+  float s = q.s, t = q.t;
+  // relative to m2, as the sums are; a logit that overflows once scaled to
+  // base 2 is far below the maximum and is taken relative to it as it stands
+  auto logprob = [&](float x, float logs) {
+    if (!(fabsf(x * c) < INFINITY)) return (x - q.raw) * invt - logs;
+    return __builtin_fmaf(__builtin_fmaf(x, c, -q.m2), kLn2, -logs);
+  };
+  float logs, lse, ent;
+  const bool extreme = fabsf(q.raw) < INFINITY && !(fabsf(q.raw * c) < 3.0e38f);
+  if (extreme) {
+    extreme_row<DT>(a, row, i, q.raw, c, lane, &s, &t);
+    m = q.raw * invt;
+  }
+  logs = logf(s);
+  lse = m + logs;
+  ent = logs - t / s * kLn2;
+  if (empty) {
+    lse = -INFINITY;
+    ent = 0.0f;
+  }
+  auto lp_of = [&](float x) {
+    if (empty) return -INFINITY;
+    return extreme ? (x - q.raw) * invt - logs : logprob(x, logs);
+  };
+  if (lane == 0) {
+    if (a.token_logprob) a.token_logprob[i] = given ? lp_of(xt) : 0.0f;
+    if (a.token_rank) a.token_rank[i] = given ? larger + 1 : 0;
+    if (a.lse) a.lse[i] = lse;
+    if (a.entropy) a.entropy[i] = ent;
+  }
+  if (lane < a.topk) {
+    const bool some = k.hi != 0;
+    a.top_ids[i * a.topk + lane] = some ? (int32_t)~k.lo : -1;
+    a.top_logprobs[i * a.topk + lane] = some ? lp_of(key_value(k.hi)) : -INFINITY;
+  }
+}
+
+}  // namespace
+
+template <int DT, bool MASK>
+__global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
+  using E = Elem<DT>;
+  constexpr int VE = E::kPerVec, U = kGroup16 / VE;
+  __shared__ Sums sh_sums[kLpWaves];
+  __shared__ int sh_larger[kLpWaves];
+  __shared__ Key sh_keys[kLpWaves][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t i = blockIdx.x / a.segs;
+  const int seg = (int)(blockIdx.x - i * a.segs);
+  const uint8_t* const row = a.x + i * a.row_stride * E::kBytes;
+  const uint32_t* const bits = MASK ? a.allowed + i * a.mask_words : nullptr;
+  const int V = a.V;
+  const int nv = (V + VE - 1) / VE, full = V / VE;       // vectors, whole vectors
+  const int v0 = seg * a.seg_vecs, v1 = min(nv, v0 + a.seg_vecs);
+  bool given;
+  const float xt_lane = token_logit<DT>(a, row, i, &given);
+  const float xt = given ? xt_lane : INFINITY;           // without a token nothing is larger
+  const float c = inv_temperature(a.temps, i) * kLog2e;
+
+  float m2 = kM2Init, s = 0.0f, t = 0.0f, raw = -INFINITY;
+  int larger = 0;
+  Key key = {0u, 0u}, kth = {0u, 0u};
+  float thr = kLowest;                                   // logits below it cannot enter the list
+  const int kk = a.topk;
+
+  auto load = [&](int v) -> u32x4 {
+    if (v < min(v1, full)) return E::load(row + (int64_t)v * 16);
+    if (v < v1) return load_tail<DT>(row, v * VE, V);
+    return u32x4{E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
+  };
+
+  u32x4 cur[U], next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) cur[u] = load(v0 + kLpThreads * u + tid);
+  for (int vb = v0; vb < v1; vb += kLpThreads * U) {
+    const bool more = vb + kLpThreads * U < v1;
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = load(vb + kLpThreads * (U + u) + tid);
+    }
+    float f[kGroup16];
+#pragma unroll
+    for (int u = 0; u < U; ++u) E::unpack(cur[u], f + VE * u);
+    if (MASK) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j0 = (vb + kLpThreads * u + tid) * VE;
+        const uint32_t w = j0 < V ? bits[j0 >> 5] >> (j0 & 31) : 0u;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) f[VE * u + e] = ((w >> e) & 1u) ? f[VE * u + e] : -INFINITY;
+      }
+    }
+    float g = f[0];
+#pragma unroll
+    for (int e = 1; e < kGroup16; ++e) g = fmaxf(g, f[e]);
+    raw = fmaxf(raw, g);
+    const float top = g * c;
+    if (top > m2) rescale(m2, s, t, top);
+#pragma unroll
+    for (int e = 0; e < kGroup16; ++e) {
+      const float y = __builtin_fmaf(f[e], c, -m2);
+      const float p = __builtin_amdgcn_exp2f(y);
+      s += p;
+      t = __builtin_fmaf(p, fmaxf(y, -1000.0f), t);      // 2^y is 0 there; a NaN stays in s
+      larger += __popcll(__ballot(f[e] > xt));
+    }
+    if (kk > 0 && __ballot(g >= thr) != 0) {
+#pragma unroll
+      for (int e = 0; e < kGroup16; ++e) {
+        const int j = (vb + kLpThreads * (e / VE) + tid) * VE + e % VE;
+        const Key mine = {key_image(f[e]), ~(uint32_t)j};
+        uint64_t todo = __ballot(f[e] >= thr && key_gt(mine, kth));
+        while (todo != 0) {
+          const int src = __ffsll((unsigned long long)todo) - 1;
+          todo &= todo - 1;
+          Key cand;
+          cand.hi = (uint32_t)__builtin_amdgcn_readlane((int)mine.hi, src);
+          cand.lo = (uint32_t)__builtin_amdgcn_readlane((int)mine.lo, src);
+          if (!key_gt(cand, kth)) continue;
+          list_insert(key, cand, lane);
+          kth.hi = (uint32_t)__builtin_amdgcn_readlane((int)key.hi, kk - 1);
+          kth.lo = (uint32_t)__builtin_amdgcn_readlane((int)key.lo, kk - 1);
+          if (kth.hi != 0) thr = key_value(kth.hi);
+        }
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = next[u];
+    }
+  }
+
+  // wavefronts -> workgroup
+  const Sums q = wave_combine(Sums{m2, s, t, raw});
+  if (lane == 0) {
+    sh_sums[wave] = q;
+    sh_larger[wave] = larger;
+  }
+  if (lane >= kk) key = Key{0u, 0u};
+  if (kk > 0) sh_keys[wave][lane] = key;
+  __syncthreads();
+  if (wave != 0) return;
+  Sums total = sh_sums[0];
+  int count = sh_larger[0];
+#pragma unroll
+  for (int w = 1; w < kLpWaves; ++w) {
+    total = combine(total, sh_sums[w]);
+    count += sh_larger[w];
+  }
+  if (kk > 0) {
+#pragma unroll
+    for (int w = 1; w < kLpWaves; ++w) key = list_merge(key, sh_keys[w][lane], lane);
+  }
+  if (a.segs == 1) {
+    finish_row<DT>(a, i, total, count, key, lane);
+    return;
+  }
+  LogprobsPart* const part = a.parts + blockIdx.x;
+  if (lane == 0) *part = LogprobsPart{total.m2, total.s, total.t, total.raw, count, {0, 0, 0}};
+  if (lane < kk) reinterpret_cast<Key*>(a.part_keys)[(int64_t)blockIdx.x * kk + lane] = key;
+}
+
+// Joins a row's segments: lane q of wavefront 0 takes segments q, q + 64, ...
+// in order; wavefront w merges the lists of segments w, w + 8, ...
+template <int DT>
+__global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(LogprobsArgs a) {
+  __shared__ Key sh_keys[kJoinWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t i = blockIdx.x;
+  const int kk = a.topk;
+  Key key = {0u, 0u};
+  if (kk > 0) {
+    const Key* const lists = reinterpret_cast<const Key*>(a.part_keys) + i * a.segs * kk;
+    for (int g = wave; g < a.segs; g += kJoinWaves) {
+      Key o = {0u, 0u};
+      if (lane < kk) o = lists[(int64_t)g * kk + lane];
+      key = g == wave ? o : list_merge(key, o, lane);
+    }
+    sh_keys[wave][lane] = key;
+#pragma unroll
+    for (int half = kJoinWaves / 2; half > 0; half >>= 1) {
+      __syncthreads();
+      if (wave < half) {
+        key = list_merge(key, sh_keys[wave + half][lane], lane);
+        sh_keys[wave][lane] = key;
+      }
+    }
+  }
+  if (wave != 0) return;
+  Sums q = {kM2Init, 0.0f, 0.0f, -INFINITY};
+  int count = 0;
+  for (int g = lane; g < a.segs; g += 64) {
+    const LogprobsPart p = a.parts[i * a.segs + g];
+    q = combine(q, Sums{p.m2, p.s, p.t, p.raw});
+    count += p.larger;
+  }
+  q = wave_combine(q);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) count += __shfl_xor(count, d, 64);
+  finish_row<DT>(a, i, q, count, key, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Backward: dx_j = (1 / T) [ g_lp 1[j = id] + p_j (g_lse - g_lp - g_H (log p_j + H)) ],
+// log p_j = x_j / T - lse; 0 where the token is not allowed or its logit is
+// -inf.  A workgroup owns a run of one row's vectors.
+// ---------------------------------------------------------------------------
+template <int DT, bool MASK>
+__global__ __launch_bounds__(kLpThreads) void logprobs_backward_kernel(LogprobsBackwardArgs a) {
+  using E = Elem<DT>;
+  constexpr int VE = E::kPerVec, U = kGroup16 / VE;
+  const int tid = threadIdx.x;
+  const int64_t i = blockIdx.x / a.segs;
+  const int seg = (int)(blockIdx.x - i * a.segs);
+  const uint8_t* const row = a.x + i * a.row_stride * E::kBytes;
+  uint8_t* const out = a.dx + i * a.dx_stride * E::kBytes;
+  const uint32_t* const bits = MASK ? a.allowed + i * a.mask_words : nullptr;
+  const int V = a.V;
+  const int nv = (V + VE - 1) / VE, full = V / VE;
+  const int v0 = seg * a.seg_vecs, v1 = min(nv, v0 + a.seg_vecs);
+  const float invt = inv_temperature(a.temps, i);
+  // what 1 / T lost in rounding, so that x / T - lse is right to its own size
+  // (log p of a likely token is a small difference of the two)
+  float invt_lo = a.temps && a.temps[i] > 0.0f ? __builtin_fmaf(-a.temps[i], invt, 1.0f) * invt : 0.0f;
+  if (!(fabsf(invt_lo) < INFINITY)) invt_lo = 0.0f;
+  const float lse = a.lse[i];
+  const bool empty = lse == -INFINITY;
+  const int id = a.tok ? a.tok[i] : -1;
+  const bool given = id >= 0 && id < V;
+  const float glp = given && a.dlogprob ? a.dlogprob[i] * invt : 0.0f;
+  const float gent = a.dentropy ? a.dentropy[i] * invt : 0.0f;
+  const float glse = a.dlse ? a.dlse[i] * invt : 0.0f;
+  const float b0 = glse - glp - (a.dentropy ? gent * a.entropy[i] : 0.0f);
+
+  auto load = [&](int v) -> u32x4 {
+    if (v < min(v1, full)) return E::load(row + (int64_t)v * 16);
+    if (v < v1) return load_tail<DT>(row, v * VE, V);
+    return u32x4{E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
+  };
+  u32x4 cur[U], next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) cur[u] = load(v0 + kLpThreads * u + tid);
+  for (int vb = v0; vb < v1; vb += kLpThreads * U) {
+    const bool more = vb + kLpThreads * U < v1;
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = load(vb + kLpThreads * (U + u) + tid);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = vb + kLpThreads * u + tid, j0 = v * VE;
+      if (v < v1) {
+        float f[VE], d[VE];
+        E::unpack(cur[u], f);
+        const uint32_t w = MASK ? bits[j0 >> 5] >> (j0 & 31) : 0xFFFFFFFFu;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          if (MASK && !((w >> e) & 1u)) f[e] = -INFINITY;
+          const float lp = __builtin_fmaf(f[e], invt_lo, __builtin_fmaf(f[e], invt, -lse));
+          const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
+          d[e] = p * __builtin_fmaf(fmaxf(lp, -1000.0f), -gent, b0);
+          if (f[e] == -INFINITY || empty) d[e] = 0.0f;
+        }
+        if (given && id >= j0 && id < j0 + VE && !empty) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e)
+            if (id == j0 + e && f[e] != -INFINITY) d[e] += glp;
+        }
+        const u32x4 o = E::pack(d);
+        if (v < full) {
+          E::store(out + (int64_t)v * 16, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) {
+            if (j0 + e < V) {
+              uint8_t* const q = out + (int64_t)(j0 + e) * E::kBytes;
+              if (DT == kF32)
+                *reinterpret_cast<uint32_t*>(q) = o[e & 3];
+              else
+                *reinterpret_cast<uint16_t*>(q) = (uint16_t)(o[(e >> 1) & 3] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+    }
+    if (more) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = next[u];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launchers.
+// ---------------------------------------------------------------------------
+namespace {
+
+int elem_bytes(int dtype) { return dtype == kF32 ? 4 : 2; }
+
+}  // namespace
+
+// Segments per row: rows alone fill the GPU from about four workgroups per
+// compute unit (256 CUs); below that a row is cut, in pieces of at least one
+// step of a workgroup (16 logits per thread).
+int64_t logprobs_segments(int64_t M, int64_t V) {
+  const int64_t steps = (V + kLpThreads * kGroup16 - 1) / (kLpThreads * kGroup16);
+  const int64_t want = (1024 + std::max<int64_t>(M, 1) - 1) / std::max<int64_t>(M, 1);
+  const int64_t per = std::max<int64_t>(1, (steps + want - 1) / want);   // steps per segment
+  return (steps + per - 1) / per;
+}
+
+int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk) {
+  const int64_t segs = logprobs_segments(M, V);
+  if (segs == 1) return 16;
+  return M * segs * ((int64_t)sizeof(LogprobsPart) + 8 * topk);
+}
+
+hipError_t launch_logprobs(LogprobsArgs a, int dtype, int64_t M, void* workspace, hipStream_t stream) {
+  const int ve = 16 / elem_bytes(dtype);
+  const int64_t nv = ((int64_t)a.V + ve - 1) / ve;
+  const int64_t step = (int64_t)kLpThreads * kGroup16 / ve;            // vectors per step
+  const int64_t steps = (nv + step - 1) / step;
+  a.segs = (int)logprobs_segments(M, a.V);
+  a.seg_vecs = (int)(step * ((steps + a.segs - 1) / a.segs));
+  a.parts = static_cast<LogprobsPart*>(workspace);
+  a.part_keys = a.parts ? reinterpret_cast<uint64_t*>(a.parts + M * a.segs) : nullptr;
+  const bool mask = a.allowed != nullptr;
+  const void* fn = nullptr;
+  switch (dtype) {
+    case kBf16: fn = mask ? (const void*)logprobs_kernel<kBf16, true> : (const void*)logprobs_kernel<kBf16, false>; break;
+    case kF16: fn = mask ? (const void*)logprobs_kernel<kF16, true> : (const void*)logprobs_kernel<kF16, false>; break;
+    default: fn = mask ? (const void*)logprobs_kernel<kF32, true> : (const void*)logprobs_kernel<kF32, false>; break;
+  }
+  hipError_t e = launch_kernel(fn, dim3((unsigned)(M * a.segs)), dim3(kLpThreads), stream, a);
+  if (e != hipSuccess || a.segs == 1) return e;
+  fn = dtype == kBf16 ? (const void*)logprobs_join_kernel<kBf16>
+       : dtype == kF16 ? (const void*)logprobs_join_kernel<kF16>
+                       : (const void*)logprobs_join_kernel<kF32>;
+  return launch_kernel(fn, dim3((unsigned)M), dim3(64 * kJoinWaves), stream, a);
+}
+
+hipError_t launch_logprobs_backward(LogprobsBackwardArgs a, int dtype, int64_t M, hipStream_t stream) {
+  const int ve = 16 / elem_bytes(dtype);
+  const int64_t nv = ((int64_t)a.V + ve - 1) / ve;
+  const int64_t step = (int64_t)kLpThreads * kGroup16 / ve;
+  const int64_t steps = (nv + step - 1) / step;
+  // two steps per workgroup, so that the second one's loads overlap the first
+  // (more only where the grid would pass 2^23 workgroups)
+  int64_t per = steps > 1 ? 2 : 1;
+  while (per < steps && M * ((steps + per - 1) / per) > ((int64_t)1 << 23)) per *= 2;
+  a.seg_vecs = (int)(step * per);
+  a.segs = (int)((steps + per - 1) / per);
+  const bool mask = a.allowed != nullptr;
+  const void* fn = nullptr;
+  switch (dtype) {
+    case kBf16:
+      fn = mask ? (const void*)logprobs_backward_kernel<kBf16, true> : (const void*)logprobs_backward_kernel<kBf16, false>;
+      break;
+    case kF16:
+      fn = mask ? (const void*)logprobs_backward_kernel<kF16, true> : (const void*)logprobs_backward_kernel<kF16, false>;
+      break;
+    default:
+      fn = mask ? (const void*)logprobs_backward_kernel<kF32, true> : (const void*)logprobs_backward_kernel<kF32, false>;
+      break;
+  }
+  return launch_kernel(fn, dim3((unsigned)(M * a.segs)), dim3(kLpThreads), stream, a);
+}
+
+}  // namespace nvfp4

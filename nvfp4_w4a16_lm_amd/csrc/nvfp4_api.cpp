@@ -387,6 +387,141 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
   return finish(e);
 }
 
+// ---------------------------------------------------------------------------
+// Log probabilities
+// ---------------------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+int64_t dtype_bytes(int dtype) { return dtype == NVFP4_F32 ? 4 : 2; }
+
+// Bytes that M rows of V elements, `stride` elements apart, span.
+Range rows_span(const void* p, int64_t M, int64_t V, int64_t stride, int64_t elem) {
+  return span(p, ((M - 1) * stride + V) * elem);
+}
+
+nvfp4_status check_logits(int dtype, int64_t M, int64_t V, int64_t row_stride) {
+  if (dtype != NVFP4_BF16 && dtype != NVFP4_F16 && dtype != NVFP4_F32) return NVFP4_ERR_ARG;
+  if (M < 0 || M > nvfp4::kLogprobsMaxRows || V < 1 || V > kMaxDim || row_stride < V ||
+      row_stride > kMaxElems || M * row_stride > kMaxElems)
+    return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+bool any_overlap(const Range* outs, int n_out, const Range* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+  }
+  return false;
+}
+
+Range optional_span(const void* p, int64_t bytes) { return span(p, p ? bytes : 0); }
+
+}  // namespace
+
+extern "C" {
+
+int64_t nvfp4_logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk) {
+  if (M < 0 || M > nvfp4::kLogprobsMaxRows || V < 1 || V > kMaxDim || topk < 0 || topk > nvfp4::kLogprobsMaxTopk)
+    return 0;
+  return nvfp4::logprobs_workspace_bytes(M, V, topk);
+}
+
+nvfp4_status nvfp4_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride,
+                            const int32_t* token_ids, const float* temperatures, const uint32_t* allowed,
+                            int64_t topk, void* workspace, float* token_logprobs, int32_t* token_ranks, float* lse,
+                            float* entropy, float* top_logprobs, int32_t* top_ids, void* stream) {
+  if (M != 0 && (!logits || !workspace || (topk != 0 && (!top_logprobs || !top_ids)))) return NVFP4_ERR_NULL;
+  const nvfp4_status st = check_logits(dtype, M, V, row_stride);
+  if (st != NVFP4_OK) return st;
+  if (topk < 0 || topk > nvfp4::kLogprobsMaxTopk) return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  const int64_t es = dtype_bytes(dtype), words = (V + 31) / 32;
+  if (!aligned(logits, es) || !aligned(workspace, 16) || !aligned(token_ids, 4) || !aligned(temperatures, 4) ||
+      !aligned(allowed, 4) || !aligned(token_logprobs, 4) || !aligned(token_ranks, 4) || !aligned(lse, 4) ||
+      !aligned(entropy, 4) || (topk != 0 && (!aligned(top_logprobs, 4) || !aligned(top_ids, 4))))
+    return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(workspace, nvfp4::logprobs_workspace_bytes(M, V, topk)),
+                        optional_span(token_logprobs, M * 4),
+                        optional_span(token_ranks, M * 4),
+                        optional_span(lse, M * 4),
+                        optional_span(entropy, M * 4),
+                        optional_span(top_logprobs, M * topk * 4),
+                        optional_span(top_ids, M * topk * 4)};
+  const Range ins[] = {rows_span(logits, M, V, row_stride, es), optional_span(token_ids, M * 4),
+                       optional_span(temperatures, M * 4), optional_span(allowed, M * words * 4)};
+  if (any_overlap(outs, 7, ins, 4)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  nvfp4::LogprobsArgs a = {};
+  a.x = static_cast<const uint8_t*>(logits);
+  a.row_stride = row_stride;
+  a.tok = token_ids;
+  a.temps = temperatures;
+  a.allowed = allowed;
+  a.mask_words = words;
+  a.V = (int32_t)V;
+  a.topk = (int32_t)topk;
+  a.token_logprob = token_logprobs;
+  a.token_rank = token_ranks;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_logprobs = top_logprobs;
+  a.top_ids = top_ids;
+  return finish(nvfp4::launch_logprobs(a, dtype, M, workspace, (hipStream_t)stream));
+}
+
+nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride,
+                                     const int32_t* token_ids, const float* temperatures, const uint32_t* allowed,
+                                     const float* lse, const float* entropy, const float* dlogprob,
+                                     const float* dentropy, const float* dlse, void* dlogits,
+                                     int64_t dlogits_stride, void* stream) {
+  if (M != 0 && (!logits || !lse || !dlogits || (dentropy && !entropy) || (dlogprob && !token_ids)))
+    return NVFP4_ERR_NULL;
+  nvfp4_status st = check_logits(dtype, M, V, row_stride);
+  if (st == NVFP4_OK) st = check_logits(dtype, M, V, dlogits_stride);
+  if (st != NVFP4_OK) return st;
+  if (M == 0) return NVFP4_OK;
+  const int64_t es = dtype_bytes(dtype), words = (V + 31) / 32;
+  if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(token_ids, 4) || !aligned(temperatures, 4) ||
+      !aligned(allowed, 4) || !aligned(lse, 4) || !aligned(entropy, 4) || !aligned(dlogprob, 4) ||
+      !aligned(dentropy, 4) || !aligned(dlse, 4))
+    return NVFP4_ERR_ALIGN;
+  const Range out = rows_span(dlogits, M, V, dlogits_stride, es);
+  const bool in_place = dlogits == logits && dlogits_stride == row_stride;
+  const Range ins[] = {in_place ? span(logits, 0) : rows_span(logits, M, V, row_stride, es),
+                       optional_span(token_ids, M * 4),
+                       optional_span(temperatures, M * 4),
+                       optional_span(allowed, M * words * 4),
+                       span(lse, M * 4),
+                       optional_span(entropy, M * 4),
+                       optional_span(dlogprob, M * 4),
+                       optional_span(dentropy, M * 4),
+                       optional_span(dlse, M * 4)};
+  if (any_overlap(&out, 1, ins, 9)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  nvfp4::LogprobsBackwardArgs a = {};
+  a.x = static_cast<const uint8_t*>(logits);
+  a.row_stride = row_stride;
+  a.tok = token_ids;
+  a.temps = temperatures;
+  a.allowed = allowed;
+  a.mask_words = words;
+  a.V = (int32_t)V;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.dlogprob = dlogprob;
+  a.dentropy = dentropy;
+  a.dlse = dlse;
+  a.dx = static_cast<uint8_t*>(dlogits);
+  a.dx_stride = dlogits_stride;
+  return finish(nvfp4::launch_logprobs_backward(a, dtype, M, (hipStream_t)stream));
+}
+
 const char* nvfp4_status_string(int status) {
   switch (status) {
     case NVFP4_OK: return "ok";

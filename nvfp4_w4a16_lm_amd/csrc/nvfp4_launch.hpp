@@ -169,4 +169,52 @@ hipError_t launch_moe_silu_mul(const void* h, int64_t P, int64_t I, void* a, hip
 hipError_t launch_moe_combine(const void* o, const float* w, int64_t T, int64_t topk, int64_t H, void* out,
                               hipStream_t stream);
 
+// Log probabilities of logits (logprobs.hip).  dtype: 0 bf16, 1 f16, 2 f32;
+// strides in elements; segs, seg_vecs, parts and part_keys are the launcher's.
+struct LogprobsPart {                       // one segment of a row
+  float m2, s, t, raw;
+  int32_t larger;
+  int32_t pad[3];
+};
+struct LogprobsArgs {
+  const uint8_t* x;
+  int64_t row_stride;
+  const int32_t* tok;
+  const float* temps;
+  const uint32_t* allowed;
+  int64_t mask_words;
+  int32_t V, topk;
+  int32_t segs, seg_vecs;
+  LogprobsPart* parts;
+  uint64_t* part_keys;
+  float* token_logprob;
+  int32_t* token_rank;
+  float* lse;
+  float* entropy;
+  float* top_logprobs;
+  int32_t* top_ids;
+};
+struct LogprobsBackwardArgs {
+  const uint8_t* x;
+  int64_t row_stride;
+  const int32_t* tok;
+  const float* temps;
+  const uint32_t* allowed;
+  int64_t mask_words;
+  int32_t V;
+  int32_t segs, seg_vecs;
+  const float* lse;
+  const float* entropy;
+  const float* dlogprob;
+  const float* dentropy;
+  const float* dlse;
+  uint8_t* dx;
+  int64_t dx_stride;
+};
+constexpr int64_t kLogprobsMaxRows = (int64_t)1 << 23;
+constexpr int64_t kLogprobsMaxTopk = 64;
+int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk);
+hipError_t launch_logprobs(LogprobsArgs a, int dtype, int64_t M, void* workspace, hipStream_t stream);
+hipError_t launch_logprobs_backward(LogprobsBackwardArgs a, int dtype, int64_t M, hipStream_t stream);
+
 }  // namespace nvfp4

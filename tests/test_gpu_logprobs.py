@@ -1,0 +1,306 @@
+"""GPU parity of nvfp4_logprobs and nvfp4_logprobs_backward with the float64
+oracle: types, odd sizes, row strides and alignments, masks, rows that have
+nothing, ties, given tokens outside the row, and the gradient against the
+formula and against differences.  Whole numbers must be equal; the others lie
+within bounds derived from float32's and the output type's rounding."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.logprobs_oracle as L
+from nvfp4_w4a16_lm_amd import binding as B
+
+from gpu_util import DEV
+from test_gpu_graphs import capture
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+U = 2.0 ** -24
+
+
+def make_logits(m, v, dtype, seed, pad=0, offset=0):
+    """[m, v] view with row stride v + pad, starting `offset` elements into its storage."""
+    g = torch.Generator().manual_seed(seed)
+    flat = (3.0 * torch.randn(offset + m * (v + pad), generator=g)).to(dtype)
+    x = flat.to(DEV)[offset:].view(m, v + pad)[:, :v]
+    return x
+
+
+def host(t):
+    return t.detach().to("cpu").to(torch.float64).numpy()
+
+
+def words_of(bits: np.ndarray) -> np.ndarray:
+    m, v = bits.shape
+    pad = np.zeros((m, (v + 31) // 32 * 32), np.uint64)
+    pad[:, :v] = bits
+    w = (pad.reshape(m, -1, 32) << np.arange(32, dtype=np.uint64)).sum(2)
+    return w.astype(np.uint32)
+
+
+def dev_words(bits):
+    return torch.from_numpy(words_of(bits).view(np.int32)).to(DEV)
+
+
+def check_forward(x, ids, topk, temps=None, bits=None, out=None):
+    tid = None if ids is None else torch.tensor(ids, dtype=torch.int32, device=DEV)
+    td = None if temps is None else torch.tensor(temps, dtype=F32, device=DEV)
+    r = B.nvfp4_logprobs(x, tid, topk=topk, temperatures=td, allowed=None if bits is None else dev_words(bits),
+                         out=out)
+    torch.cuda.synchronize()
+    t64 = None if temps is None else np.float32(temps).astype(np.float64)
+    lp, rank, lse, ent, tlp, top = L.forward(host(x), ids, topk, t64, bits)
+    b_s, b_lse, b_h = L.forward_bounds(host(x), t64, bits)
+    got = [host(t) for t in r[:6]]
+    assert np.array_equal(got[5].astype(np.int64), top), "alternatives"
+    if ids is not None:
+        assert np.array_equal(got[1].astype(np.int64), rank), "ranks"
+
+    def close(g, want, bound, what):
+        same = (g == want) | (np.isnan(g) & np.isnan(want))
+        with np.errstate(invalid="ignore"):
+            ok = same | (np.abs(g - want) <= bound)
+        assert np.all(ok), f"{what}: {g[~ok][:4]} != {want[~ok][:4]} (bound {np.broadcast_to(bound, g.shape)[~ok][:4]})"
+    raw, z = L.scaled(host(x), t64, bits)
+    with np.errstate(invalid="ignore"):
+        top_z = np.max(np.where(np.isnan(z), -np.inf, z), axis=1)
+        top_z = np.where(np.isfinite(top_z), top_z, 0.0)
+    close(got[2], lse, b_lse, "lse")
+    close(got[3], ent, b_h, "entropy")
+    if ids is not None:
+        zi = np.array([z[i, j] if 0 <= j < z.shape[1] else 0.0 for i, j in enumerate(ids)])
+        close(got[0], lp, b_s + 6 * U * np.where(np.isfinite(zi), np.abs(zi - top_z), 0.0)
+              + 4 * U * np.where(np.isfinite(lp), np.abs(lp), 0.0), "logprobs")
+    zt = np.where(top >= 0, np.take_along_axis(z, np.maximum(top, 0), 1), 0.0)
+    zt = np.where(np.isfinite(zt) & (top >= 0), np.abs(zt - top_z[:, None]), 0.0)
+    close(got[4], tlp, b_s[:, None] + 6 * U * zt + 4 * U * np.where(np.isfinite(tlp), np.abs(tlp), 0.0),
+          "top logprobs")
+    return r
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("m,v,topk,pad,offset", [
+    (1, 1, 1, 0, 0), (3, 2, 5, 0, 1), (2, 7, 7, 1, 3), (5, 31, 3, 0, 0), (4, 33, 64, 2, 1), (3, 255, 20, 0, 0),
+    (2, 4095, 1, 0, 0), (2, 4096, 8, 8, 0), (2, 4097, 64, 0, 5), (1, 32003, 20, 0, 0), (7, 32003, 0, 5, 1),
+    (1030, 1003, 2, 0, 0), (1, 128256, 5, 0, 0), (33, 20000, 33, 0, 0)])
+def test_forward_sizes(dtype, m, v, topk, pad, offset):
+    x = make_logits(m, v, dtype, 100 * m + v, pad, offset)
+    rng = np.random.default_rng(v)
+    ids = rng.integers(0, v, m).astype(np.int32)
+    temps = rng.uniform(0.5, 1.5, m).astype(np.float32) if m % 2 else None
+    check_forward(x, ids, topk, temps)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("m,v,topk", [(6, 37, 40), (6, 1000, 20), (6, 9001, 64), (6, 70001, 5)])
+def test_forward_masks_hide_whatever_they_cover(dtype, m, v, topk):
+    x = make_logits(m, v, dtype, v)
+    rng = np.random.default_rng(v + 1)
+    bits = rng.random((m, v)) < 0.3
+    bits[0] = False                                      # nothing allowed
+    bits[1] = False
+    bits[1, v - 1] = True                                # one token
+    bits[2] = True
+    ids = rng.integers(0, v, m).astype(np.int32)
+    bits[3, ids[3]] = False                              # the given token is not allowed
+    bits[4, ids[4]] = True
+    hidden = torch.from_numpy(~bits).to(DEV)
+    for bad in (float("nan"), float("inf"), float("-inf"), torch.finfo(dtype).min):
+        check_forward(torch.where(hidden, torch.tensor(bad, dtype=dtype, device=DEV), x), ids, topk,
+                      np.full(m, 0.7, np.float32), bits)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("v", [5, 600, 5001, 40000])
+def test_forward_special_rows(dtype, v):
+    m = 11
+    x = make_logits(m, v, dtype, v + 2).contiguous()
+    lowest = torch.finfo(dtype).min
+    x[0] = float("-inf")
+    x[1] = float("-inf")
+    x[1, v // 2] = 1.5                                   # one finite logit: entropy 0
+    x[2] = 0.0                                           # all equal
+    x[3] = 0.0
+    x[3, ::2] = -0.0                                     # equal too
+    x[4] = lowest                                        # all of the type's lowest value: uniform
+    x[5, 1:] = lowest
+    x[6, v - 1] = float("nan")
+    x[7, 0] = float("inf")
+    x[8] = torch.finfo(dtype).max                        # overflows once scaled to base 2 (bf16, f32)
+    x[9] = torch.linspace(-5, 5, v).to(dtype)            # rising: every group brings new alternatives
+    ids = np.full(m, v // 2, np.int32)
+    ids[10] = -1
+    for topk in (0, 1, 20, 64):
+        r = check_forward(x, ids, topk)
+    assert int(r.token_ranks[10]) == 0 and float(r.token_logprobs[10]) == 0.0
+    for bad in (v, -100, 2 ** 31 - 1):
+        r = check_forward(x, np.full(m, bad, np.int32), 3)
+        assert not r.token_ranks.any() and not r.token_logprobs.any()
+    check_forward(x, None, 2)
+
+
+def test_forward_temperatures_and_optional_outputs():
+    x = make_logits(5, 3001, BF16, 9)
+    check_forward(x, np.arange(5, dtype=np.int32), 4, np.float32([0.0, -1.0, 0.05, 4.0, 1.0]))
+    nan_t = torch.tensor([float("nan")] * 5, device=DEV)
+    one = B.nvfp4_logprobs(x, None, topk=3)
+    got = B.nvfp4_logprobs(x, None, topk=3, temperatures=nan_t)
+    for a, b in zip(one[2:6], got[2:6]):
+        assert torch.equal(a, b)
+
+
+def test_forward_empty_batch():
+    x = torch.empty((0, 100), dtype=BF16, device=DEV)
+    r = B.nvfp4_logprobs(x, torch.empty((0,), dtype=torch.int32, device=DEV), topk=3)
+    assert r.lse.shape == (0,) and r.top_ids.shape == (0, 3)
+
+
+def test_forward_same_bits_every_time_and_on_a_side_stream():
+    x = make_logits(3, 128256, BF16, 11)
+    ids = torch.tensor([5, 6, 7], dtype=torch.int32, device=DEV)
+    first = B.nvfp4_logprobs(x, ids, topk=20)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = B.logprobs_buffers(3, 128256, 20, DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            B.nvfp4_logprobs(x, ids, topk=20, out=out)
+        side.synchronize()
+        for a, b in zip(first[:6], out[:6]):
+            assert torch.equal(a, b)
+
+
+GRAD_TYPES = {BF16: 2.0 ** -8, F16: 2.0 ** -11, F32: 2.0 ** -24}
+
+
+def run_backward(x, ids, dlp, dent, dlse, temps, bits, out=None):
+    dev = lambda a, t=F32: None if a is None else torch.tensor(a, dtype=t, device=DEV)
+    words = None if bits is None else dev_words(bits)
+    tid, td = dev(ids, torch.int32), dev(temps)
+    f = B.nvfp4_logprobs(x, tid, temperatures=td, allowed=words)
+    g = B.nvfp4_logprobs_backward(x, tid, f.lse, f.entropy, dev(dlp), dev(dent), dev(dlse), td, words, out=out)
+    torch.cuda.synchronize()
+    return g, host(f.lse), host(f.entropy)
+
+
+def check_backward(x, ids, dlp=None, dent=None, dlse=None, temps=None, bits=None, out=None):
+    want_x = host(x)
+    g, lse, ent = run_backward(x, ids, dlp, dent, dlse, temps, bits, out)
+    t64 = None if temps is None else np.float32(temps).astype(np.float64)
+    f64 = lambda a: None if a is None else np.float32(a).astype(np.float64)
+    want, mag = L.backward(want_x, ids, lse, ent, f64(dlp), f64(dent), f64(dlse), t64, bits)
+    _, z = L.scaled(want_x, t64, bits)
+    z = np.where(np.isfinite(z), np.abs(z), 0.0)
+    lse_mag = np.where(np.isfinite(lse), np.abs(lse), 0.0)[:, None]
+    # log p within 3 u of |z| and |lse|, p relative to it, a few more roundings of each term;
+    # below float32's normal range a result may become 0
+    bound = mag * (4 * U * (z + lse_mag) + 16 * U) + GRAD_TYPES[x.dtype] * np.abs(want) * (1 + 2.0 ** -7)
+    tiny = {BF16: 2.0 ** -126, F16: 2.0 ** -25, F32: 2.0 ** -126}[x.dtype]
+    got = host(g)
+    ok = np.abs(got - want) <= bound + tiny * 1.01
+    assert np.all(ok), (got[~ok][:4], want[~ok][:4], bound[~ok][:4])
+    return g
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("m,v,pad,offset", [(1, 1, 0, 0), (3, 5, 2, 1), (2, 31, 0, 0), (4, 4096, 0, 0),
+                                            (3, 4099, 1, 3), (5, 9001, 0, 1), (2, 32003, 5, 0), (70, 513, 0, 0)])
+def test_backward_sizes(dtype, m, v, pad, offset):
+    x = make_logits(m, v, dtype, m + v, pad, offset)
+    rng = np.random.default_rng(m + v)
+    ids = rng.integers(0, v, m).astype(np.int32)
+    ids[m // 2] = -1 if m > 1 else ids[0]
+    dlp, dent, dlse = (rng.standard_normal(m) for _ in range(3))
+    temps = rng.uniform(0.5, 1.5, m).astype(np.float32)
+    check_backward(x, ids, dlp, None, None)
+    check_backward(x, ids, dlp, dent, dlse, temps)
+    check_backward(x, None, None, dent, None, temps)
+    bits = rng.random((m, v)) < 0.4
+    bits[0] = False
+    bits[m - 1, ids[m - 1] if ids[m - 1] >= 0 else 0] = True
+    check_backward(x, ids, dlp, dent, dlse, temps, bits)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_backward_strided_output_and_in_place(dtype):
+    m, v = 5, 3003
+    x = make_logits(m, v, dtype, 77, pad=3, offset=1)
+    rng = np.random.default_rng(4)
+    ids, dlp, dent = rng.integers(0, v, m).astype(np.int32), rng.standard_normal(m), rng.standard_normal(m)
+    plain = check_backward(x, ids, dlp, dent).clone()
+    buf = torch.full((m, v + 6), 7.0, dtype=dtype, device=DEV)
+    check_backward(x, ids, dlp, dent, out=buf[:, 2:v + 2])
+    assert torch.equal(buf[:, 2:v + 2], plain)
+    assert torch.all(buf[:, :2] == 7.0) and torch.all(buf[:, v + 2:] == 7.0), "wrote outside its rows"
+    check_backward(x, ids, dlp, dent, out=x)             # the gradient replaces the logits
+    assert torch.equal(x, plain)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_backward_special_rows(dtype):
+    m, v = 6, 700
+    x = make_logits(m, v, dtype, 5).contiguous()
+    x[0] = float("-inf")
+    x[1] = float("-inf")
+    x[1, 3] = 2.0
+    x[2, ::3] = float("-inf")
+    x[3] = 1.0
+    ids = np.int32([3, 3, 3, 4, v, -5])
+    check_backward(x, ids, np.ones(m), np.full(m, 0.3), np.full(m, -0.2))
+    x[4, 7] = float("nan")                               # reaches every gradient of its row, no other row
+    g, _, _ = run_backward(x, ids, np.ones(m), np.full(m, 0.3), None, None, None)
+    assert torch.isnan(g[4]).all() and not torch.isnan(g[[0, 1, 2, 3, 5]]).any()
+
+
+def test_backward_against_differences():
+    """Central differences of the float64 forward, h = 2^-10: its error is h^2 / 6 times the
+    third derivative of each term (log softmax and entropy: below 4 (1 + H) in size) plus the
+    rounding of the difference."""
+    m, v, h = 3, 40, 2.0 ** -10
+    x = make_logits(m, v, F32, 21)
+    rng = np.random.default_rng(2)
+    ids = rng.integers(0, v, m).astype(np.int32)
+    dlp, dent, dlse = (rng.standard_normal(m).astype(np.float32).astype(np.float64) for _ in range(3))
+    temps = np.float64([0.75, 1.0, 1.5])
+    g, _, _ = run_backward(x, ids, dlp, dent, dlse, temps, None)
+
+    def loss(xs):
+        lp, _, lse, ent, _, _ = L.forward(xs, ids, 0, temps)
+        return dlp * lp + dent * ent + dlse * lse
+    x64 = host(x)
+    num = np.empty((m, v))
+    for j in range(v):
+        up, dn = x64.copy(), x64.copy()
+        up[:, j] += h
+        dn[:, j] -= h
+        num[:, j] = (loss(up) - loss(dn)) / (2 * h)
+    weight = (np.abs(dlp) + np.abs(dent) * (1 + np.log(v)) + np.abs(dlse))[:, None] / temps[:, None] ** 3
+    assert np.all(np.abs(host(g) - num) <= weight * (4 * h * h / 6 + 2.0 ** -20))
+
+
+def test_logprobs_graph_replays():
+    m, v, topk = 4, 20011, 8
+    x = make_logits(m, v, BF16, 1).contiguous()
+    ids = torch.zeros((m,), dtype=torch.int32, device=DEV)
+    out = B.logprobs_buffers(m, v, topk, DEV)
+    dlp = torch.ones((m,), device=DEV)
+    dx = torch.empty((m, v), dtype=BF16, device=DEV)
+
+    def step():
+        B.nvfp4_logprobs(x, ids, topk=topk, out=out)
+        B.nvfp4_logprobs_backward(x, ids, out.lse, out.entropy, dlp, dentropy=dlp, out=dx)
+    graph = capture(step)
+    for seed in (2, 3, 4):
+        x.copy_(make_logits(m, v, BF16, seed))
+        ids.fill_(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out[:6]] + [dx.clone()]
+        eager = B.nvfp4_logprobs(x, ids, topk=topk)
+        edx = B.nvfp4_logprobs_backward(x, ids, eager.lse, eager.entropy, dlp, dentropy=dlp)
+        torch.cuda.synchronize()
+        for a, b in zip(got, [*eager[:6], edx]):
+            assert torch.equal(a, b), f"replay {seed}"
