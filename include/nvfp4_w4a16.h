@@ -382,6 +382,34 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
                                      void* out, uint32_t* invalid_pairs, void* stream);
 
 /*
+ * int4 weights with group scales.
+ * (vLLM API docs, compressed_tensors.schemes, class CompressedTensorsWNA16,
+ * 4 bits without activation reordering.)
+ *
+ * nvfp4_int4_gemm -- logits from bf16 activations and an int4 weight, for few
+ * activation rows:
+ *   y[m, n] = bf16_rne( sum_j scale[n, j] * sum_{k in group j} x[m, k] * (code[n, k] - zero[n, j]) + bias[n] )
+ * The sums are float32 over exact products (a group's sum holds
+ * sum x * (128 + code), from which (128 + zero) * sum x is subtracted in
+ * float32); summation order is unspecified but deterministic.
+ *
+ *   x            in  bf16 [M, K], 16-byte aligned; M >= 0 (M == 0 enqueues nothing, x and y may
+ *                    then be NULL).  Beyond 64 rows the weight is read once per 64 rows.
+ *   packed       in  int32 [N, K / 8], 16-byte aligned: code k of a row is bits 4 (k % 8) .. + 3 of word
+ *                    k / 8, in 0 .. 15
+ *   scales       in  scale_dtype (NVFP4_BF16 or NVFP4_F16) [N, K / group]
+ *   zero_points  in  int32 [ceil(N / 8), K / group] or NULL (zero = 8): row n's is bits
+ *                    4 (n % 8) .. + 3 of word [n / 8, j]
+ *   group        in  32, 64, a multiple of 128, or K (one scale per row); K % group == 0 and
+ *                    K % 32 == 0
+ *   bias         in  bf16 [N] or NULL
+ *   y            out bf16 [M, N], 16-byte aligned
+ */
+nvfp4_status nvfp4_int4_gemm(const void* x, int64_t M, int64_t K, const int32_t* packed, const void* scales,
+                             int scale_dtype, const int32_t* zero_points, int64_t group, int64_t N,
+                             const void* bias, void* y, void* stream);
+
+/*
  * Log probabilities of given tokens, from the logits a GEMM above wrote (or
  * any other logits).
  *

@@ -44,7 +44,7 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_refresh_inplace", "nvfp4_w4a16_gemm",
             "nvfp4_w4a4_gemm_noalloc",
             "nvfp4_moe_gemm_workspace_bytes", "nvfp4_moe_w4a16_gemm", "nvfp4_moe_silu_and_mul",
             "nvfp4_moe_combine", "nvfp4_moe_workspace_bytes", "nvfp4_moe_w4a16_forward",
-            "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "nvfp4_logprobs_backward",
+            "nvfp4_int4_gemm", "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "nvfp4_logprobs_backward",
             "nvfp4_status_string", "nvfp4_last_hip_error", "nvfp4_abi_version")
 
 
@@ -113,6 +113,8 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_moe_w4a16_forward.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp,
                                             vp, vp]
     lib.nvfp4_moe_w4a16_forward.restype = ctypes.c_int
+    lib.nvfp4_int4_gemm.argtypes = [vp, i64, i64, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp]
+    lib.nvfp4_int4_gemm.restype = ctypes.c_int
     lib.nvfp4_logprobs_workspace_bytes.argtypes = [i64, i64, i64]
     lib.nvfp4_logprobs_workspace_bytes.restype = i64
     lib.nvfp4_logprobs.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -562,6 +564,43 @@ def nvfp4_moe_w4a16_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weight
            lib.nvfp4_moe_w4a16_forward(_ptr(x), t, hdim, _ptr(ids), _ptr(w), topk, _ptr(w13[0]), _ptr(w13[1]),
                                        _ptr(w13[2]), _ptr(w2[0]), _ptr(w2[1]), _ptr(w2[2]), e, i,
                                        _ptr(workspace), _ptr(out), _ptr(invalid_pairs), _stream_of(x, stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# int4 weights with group scales
+# ---------------------------------------------------------------------------
+
+def nvfp4_int4_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                    zero_points: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bf16 x [M, K] . ((codes - zeros) * scales)^T (+ bias) -> bf16 [M, N].  ``packed``
+    int32 [N, K / 8] (eight codes per word along K), ``scales`` bfloat16 or
+    float16 [N, K / group], ``zero_points`` int32 [ceil(N / 8), K / group] (eight
+    rows per word) or None for 8."""
+    x = _as_bf16_2d(x, "x")
+    m, k = x.shape
+    dev = x.device
+    if packed.dim() != 2 or packed.shape[1] * 8 != k:
+        raise ValueError(f"packed shape {tuple(packed.shape)} does not match K={k}")
+    n = packed.shape[0]
+    _check_out(packed, (n, k // 8), (torch.int32,), dev, "packed")
+    if scales.dim() != 2 or scales.shape[1] < 1 or k % scales.shape[1] != 0:
+        raise ValueError(f"scales shape {tuple(scales.shape)} does not divide K={k}")
+    groups = scales.shape[1]
+    _check_out(scales, (n, groups), (torch.bfloat16, torch.float16), dev, "scales")
+    if zero_points is not None:
+        _check_out(zero_points, ((n + 7) // 8, groups), (torch.int32,), dev, "zero_points")
+    if bias is not None:
+        _check_out(bias, (n,), (torch.bfloat16,), dev, "bias")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out(out, (m, n), (torch.bfloat16,), dev, "out")
+    lib = load_library()
+    _check("nvfp4_int4_gemm",
+           lib.nvfp4_int4_gemm(_ptr(x), m, k, _ptr(packed), _ptr(scales), LOGIT_DTYPES[scales.dtype],
+                               _ptr(zero_points), k // groups, n, _ptr(bias), _ptr(out), _stream_of(x, stream)))
     return out
 
 

@@ -522,6 +522,48 @@ nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, i
   return finish(nvfp4::launch_logprobs_backward(a, dtype, M, (hipStream_t)stream));
 }
 
+// ---------------------------------------------------------------------------
+// int4 weights with group scales
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxInt4M = (int64_t)65535 * 64;       // grid.y limit, 64 rows per workgroup
+
+nvfp4_status nvfp4_int4_gemm(const void* x, int64_t M, int64_t K, const int32_t* packed, const void* scales,
+                             int scale_dtype, const int32_t* zero_points, int64_t group, int64_t N,
+                             const void* bias, void* y, void* stream) {
+  if (!packed || !scales || (M != 0 && (!x || !y))) return NVFP4_ERR_NULL;
+  if (scale_dtype != NVFP4_BF16 && scale_dtype != NVFP4_F16) return NVFP4_ERR_ARG;
+  if (N < 1 || N > kMaxDim || K < 32 || K % 32 != 0 || K > kMaxDim || N * K > kMaxElems || M < 0 ||
+      M > kMaxInt4M || M * K > kMaxElems || M * N > kMaxElems)
+    return NVFP4_ERR_SHAPE;
+  if (group < 1 || K % group != 0 || !(group == 32 || group == 64 || group % 128 == 0 || group == K))
+    return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 2) || !aligned(zero_points, 4) ||
+      !aligned(bias, 2) || !aligned(y, 16))
+    return NVFP4_ERR_ALIGN;
+  const int64_t groups = K / group;
+  const Range out = span(y, M * N * 2);
+  const Range ins[] = {span(x, M * K * 2), span(packed, N * K / 2), span(scales, N * groups * 2),
+                       optional_span(zero_points, (N + 7) / 8 * groups * 4), optional_span(bias, N * 2)};
+  if (any_overlap(&out, 1, ins, 5)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  nvfp4::Int4Args a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.packed = reinterpret_cast<const uint8_t*>(packed);
+  a.scales = static_cast<const uint16_t*>(scales);
+  a.zeros = reinterpret_cast<const uint32_t*>(zero_points);
+  a.bias = static_cast<const uint16_t*>(bias);
+  a.y = static_cast<uint16_t*>(y);
+  a.M = (int32_t)M;
+  a.K = (int32_t)K;
+  a.N = (int32_t)N;
+  a.group = (int32_t)group;
+  a.groups = (int32_t)groups;
+  a.scale_f16 = scale_dtype == NVFP4_F16;
+  return finish(nvfp4::launch_int4_gemm(a, (hipStream_t)stream));
+}
+
 const char* nvfp4_status_string(int status) {
   switch (status) {
     case NVFP4_OK: return "ok";

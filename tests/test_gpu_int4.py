@@ -1,0 +1,112 @@
+"""GPU parity of nvfp4_int4_gemm with the float64 oracle: group sizes, zero
+points, both scale types, odd row and activation counts, K that ends inside a
+chunk, bias, long K, and graph replays."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.int4_oracle as Q
+from nvfp4_w4a16_lm_amd import binding as B
+
+from gpu_util import DEV
+from test_gpu_graphs import capture
+
+pytestmark = pytest.mark.gpu
+
+
+def make(m, n, k, group, zeros, seed, scale_dtype=torch.bfloat16, bias=False):
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 16, (n, k))
+    packed = Q.pack(codes, 1)
+    g = k // group
+    scales = torch.from_numpy(rng.uniform(0.001, 0.01, (n, g)) * rng.choice([-1, 1], (n, g))).to(scale_dtype)
+    zp = Q.pack(rng.integers(0, 16, ((n + 7) // 8 * 8, g)), 0) if zeros else None
+    x = torch.from_numpy(rng.standard_normal((m, k))).to(torch.bfloat16)
+    b = torch.from_numpy(0.5 * rng.standard_normal(n)).to(torch.bfloat16) if bias else None
+    return x, packed, scales, zp, b
+
+
+def run(x, packed, scales, zp, b, out=None):
+    dev = lambda a: None if a is None else (a if torch.is_tensor(a) else torch.from_numpy(a)).to(DEV)
+    y = B.nvfp4_int4_gemm(dev(x), dev(packed), dev(scales), dev(zp), dev(b), out=out)
+    torch.cuda.synchronize()
+    return y
+
+
+def check(m, n, k, group, zeros, seed, scale_dtype=torch.bfloat16, bias=False):
+    x, packed, scales, zp, b = make(m, n, k, group, zeros, seed, scale_dtype, bias)
+    y = run(x, packed, scales, zp, b)
+    f64 = lambda t: None if t is None else t.to(torch.float64).numpy()
+    want, bound = Q.gemm(f64(x), packed, f64(scales), zp, f64(b))
+    err = np.abs(y.cpu().to(torch.float64).numpy() - want)
+    assert np.all(err <= bound), (np.argwhere(err > bound)[:4], err.max(), bound.min())
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [
+    (1, 1, 32, 32), (1, 7, 64, 64), (2, 33, 96, 32), (1, 100, 128, 128), (3, 65, 160, 32), (5, 31, 192, 64),
+    (1, 515, 2080, 32), (16, 129, 640, 128), (17, 40, 512, 64), (33, 300, 1056, 32), (64, 100, 768, 256),
+    (65, 50, 256, 128), (130, 17, 384, 64), (4, 96, 1024, 1024), (9, 70, 2080, 2080), (16, 1000, 4096, 128),
+    (1, 32, 8192, 128), (48, 333, 1344, 64)])
+def test_sizes(m, n, k, group, zeros):
+    check(m, n, k, group, zeros, seed=m * 1000 + n + k, bias=(n % 2 == 1))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 512])
+def test_f16_scales(group):
+    check(7, 77, 1024, group, True, seed=group, scale_dtype=torch.float16, bias=True)
+
+
+def test_every_code_and_zero_point_exactly():
+    """x = one-hot rows: the output is one dequantized weight, exact before its bf16 rounding."""
+    k, n, group = 128, 16, 32
+    codes = (np.arange(n)[:, None] + np.arange(k)[None, :]) % 16
+    zp = (3 * np.arange(n)[:, None] + np.arange(k // group)[None, :]) % 16
+    scales = torch.full((n, k // group), 0.5, dtype=torch.bfloat16)
+    for k0 in range(0, k, 64):
+        x = torch.zeros((64, k), dtype=torch.bfloat16)
+        x[torch.arange(64), k0 + torch.arange(64)] = 1.0
+        y = run(x, Q.pack(codes, 1), scales, Q.pack(zp, 0), None).cpu().float().numpy()
+        want = 0.5 * (codes - np.repeat(zp, group, 1))[:, k0:k0 + 64].T
+        assert np.array_equal(y, want)
+
+
+def test_many_rows_and_columns():
+    check(16, 20011, 512, 128, False, seed=3)
+    check(2, 70000, 256, 64, True, seed=4)
+
+
+def test_infinite_activation_reaches_its_row_only():
+    x, packed, scales, zp, _ = make(5, 64, 256, 64, True, 8)
+    x[2, 17] = float("inf")
+    y = run(x, packed, scales, zp, None).float().cpu()
+    assert not torch.isfinite(y[2]).any() and torch.isfinite(y[[0, 1, 3, 4]]).all()
+
+
+def test_output_buffer_is_written_exactly():
+    m, n, k = 3, 45, 256
+    x, packed, scales, zp, _ = make(m, n, k, 64, False, 9)
+    buf = torch.full((m * n + 64,), 3.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[:m * n].view(m, n)
+    run(x, packed, scales, zp, None, out=out)
+    assert torch.equal(out, run(x, packed, scales, zp, None)) and torch.all(buf[m * n:] == 3.0)
+
+
+def test_empty_batch():
+    x, packed, scales, zp, _ = make(1, 16, 64, 32, False, 1)
+    assert run(x[:0], packed, scales, zp, None).shape == (0, 16)
+
+
+def test_graph_replays():
+    m, n, k = 4, 1003, 1024
+    x, packed, scales, zp, b = (None if t is None else (t if torch.is_tensor(t) else torch.from_numpy(t)).to(DEV)
+                                for t in make(m, n, k, 128, True, 5, bias=True))
+    y = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
+    graph = capture(lambda: B.nvfp4_int4_gemm(x, packed, scales, zp, b, out=y))
+    for seed in (1, 2, 3):
+        x.copy_(torch.randn((m, k), generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, B.nvfp4_int4_gemm(x, packed, scales, zp, b))
