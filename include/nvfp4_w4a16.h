@@ -382,6 +382,51 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
                                      void* out, uint32_t* invalid_pairs, void* stream);
 
 /*
+ * The whole W4A16 expert layer for a few tokens, from the router's logits.
+ *
+ * nvfp4_moe_decode_workspace_bytes -- workspace of nvfp4_moe_w4a16_decode
+ * (host helper; 0 for sizes the call rejects).
+ *
+ * nvfp4_moe_w4a16_decode -- routing, both expert products, SiLU-and-mul and the
+ * weighted sum in two kernels, for 0 <= T <= 16 tokens (T == 0 enqueues nothing):
+ *   score[t, e] = softmax over e or sigmoid of router_logits[t, e]
+ *   topk_ids[t] = the topk experts of largest logit -- of largest score + correction_bias
+ *                 where a bias is given -- equal ones by the lower index
+ *   topk_weights[t, j] = score[t, e_j] (/ their sum over j, with renormalize) * weight_scale
+ *   a[t, j] = silu(g) * u,  g = w1_e x[t],  u = w3_e x[t]        (w13 rows 0..I, I..2I)
+ *   out[t] = bf16_rne( sum_j topk_weights[t, j] * w2_e a[t, j] )
+ * float32 sums of exact products; a is kept to 16 bits (a bf16 pair), only out
+ * is rounded to bf16.  A chosen expert's weights are read once, the others' not
+ * at all.  An expert whose logit is -inf or NaN is never chosen; a slot left
+ * without an expert has id -1, weight 0 and adds nothing.
+ *
+ *   x               in  bf16 [T, H], 16-byte aligned
+ *   router_logits   in  router_dtype (NVFP4_F32 or NVFP4_BF16) [T, E], 1 <= E <= 1024
+ *   topk            in  1 .. min(E, 32)
+ *   scoring         in  an nvfp4_moe_scoring
+ *   renormalize     in  0 or 1
+ *   correction_bias in  float [E] or NULL (it moves the choice, not the weights)
+ *   weight_scale    in  factor of every weight (1 = none)
+ *   w13_*, w2_*     in  as for nvfp4_moe_w4a16_forward (w2_packed and w13_packed 16-byte aligned)
+ *   workspace       tmp nvfp4_moe_decode_workspace_bytes(T, topk, E, H, I) bytes, 16-byte aligned;
+ *                       its contents need no preparation
+ *   out             out bf16 [T, H], 16-byte aligned
+ *   topk_ids, topk_weights   out  int32 / float [T, topk], each optional (NULL)
+ */
+typedef enum {
+  NVFP4_MOE_SOFTMAX = 0,
+  NVFP4_MOE_SIGMOID = 1
+} nvfp4_moe_scoring;
+int64_t nvfp4_moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I);
+nvfp4_status nvfp4_moe_w4a16_decode(const void* x, int64_t T, int64_t H, const void* router_logits,
+                                    int router_dtype, int64_t E, int64_t topk, int scoring, int renormalize,
+                                    const float* correction_bias, float weight_scale, const uint8_t* w13_packed,
+                                    const uint8_t* w13_scales, const float* w13_global_scales,
+                                    const uint8_t* w2_packed, const uint8_t* w2_scales,
+                                    const float* w2_global_scales, int64_t I, void* workspace, void* out,
+                                    int32_t* topk_ids, float* topk_weights, void* stream);
+
+/*
  * int4 weights with group scales.
  * (vLLM API docs, compressed_tensors.schemes, class CompressedTensorsWNA16,
  * 4 bits without activation reordering.)

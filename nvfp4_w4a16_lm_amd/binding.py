@@ -44,7 +44,8 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_refresh_inplace", "nvfp4_w4a16_gemm",
             "nvfp4_w4a4_gemm_noalloc",
             "nvfp4_moe_gemm_workspace_bytes", "nvfp4_moe_w4a16_gemm", "nvfp4_moe_silu_and_mul",
             "nvfp4_moe_combine", "nvfp4_moe_workspace_bytes", "nvfp4_moe_w4a16_forward",
-            "nvfp4_int4_gemm", "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "nvfp4_logprobs_backward",
+            "nvfp4_moe_decode_workspace_bytes", "nvfp4_moe_w4a16_decode", "nvfp4_int4_gemm",
+            "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "nvfp4_logprobs_backward",
             "nvfp4_status_string", "nvfp4_last_hip_error", "nvfp4_abi_version")
 
 
@@ -113,6 +114,11 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_moe_w4a16_forward.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, vp,
                                             vp, vp]
     lib.nvfp4_moe_w4a16_forward.restype = ctypes.c_int
+    lib.nvfp4_moe_decode_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.nvfp4_moe_decode_workspace_bytes.restype = i64
+    lib.nvfp4_moe_w4a16_decode.argtypes = [vp, i64, i64, vp, ctypes.c_int, i64, i64, ctypes.c_int, ctypes.c_int, vp,
+                                           ctypes.c_float, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    lib.nvfp4_moe_w4a16_decode.restype = ctypes.c_int
     lib.nvfp4_int4_gemm.argtypes = [vp, i64, i64, vp, vp, ctypes.c_int, vp, i64, i64, vp, vp, vp]
     lib.nvfp4_int4_gemm.restype = ctypes.c_int
     lib.nvfp4_logprobs_workspace_bytes.argtypes = [i64, i64, i64]
@@ -565,6 +571,64 @@ def nvfp4_moe_w4a16_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weight
                                        _ptr(w13[2]), _ptr(w2[0]), _ptr(w2[1]), _ptr(w2[2]), e, i,
                                        _ptr(workspace), _ptr(out), _ptr(invalid_pairs), _stream_of(x, stream)))
     return out
+
+
+#: Scores of nvfp4_moe_w4a16_decode (nvfp4_moe_scoring) and its largest batch.
+MOE_SCORING = {"softmax": 0, "sigmoid": 1}
+MOE_DECODE_MAX_TOKENS = 16
+
+
+def moe_decode_workspace(t: int, topk: int, e: int, h: int, i: int, device) -> torch.Tensor:
+    """Workspace of nvfp4_moe_w4a16_decode for these sizes, to be kept."""
+    need = int(load_library().nvfp4_moe_decode_workspace_bytes(t, topk, e, h, i))
+    if need == 0:
+        raise NVFP4ShapeError("nvfp4_moe_w4a16_decode", 2, f"T={t}, topk={topk}, E={e}, H={h}, I={i}")
+    return torch.empty((need,), dtype=torch.uint8, device=device)
+
+
+def nvfp4_moe_w4a16_decode(x: torch.Tensor, router_logits: torch.Tensor, topk: int, w13: tuple, w2: tuple,
+                           scoring: str = "softmax", renormalize: bool = True,
+                           correction_bias: torch.Tensor | None = None, weight_scale: float = 1.0,
+                           out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The whole W4A16 expert layer for T <= 16 tokens in two kernels: bf16 x
+    [T, H] and router logits (float32 or bfloat16 [T, E]) -> (bf16 [T, H],
+    topk_ids int32 [T, topk], topk_weights float32 [T, topk]).  ``w13`` / ``w2`` as
+    for nvfp4_moe_w4a16_forward; ``correction_bias`` float32 [E] is added to the
+    scores for the choice only."""
+    x = _as_bf16_2d(x, "x")
+    t, hdim = x.shape
+    dev = x.device
+    if scoring not in MOE_SCORING:
+        raise ValueError(f"scoring must be one of {sorted(MOE_SCORING)}, got {scoring!r}")
+    e, n13 = _check_experts(*w13, hdim, dev, "w13")
+    if w2[0].dim() != 3:
+        raise ValueError("w2 packed must be [E, H, I/2]")
+    i = w2[0].shape[2] * 2
+    e2, n2 = _check_experts(*w2, i, dev, "w2")
+    if n13 != 2 * i or e2 != e or n2 != hdim:
+        raise ValueError(f"w13 [E, {n13}, .] and w2 [{e2}, {n2}, {i // 2}] do not fit H={hdim}")
+    _check_out(router_logits, (t, e), (torch.float32, torch.bfloat16), dev, "router_logits")
+    _check_vec(correction_bias, e, torch.float32, dev, "correction_bias")
+    if out is None:
+        out = torch.empty((t, hdim), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out(out, (t, hdim), (torch.bfloat16,), dev, "out")
+    lib = load_library()
+    if workspace is None:
+        workspace = moe_decode_workspace(t, topk, e, hdim, i, dev)
+    else:
+        need = int(lib.nvfp4_moe_decode_workspace_bytes(t, topk, e, hdim, i))
+        if workspace.numel() * workspace.element_size() < need or workspace.device != dev:
+            raise ValueError(f"workspace needs {need} bytes on {dev}")
+    ids = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    weights = torch.empty((t, topk), dtype=torch.float32, device=dev)
+    _check("nvfp4_moe_w4a16_decode",
+           lib.nvfp4_moe_w4a16_decode(_ptr(x), t, hdim, _ptr(router_logits), LOGIT_DTYPES[router_logits.dtype], e,
+                                      topk, MOE_SCORING[scoring], int(renormalize), _ptr(correction_bias),
+                                      float(weight_scale), _ptr(w13[0]), _ptr(w13[1]), _ptr(w13[2]), _ptr(w2[0]),
+                                      _ptr(w2[1]), _ptr(w2[2]), i, _ptr(workspace), _ptr(out), _ptr(ids),
+                                      _ptr(weights), _stream_of(x, stream)))
+    return out, ids, weights
 
 
 # ---------------------------------------------------------------------------

@@ -30,6 +30,20 @@ bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+bool any_overlap(const Range* outs, int n_out, const Range* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlap(outs[i], outs[j])) return true;
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(outs[i], ins[j])) return true;
+  }
+  return false;
+}
+
+Range optional_span(const void* p, int64_t bytes) { return span(p, p ? bytes : 0); }
+
+int64_t dtype_bytes(int dtype) { return dtype == NVFP4_F32 ? 4 : 2; }
+
 nvfp4_status check_weight_shape(int64_t N, int64_t K) {
   if (N < 1 || K < NVFP4_GROUP || K % NVFP4_GROUP != 0) return NVFP4_ERR_SHAPE;
   if (N > kMaxDim || K > kMaxDim || N * K > kMaxElems) return NVFP4_ERR_SHAPE;
@@ -395,8 +409,6 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
 
 namespace {
 
-int64_t dtype_bytes(int dtype) { return dtype == NVFP4_F32 ? 4 : 2; }
-
 // Bytes that M rows of V elements, `stride` elements apart, span.
 Range rows_span(const void* p, int64_t M, int64_t V, int64_t stride, int64_t elem) {
   return span(p, ((M - 1) * stride + V) * elem);
@@ -409,18 +421,6 @@ nvfp4_status check_logits(int dtype, int64_t M, int64_t V, int64_t row_stride) {
     return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
-
-bool any_overlap(const Range* outs, int n_out, const Range* ins, int n_in) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-    for (int j = 0; j < n_in; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-  }
-  return false;
-}
-
-Range optional_span(const void* p, int64_t bytes) { return span(p, p ? bytes : 0); }
 
 }  // namespace
 
@@ -520,6 +520,89 @@ nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, i
   a.dx = static_cast<uint8_t*>(dlogits);
   a.dx_stride = dlogits_stride;
   return finish(nvfp4::launch_logprobs_backward(a, dtype, M, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// The whole expert layer for a few tokens
+// ---------------------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+nvfp4_status check_moe_decode(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I) {
+  if (T < 0 || T > nvfp4::kMoeDecodeMaxT || E < 1 || E > nvfp4::kMoeDecodeMaxE || topk < 1 || topk > E ||
+      topk > nvfp4::kMoeDecodeMaxTopk || I < NVFP4_GROUP || I > kMaxDim)
+    return NVFP4_ERR_SHAPE;
+  const nvfp4_status s = check_experts(E, 2 * I, H);
+  return s != NVFP4_OK ? s : check_experts(E, H, I);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t nvfp4_moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I) {
+  return check_moe_decode(T, topk, E, H, I) == NVFP4_OK ? nvfp4::moe_decode_workspace_bytes(T, topk, H, I) : 0;
+}
+
+nvfp4_status nvfp4_moe_w4a16_decode(const void* x, int64_t T, int64_t H, const void* router_logits,
+                                    int router_dtype, int64_t E, int64_t topk, int scoring, int renormalize,
+                                    const float* correction_bias, float weight_scale, const uint8_t* w13_packed,
+                                    const uint8_t* w13_scales, const float* w13_global_scales,
+                                    const uint8_t* w2_packed, const uint8_t* w2_scales,
+                                    const float* w2_global_scales, int64_t I, void* workspace, void* out,
+                                    int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (!w13_packed || !w13_scales || !w13_global_scales || !w2_packed || !w2_scales || !w2_global_scales ||
+      (T != 0 && (!x || !router_logits || !workspace || !out)))
+    return NVFP4_ERR_NULL;
+  if ((router_dtype != NVFP4_F32 && router_dtype != NVFP4_BF16) ||
+      (scoring != NVFP4_MOE_SOFTMAX && scoring != NVFP4_MOE_SIGMOID) || (renormalize != 0 && renormalize != 1))
+    return NVFP4_ERR_ARG;
+  const nvfp4_status s = check_moe_decode(T, topk, E, H, I);
+  if (s != NVFP4_OK) return s;
+  if (T == 0) return NVFP4_OK;
+  const int64_t P = T * topk, rb = dtype_bytes(router_dtype);
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(w13_packed, 16) || !aligned(w2_packed, 16) ||
+      !aligned(w13_global_scales, 4) || !aligned(w2_global_scales, 4) || !aligned(router_logits, rb) ||
+      !aligned(correction_bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(out, T * H * 2), span(workspace, nvfp4::moe_decode_workspace_bytes(T, topk, H, I)),
+                        optional_span(topk_ids, P * 4), optional_span(topk_weights, P * 4)};
+  const Range ins[] = {span(x, T * H * 2),
+                       span(router_logits, T * E * rb),
+                       optional_span(correction_bias, E * 4),
+                       span(w13_packed, E * 2 * I * H / 2),
+                       span(w13_scales, E * 2 * I * H / 16),
+                       span(w13_global_scales, E * 4),
+                       span(w2_packed, E * H * I / 2),
+                       span(w2_scales, E * H * I / 16),
+                       span(w2_global_scales, E * 4)};
+  if (any_overlap(outs, 4, ins, 9)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  nvfp4::MoeDecodeArgs a = {};
+  a.x = static_cast<const uint16_t*>(x);
+  a.router = router_logits;
+  a.bias = correction_bias;
+  a.w13_packed = w13_packed;
+  a.w13_scales = w13_scales;
+  a.w13_gs = w13_global_scales;
+  a.w2_packed = w2_packed;
+  a.w2_scales = w2_scales;
+  a.w2_gs = w2_global_scales;
+  a.out = static_cast<uint16_t*>(out);
+  a.ids_out = topk_ids;
+  a.weights_out = topk_weights;
+  a.T = (int32_t)T;
+  a.H = (int32_t)H;
+  a.I = (int32_t)I;
+  a.E = (int32_t)E;
+  a.topk = (int32_t)topk;
+  a.router_f32 = router_dtype == NVFP4_F32;
+  a.sigmoid = scoring == NVFP4_MOE_SIGMOID;
+  a.renormalize = renormalize;
+  a.weight_scale = weight_scale;
+  return finish(nvfp4::launch_moe_decode(a, workspace, (hipStream_t)stream));
 }
 
 // ---------------------------------------------------------------------------

@@ -231,4 +231,38 @@ struct Int4Args {
 };
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream);
 
+// The whole expert layer for a few tokens (moe_decode.hip); the fields from
+// `ids` on are the launcher's.
+constexpr int kMoeDecodeMaxT = 16;
+constexpr int kMoeDecodeMaxTopk = 32;
+constexpr int kMoeDecodeMaxE = 1024;
+struct MoeDecodeArgs {
+  const uint16_t* x;
+  const void* router;
+  const float* bias;
+  const uint8_t* w13_packed;
+  const uint8_t* w13_scales;
+  const float* w13_gs;
+  const uint8_t* w2_packed;
+  const uint8_t* w2_scales;
+  const float* w2_gs;
+  uint16_t* out;
+  int32_t* ids_out;
+  float* weights_out;
+  int32_t T, H, I, E, topk;
+  int32_t router_f32, sigmoid, renormalize;
+  float weight_scale;
+  int32_t* ids;
+  float* weights;
+  int32_t* list;
+  int32_t* active;
+  uint16_t* a_hi;
+  uint16_t* a_lo;
+  int32_t* counters;
+  float* parts;
+  int32_t splitk, down_split, n_counters;
+};
+int64_t moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t H, int64_t I);
+hipError_t launch_moe_decode(MoeDecodeArgs a, void* workspace, hipStream_t stream);
+
 }  // namespace nvfp4
