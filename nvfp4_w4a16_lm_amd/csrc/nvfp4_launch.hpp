@@ -217,7 +217,8 @@ int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk);
 hipError_t launch_logprobs(LogprobsArgs a, int dtype, int64_t M, void* workspace, hipStream_t stream);
 hipError_t launch_logprobs_backward(LogprobsBackwardArgs a, int dtype, int64_t M, hipStream_t stream);
 
-// int4 weights with group scales (int4_gemm.hip); splitk is the launcher's.
+// int4 weights with group scales (int4_gemm.hip); splitk and scale_pitch are the
+// launcher's.
 struct Int4Args {
   const uint16_t* x;
   const uint8_t* packed;
@@ -227,7 +228,7 @@ struct Int4Args {
   uint16_t* y;
   int32_t M, K, N, group, groups;
   int32_t scale_f16;
-  int32_t splitk;
+  int32_t splitk, scale_pitch;
 };
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream);
 
