@@ -28,6 +28,7 @@
 
 #include "nvfp4_device.hpp"
 #include "nvfp4_launch.hpp"
+#include "stream4.hpp"
 
 namespace nvfp4 {
 
@@ -187,6 +188,47 @@ __device__ __forceinline__ void load_x(const uint16_t* row, bool use, int c, int
     xv[s] = use && k0 + 8 * s < K ? *reinterpret_cast<const u32x4*>(row + k0 + 8 * s) : u32x4{0u, 0u, 0u, 0u};
 }
 
+// Routes every token of the batch and lists the chosen experts in increasing
+// order, in LDS (one workgroup of W wavefronts); workgroup 0 leaves the results
+// for the second kernel and the caller.  flag has 64 NI words.
+template <int NI>
+__device__ __forceinline__ int route_all(const MoeDecodeArgs& a, int32_t* ids, float* weights, int32_t* flag,
+                                         int32_t* list, int32_t* n_active) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int threads = blockDim.x, pairs = a.T * a.topk;
+  for (int e = tid; e < 64 * NI; e += threads) flag[e] = 0;
+  for (int t = wave; t < a.T; t += threads >> 6) route_token<NI>(a, t, lane, ids, weights);
+  __syncthreads();
+  for (int p = tid; p < pairs; p += threads)
+    if (ids[p] >= 0) flag[ids[p]] = 1;
+  __syncthreads();
+  if (wave == 0) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool on = flag[64 * i + lane] != 0;
+      const uint64_t all = __ballot(on);
+      if (on) list[n + __popcll(all & (((uint64_t)1 << lane) - 1))] = 64 * i + lane;
+      n += __popcll(all);
+    }
+    if (lane == 0) *n_active = n;
+  }
+  __syncthreads();
+  const int active = *n_active;
+  if (blockIdx.x == 0) {
+    for (int p = tid; p < pairs; p += threads) {
+      a.ids[p] = ids[p];
+      a.weights[p] = weights[p];
+      if (a.ids_out) a.ids_out[p] = ids[p];
+      if (a.weights_out) a.weights_out[p] = weights[p];
+    }
+    for (int s = tid; s < active; s += threads) a.list[s] = list[s];
+    if (tid == 0) *a.active = active;
+    for (int i = tid; i < a.n_counters; i += threads) a.counters[i] = 0;
+  }
+  return active;
+}
+
 #define NVFP4_MD_STEPS(F) F(0) F(1) F(2) F(3) F(4) F(5) F(6) F(7)
 
 }  // namespace
@@ -201,37 +243,7 @@ __global__ __launch_bounds__(64 * kMdWaves) void moe_decode_up_kernel(MoeDecodeA
   __shared__ float red[kMdWaves][8][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int pairs = a.T * a.topk;
-  for (int e = tid; e < 64 * NI; e += 64 * kMdWaves) sh_flag[e] = 0;
-  for (int t = wave; t < a.T; t += kMdWaves) route_token<NI>(a, t, lane, sh_ids, sh_w);
-  __syncthreads();
-  for (int p = tid; p < pairs; p += 64 * kMdWaves)
-    if (sh_ids[p] >= 0) sh_flag[sh_ids[p]] = 1;
-  __syncthreads();
-  if (wave == 0) {                                      // the chosen experts in increasing order
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const bool on = sh_flag[64 * i + lane] != 0;
-      const uint64_t all = __ballot(on);
-      if (on) sh_list[n + __popcll(all & (((uint64_t)1 << lane) - 1))] = 64 * i + lane;
-      n += __popcll(all);
-    }
-    if (lane == 0) sh_active = n;
-  }
-  __syncthreads();
-  const int active = sh_active;
-  if (blockIdx.x == 0) {                                // for the second kernel and the caller
-    for (int p = tid; p < pairs; p += 64 * kMdWaves) {
-      a.ids[p] = sh_ids[p];
-      a.weights[p] = sh_w[p];
-      if (a.ids_out) a.ids_out[p] = sh_ids[p];
-      if (a.weights_out) a.weights_out[p] = sh_w[p];
-    }
-    for (int s = tid; s < active; s += 64 * kMdWaves) a.list[s] = sh_list[s];
-    if (tid == 0) *a.active = active;
-    for (int i = tid; i < a.n_counters; i += 64 * kMdWaves) a.counters[i] = 0;
-  }
+  const int active = route_all<NI>(a, sh_ids, sh_w, sh_flag, sh_list, &sh_active);
 
   const int splitk = a.splitk, rg = wave / splitk, ph = wave - rg * splitk;
   const int per = kMdWaves / splitk;                    // 16-column tiles per workgroup and item
@@ -414,6 +426,484 @@ __global__ __launch_bounds__(64 * kMdDownWaves) void moe_decode_down_kernel(MoeD
   if (mine) a.out[(int64_t)t * a.H + 16 * tile + n] = __builtin_bit_cast(uint16_t, (__bf16)sum);
 }
 
+// ---------------------------------------------------------------------------
+// The streamed form (H and I multiples of 32, from 64; stream4.hpp's scheme).
+//
+// A wavefront keeps the activations of its chunks as f16 MFMA operands, scaled by a power
+// of two of its own per token, chosen so that the largest magnitude among its
+// k lands in [2^14, 2^15): a bf16 value down to 2^-28 of that largest one stays
+// exact, a float32 one keeps 11 bits.  The wavefront's sums are scaled back
+// before they meet the others', so the scales need not agree.  In f16 a code
+// times its block scale costs half of what it costs in bf16 (and is as exact).
+// ---------------------------------------------------------------------------
+namespace {
+
+__device__ __forceinline__ f32x4 mfma_md16(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Largest of the four lanes of a column (r, r + 16, r + 32, r + 48).
+__device__ __forceinline__ uint32_t column_max(uint32_t v) {
+  auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(p[0], p[1]);
+  p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(p[0], p[1]);
+}
+
+// Exponent p with the magnitude (float32 bits) times 2^-p in [2^14, 2^15).
+__device__ __forceinline__ int scale_exponent(uint32_t mag) {
+  return mag < 0x00800000u ? 0 : max(-126, (int)(mag >> 23) - 141);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ f16x8 pack_f16(const float* v, float down) {
+  f16x8 h;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) h[e] = (_Float16)(v[e] * down);
+  return h;
+}
+
+// Block scales of rows for the workgroup: thread `it` holds word it % words of row
+// it / words of a 16-row tile; nb = bytes of a row's scales.
+__device__ __forceinline__ uint32_t load_scale_word(const uint8_t* row, int word, int nb) {
+  const int off = min(4 * word, nb - 4), shift = 8 * (4 * word - off);
+  const uint32_t w = reinterpret_cast<const Word4A1*>(row + off)->v;
+  return shift < 32 ? w >> shift : 0u;                   // blocks past the row's end have scale 0
+}
+
+struct ScaleSplit {
+  float s[4];
+  f16x2 mu[4];
+};
+__device__ __forceinline__ ScaleSplit split4(uint32_t w) {
+  ScaleSplit o;
+  o.s[0] = NVFP4_E4M3_TO_F32(w, 0);
+  o.s[1] = NVFP4_E4M3_TO_F32(w, 1);
+  o.s[2] = NVFP4_E4M3_TO_F32(w, 2);
+  o.s[3] = NVFP4_E4M3_TO_F32(w, 3);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) o.mu[b] = scale_mantissa_f16(o.s[b]);
+  return o;
+}
+
+// acc += (tile chunk) x (activations of the chunk), k = 64 g + 8 s + [0, 8).
+__device__ __forceinline__ f32x4 chunk_product(u32x4 w0, u32x4 w1, uint32_t sw, const f16x8* xb, f32x4 acc) {
+  const ScaleSplit q = split4(sw);
+  f32x4 odd = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const uint32_t w = s < 4 ? w0[s & 3] : w1[s & 3];
+    const f16x8 a = dequant8_f16(w, q.s[s >> 1], q.mu[s >> 1]);
+    if (s & 1)
+      odd = mfma_md16(a, xb[s], odd);
+    else
+      acc = mfma_md16(a, xb[s], acc);
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] += odd[v];
+  return acc;
+}
+
+constexpr int kMdDepth = 3;                  // tiles in flight per wavefront
+
+// LDS words of a row's scales for W wavefronts of NC chunks, padded to spread the rows.
+__device__ __host__ constexpr int md_scale_pitch(int slots) { return 4 * slots + 1; }
+
+}  // namespace
+
+// Up: a[pair, i] = silu(gate) * up, float32.  Units (expert, 16 columns of I) are
+// dealt to the workgroups in contiguous runs; each is two tiles, the gate's and
+// the up's.
+template <int NI, int NC>
+__global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
+  __shared__ int32_t sh_ids[kMdMaxPairs];
+  __shared__ float sh_w[kMdMaxPairs];
+  __shared__ int32_t sh_flag[64 * NI];
+  __shared__ int32_t sh_list[kMdMaxPairs];
+  __shared__ int32_t sh_active;
+  constexpr int D = kMdDepth;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int W = blockDim.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int K = a.H, nb = K >> 4, nch = (K + kSt4Chunk - 1) / kSt4Chunk;
+  const int64_t pitch = K >> 1;
+  const int phases = (nch + W * NC - 1) / (W * NC);
+  uint8_t* const ring = lds8 + wave * (D * NC * kSt4Bytes);
+  float* const red = reinterpret_cast<float*>(lds8 + W * (D * NC * kSt4Bytes));          // [W][2][256]
+  const int spitch = md_scale_pitch(W * NC);
+  uint32_t* const scl = reinterpret_cast<uint32_t*>(red + W * 512);                      // [2][16][spitch]
+  float* const held = reinterpret_cast<float*>(scl + 32 * spitch);                       // [units][512], several phases
+
+  const int active = route_all<NI>(a, sh_ids, sh_w, sh_flag, sh_list, &sh_active);
+  const int tiles = a.I >> 4, units = active * tiles;
+  const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  if (u0 >= u1) return;
+  const int s0 = 2 * u0, s1 = 2 * u1;                     // steps: tile 2 u is gate, 2 u + 1 is up
+  // first weight row of step s's tile
+  auto row_of = [&](int s) {
+    const int u = s >> 1, slot = u / tiles;
+    return (int64_t)sh_list[slot] * 2 * a.I + (s & 1) * a.I + 16 * (u - slot * tiles);
+  };
+
+  for (int ph = 0; ph < phases; ++ph) {
+    const int c0 = (ph * W + wave) * NC, words = 4 * W * NC;
+    int srow[NC], sword[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int it = tid + i * blockDim.x;
+      srow[i] = it / words;
+      sword[i] = it - srow[i] * words;
+    }
+    uint32_t sv[D][NC];
+    auto load_scales = [&](int s, int slot) {
+      const uint8_t* const base = a.w13_scales + row_of(min(s, s1 - 1)) * nb;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        sv[slot][i] = load_scale_word(base + (int64_t)srow[i] * nb, 4 * ph * W * NC + sword[i], nb);
+    };
+    auto store_scales = [&](int s, int slot) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) scl[((s & 1) * 16 + srow[i]) * spitch + sword[i]] = sv[slot][i];
+    };
+    auto copy_tile = [&](int s, int slot) {
+      const uint8_t* const base = a.w13_packed + row_of(min(s, s1 - 1)) * pitch;
+#pragma unroll
+      for (int q = 0; q < NC; ++q) st4_copy(base, pitch, 15, c0 + q, ring + (slot * NC + q) * kSt4Bytes, lane);
+    };
+    // the scales travel one tile ahead of the copies (see int4_gemm.hip)
+    load_scales(s0, 0);
+    store_scales(s0, 0);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      load_scales(s0 + d + 1, d);
+      copy_tile(s0 + d, d);
+    }
+    // activations: column r is token r
+    f16x8 xb[NC][8];
+    float back;
+    {
+      u32x4 xv[NC][8];
+      uint32_t mag = 0;
+      const uint16_t* const xrow = a.x + (int64_t)min(r, a.T - 1) * K;
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        load_x(xrow, true, c0 + q, g, K, xv[q]);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mag = pk_max_u16(mag, xv[q][s][e] & 0x7FFF7FFFu);
+      }
+      mag = max(mag & 0xFFFFu, mag >> 16) << 16;
+      const int p = scale_exponent(column_max(mag));
+      back = pow2(p);
+      const float down = pow2(-p);
+#pragma unroll
+      for (int q = 0; q < NC; ++q)
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[2 * e] = bf16_lo(xv[q][s][e]);
+            f[2 * e + 1] = bf16_hi(xv[q][s][e]);
+          }
+          xb[q][s] = pack_f16(f, down);
+        }
+    }
+    st4_barrier();
+
+    f32x4 gate;
+    auto step = [&](int s, int slot) {
+      __builtin_amdgcn_s_waitcnt(st4_vm((D - 1) * 3 * NC));
+      __asm__ volatile("" ::: "memory");
+      u32x4 w[NC][2];
+      uint32_t sw[NC];
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        w[q][0] = st4_read(ring + (slot * NC + q) * kSt4Bytes, r, 2 * g);
+        w[q][1] = st4_read(ring + (slot * NC + q) * kSt4Bytes, r, 2 * g + 1);
+        sw[q] = scl[((s & 1) * 16 + r) * spitch + 4 * (wave * NC + q) + g];
+      }
+      __builtin_amdgcn_s_waitcnt(kSt4Lgkm0);
+      __asm__ volatile("" ::: "memory");
+      store_scales(s + 1, slot);
+      load_scales(s + D + 1, slot);
+      copy_tile(s + D, slot);
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < NC; ++q) acc = chunk_product(w[q][0], w[q][1], sw[q], xb[q], acc);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[v] *= back;
+      // the gate's sums wait in registers: between two units' writes to red lies
+      // the barrier of the second one's gate step
+      if (s & 1) {
+        *reinterpret_cast<f32x4*>(red + wave * 512 + 4 * lane) = gate;
+        *reinterpret_cast<f32x4*>(red + wave * 512 + 256 + 4 * lane) = acc;
+      } else {
+        gate = acc;
+      }
+      st4_barrier();
+    };
+    // the unit's sums: element 4 l + v is lane l's v: token l % 16, column 4 (l / 16) + v of the tile
+    auto finish = [&](int u) {
+      const int slot = u / tiles, e = sh_list[slot];
+      for (int i = tid; i < 256; i += blockDim.x) {
+        const int t = (i >> 2) & 15, n = 4 * (i >> 6) + (i & 3);
+        float sum[2] = {0.0f, 0.0f};
+        for (int v = 0; v < W; v += 4) {
+          float q[4][2];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            q[b][0] = red[min(v + b, W - 1) * 512 + i];
+            q[b][1] = red[min(v + b, W - 1) * 512 + 256 + i];
+          }
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            sum[0] += v + b < W ? q[b][0] : 0.0f;
+            sum[1] += v + b < W ? q[b][1] : 0.0f;
+          }
+        }
+        if (phases > 1) {
+          float* const h = held + (u - u0) * 512 + i;
+          if (ph > 0) {
+            sum[0] += h[0];
+            sum[1] += h[256];
+          }
+          if (ph + 1 < phases) {
+            h[0] = sum[0];
+            h[256] = sum[1];
+            continue;
+          }
+        }
+        if (t >= a.T) continue;
+        int pair = -1;
+        for (int j = 0; j < a.topk; ++j)
+          if (sh_ids[t * a.topk + j] == e) pair = t * a.topk + j;
+        if (pair < 0) continue;
+        const float gs = a.w13_gs[e];
+        const float gv = sum[0] * gs, uv = sum[1] * gs;
+        a.act[(int64_t)pair * a.I + 16 * (u - slot * tiles) + n] = gv / (1.0f + expf(-gv)) * uv;
+      }
+    };
+    // two steps a unit, D in flight: the pattern repeats every 2 D steps
+    for (int s = s0; s < s1; s += 2 * D) {
+#pragma unroll
+      for (int d = 0; d < 2 * D; d += 2) {
+        if (s + d < s1) {
+          step(s + d, d % D);
+          step(s + d + 1, (d + 1) % D);
+          finish((s + d) >> 1);
+        }
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(st4_vm(0));
+    __syncthreads();
+  }
+}
+
+// Down: units (expert, slice of I of W chunks, 16 output columns) in contiguous
+// runs; each leaves w[t, j] W2_e a over its slice in parts[slice][pair][column].
+// A workgroup counts its units' columns when it is done; whoever completes a
+// column tile's count adds its parts, in order of slice and slot.
+template <int NC>
+__global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
+  __shared__ int32_t sh_ids[kMdMaxPairs];
+  __shared__ float sh_w[kMdMaxPairs];
+  __shared__ int32_t sh_list[kMdMaxPairs];
+  __shared__ int32_t sh_done[1024];
+  constexpr int D = kMdDepth;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int W = blockDim.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int K = a.I, nb = K >> 4, P = a.T * a.topk;
+  const int64_t pitch = K >> 1;
+  uint8_t* const ring = lds8 + wave * (D * NC * kSt4Bytes);
+  float* const red = reinterpret_cast<float*>(lds8 + W * (D * NC * kSt4Bytes));          // [2][W][256]
+  const int spitch = md_scale_pitch(W * NC);
+  uint32_t* const scl = reinterpret_cast<uint32_t*>(red + 2 * W * 256);                  // [2][16][spitch]
+
+  const int active = *a.active, slices = a.slices, tiles = a.H >> 4;
+  for (int p = tid; p < P; p += blockDim.x) {
+    sh_ids[p] = a.ids[p];
+    sh_w[p] = a.weights[p];
+  }
+  for (int s = tid; s < active; s += blockDim.x) sh_list[s] = a.list[s];
+  __syncthreads();
+  const int units = active * slices * tiles;
+  const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+  if (active == 0) {                                       // no token has an expert
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + tid; i < (int64_t)a.T * a.H; i += (int64_t)gridDim.x * blockDim.x)
+      a.out[i] = 0;
+    return;
+  }
+  if (u0 >= u1) return;
+  auto row_of = [&](int u) {                               // first weight row of a unit's tile
+    const int c = u / tiles;
+    return (int64_t)sh_list[c / slices] * a.H + 16 * (u - c * tiles);
+  };
+  auto slice_of = [&](int u) { return (u / tiles) % slices; };
+  const int words = 4 * W * NC;
+  int srow[NC], sword[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int it = tid + i * blockDim.x;
+    srow[i] = it / words;
+    sword[i] = it - srow[i] * words;
+  }
+  uint32_t sv[D][NC];
+  auto load_scales = [&](int u, int slot) {
+    const int uc = min(u, u1 - 1);
+    const uint8_t* const base = a.w2_scales + row_of(uc) * nb;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      sv[slot][i] = load_scale_word(base + (int64_t)srow[i] * nb, words * slice_of(uc) + sword[i], nb);
+  };
+  auto store_scales = [&](int u, int slot) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) scl[((u & 1) * 16 + srow[i]) * spitch + sword[i]] = sv[slot][i];
+  };
+  auto copy_tile = [&](int u, int slot) {
+    const int uc = min(u, u1 - 1);
+    const uint8_t* const base = a.w2_packed + row_of(uc) * pitch;
+#pragma unroll
+    for (int q = 0; q < NC; ++q)
+      st4_copy(base, pitch, 15, (slice_of(uc) * W + wave) * NC + q, ring + (slot * NC + q) * kSt4Bytes, lane);
+  };
+  load_scales(u0, 0);
+  store_scales(u0, 0);
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load_scales(u0 + d + 1, d);
+    copy_tile(u0 + d, d);
+  }
+  st4_barrier();
+
+  f16x8 xb[NC][8];
+  float back = 0.0f;
+  int combo = -1, pair = -1;
+  // the activations of (expert, slice) c: column r is token r's pair with the expert, or zeros
+  auto load_act = [&](int c) {
+    combo = c;
+    const int e = sh_list[c / slices], c0 = ((c % slices) * W + wave) * NC;
+    pair = -1;
+    if (r < a.T)
+      for (int j = 0; j < a.topk; ++j)
+        if (sh_ids[r * a.topk + j] == e) pair = r * a.topk + j;
+    const float* const row = a.act + (int64_t)max(pair, 0) * K;
+    uint32_t mag = 0;
+    float f[NC][8][8];
+#pragma unroll
+    for (int q = 0; q < NC; ++q)
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int k = kSt4Chunk * (c0 + q) + 64 * g + 8 * s;
+        f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+        if (pair >= 0 && k < K) {
+          lo = *reinterpret_cast<const f32x4*>(row + k);
+          hi = *reinterpret_cast<const f32x4*>(row + k + 4);
+        }
+#pragma unroll
+        for (int e2 = 0; e2 < 4; ++e2) {
+          f[q][s][e2] = lo[e2];
+          f[q][s][4 + e2] = hi[e2];
+          mag = max(mag, max(__float_as_uint(lo[e2]) & 0x7FFFFFFFu, __float_as_uint(hi[e2]) & 0x7FFFFFFFu));
+        }
+      }
+    const int p = scale_exponent(column_max(mag));
+    back = pow2(p) * a.w2_gs[e] * (pair >= 0 ? sh_w[pair] : 0.0f);
+    const float down = pow2(-p);
+#pragma unroll
+    for (int q = 0; q < NC; ++q)
+#pragma unroll
+      for (int s = 0; s < 8; ++s) xb[q][s] = pack_f16(f[q][s], down);
+  };
+
+  auto step = [&](int u, int slot) {
+    const int c = u / tiles;
+    if (c != combo) load_act(c);                           // uniform over the workgroup
+    __builtin_amdgcn_s_waitcnt(st4_vm((D - 1) * 3 * NC));
+    __asm__ volatile("" ::: "memory");
+    u32x4 w[NC][2];
+    uint32_t sw[NC];
+#pragma unroll
+    for (int q = 0; q < NC; ++q) {
+      w[q][0] = st4_read(ring + (slot * NC + q) * kSt4Bytes, r, 2 * g);
+      w[q][1] = st4_read(ring + (slot * NC + q) * kSt4Bytes, r, 2 * g + 1);
+      sw[q] = scl[((u & 1) * 16 + r) * spitch + 4 * (wave * NC + q) + g];
+    }
+    __builtin_amdgcn_s_waitcnt(kSt4Lgkm0);
+    __asm__ volatile("" ::: "memory");
+    store_scales(u + 1, slot);
+    load_scales(u + D + 1, slot);
+    copy_tile(u + D, slot);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int q = 0; q < NC; ++q) acc = chunk_product(w[q][0], w[q][1], sw[q], xb[q], acc);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] *= back;
+    *reinterpret_cast<f32x4*>(red + ((u & 1) * W + wave) * 256 + 4 * lane) = acc;
+    st4_barrier();
+    for (int i = tid; i < 256; i += blockDim.x) {
+      const int t = (i >> 2) & 15, n = 4 * (i >> 6) + (i & 3);
+      if (t >= a.T) continue;
+      const float* const part = red + (u & 1) * W * 256 + i;
+      float sum = 0.0f;
+      for (int v = 0; v < W; v += 4) {
+        float q[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) q[b] = part[min(v + b, W - 1) * 256];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) sum += v + b < W ? q[b] : 0.0f;
+      }
+      const int e = sh_list[c / slices];
+      int p = -1;
+      for (int j = 0; j < a.topk; ++j)
+        if (sh_ids[t * a.topk + j] == e) p = t * a.topk + j;
+      if (p >= 0)
+        __hip_atomic_store(a.parts + ((int64_t)(c % slices) * P + p) * a.H + 16 * (u - c * tiles) + n, sum,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  };
+  for (int u = u0; u < u1; u += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (u + d < u1) step(u + d, d);
+  }
+
+  // count the units; a tile is complete with active * slices of them.  The parts
+  // were stored past the caches (agent scope) and have arrived once this wait
+  // ends, so the counting needs no cache write-back, only order
+  __builtin_amdgcn_s_waitcnt(st4_vm(0));
+  __syncthreads();
+  for (int v0 = u0; v0 < u1; v0 += 1024) {
+    const int n = min(1024, u1 - v0);
+    for (int i = tid; i < n; i += blockDim.x) {
+      const int tile = (v0 + i) % tiles;
+      const int before = __hip_atomic_fetch_add(a.counters + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      sh_done[i] = before + 1 == active * slices ? tile : -1;
+    }
+    __syncthreads();
+    for (int i = wave; i < n; i += W) {
+      const int tile = sh_done[i];
+      if (tile < 0) continue;
+      for (int o = lane; o < 16 * a.T; o += 64) {
+        const int t = o >> 4, n0 = 16 * tile + (o & 15);
+        float sum = 0.0f;
+        for (int j = 0; j < a.topk; ++j)
+          if (sh_ids[t * a.topk + j] >= 0)
+            for (int sl = 0; sl < slices; ++sl)
+              sum += __hip_atomic_load(a.parts + ((int64_t)sl * P + t * a.topk + j) * a.H + n0, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+        a.out[(int64_t)t * a.H + n0] = __builtin_bit_cast(uint16_t, (__bf16)sum);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 namespace {
 
 int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -426,11 +916,74 @@ int64_t down_split(int64_t H) {
 
 }  // namespace
 
+namespace {
+
+// Streamed form: chunks per wavefront and wavefronts over K, and passes over it.
+struct StreamPlan {
+  int nc, waves, passes;
+};
+StreamPlan stream_plan(int64_t K) {
+  const int64_t nch = (K + kSt4Chunk - 1) / kSt4Chunk;
+  const int64_t passes = (nch + 15) / 16;
+  return StreamPlan{1, (int)((nch + passes - 1) / passes), (int)passes};
+}
+
+bool streamed(int64_t H, int64_t I) { return H % 32 == 0 && I % 32 == 0 && H >= 64 && I >= 64; }
+
+}  // namespace
+
 int64_t moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t H, int64_t I) {
   const int64_t P = T * topk, split = down_split(H);
-  return 3 * up256(P * 4) + 256 + 2 * up256(P * I * 2) + up256(H / 16 * 4) +
-         (split > 1 ? H / 16 * split * 256 * 4 : 0);
+  const int64_t parts = streamed(H, I) ? stream_plan(I).passes * P * H * 4
+                                       : (split > 1 ? H / 16 * split * 256 * 4 : 0);
+  return 3 * up256(P * 4) + 256 + up256(P * I * 4) + up256(H / 16 * 4) + parts;
 }
+
+namespace {
+
+template <int NI>
+hipError_t launch_stream_up(const MoeDecodeArgs& a, int64_t active, hipStream_t stream) {
+  const StreamPlan p = stream_plan(a.H);
+  const int dev = current_device();
+  const void* const fn = (const void*)moe_stream_up_kernel<NI, 1>;
+  int64_t lds = (int64_t)p.waves * (kMdDepth * kSt4Bytes + 2048) + 128 * md_scale_pitch(p.waves);
+  const int per_cu = std::max(1, 16 / p.waves);
+  const int64_t units = active * (a.I / 16);
+  int64_t grid = std::min<int64_t>(units, (int64_t)device_cus(dev) * std::min(per_cu, 4));
+  if (p.passes > 1) {                                     // the held sums of a workgroup's units fit beside
+    const int64_t room = std::max<int64_t>(1, (120 * 1024 / per_cu + 24 * 1024 - lds) / 2048);
+    grid = std::max<int64_t>(grid, (units + room - 1) / room);
+    lds += (units + grid - 1) / grid * 2048;
+  }
+  if (lds > 32768) {
+    const hipError_t e = ensure_dynamic_lds(fn, dev, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel_lds(fn, dim3((unsigned)grid), dim3(64 * p.waves), (size_t)lds, stream, a);
+}
+
+hipError_t launch_stream(MoeDecodeArgs a, int64_t active, hipStream_t stream) {
+  const StreamPlan p = stream_plan(a.I);
+  a.slices = p.passes;
+  a.n_counters = a.H / 16;
+  hipError_t e = a.E <= 64    ? launch_stream_up<1>(a, active, stream)
+                 : a.E <= 256 ? launch_stream_up<4>(a, active, stream)
+                              : launch_stream_up<16>(a, active, stream);
+  if (e != hipSuccess) return e;
+  const int dev = current_device();
+  const void* const fn = (const void*)moe_stream_down_kernel<1>;
+  const int64_t lds = (int64_t)p.waves * (kMdDepth * kSt4Bytes + 2048) + 128 * md_scale_pitch(p.waves);
+  const int per_cu = std::max(1, 16 / p.waves);
+  const int64_t units = active * p.passes * (a.H / 16);
+  const int64_t grid = std::min<int64_t>(units, (int64_t)device_cus(dev) * std::min(per_cu, 4));
+  if (lds > 32768) {
+    e = ensure_dynamic_lds(fn, dev, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  return launch_kernel_lds(fn, dim3((unsigned)grid), dim3(64 * p.waves), (size_t)lds, stream, a);
+}
+
+}  // namespace
 
 hipError_t launch_moe_decode(MoeDecodeArgs a, void* workspace, hipStream_t stream) {
   const int64_t P = (int64_t)a.T * a.topk;
@@ -444,15 +997,17 @@ hipError_t launch_moe_decode(MoeDecodeArgs a, void* workspace, hipStream_t strea
   a.weights = reinterpret_cast<float*>(take(P * 4));
   a.list = reinterpret_cast<int32_t*>(take(P * 4));
   a.active = reinterpret_cast<int32_t*>(take(4));
-  a.a_hi = reinterpret_cast<uint16_t*>(take(P * a.I * 2));
-  a.a_lo = reinterpret_cast<uint16_t*>(take(P * a.I * 2));
+  a.act = reinterpret_cast<float*>(take(P * a.I * 4));
+  a.a_hi = reinterpret_cast<uint16_t*>(a.act);
+  a.a_lo = a.a_hi + P * a.I;
   a.counters = reinterpret_cast<int32_t*>(take(a.H / 16 * 4));
   a.parts = reinterpret_cast<float*>(p);
+  const int64_t active = std::min<int64_t>(a.E, P), tiles = a.I / 16;   // chosen experts at most
+  if (streamed(a.H, a.I)) return launch_stream(a, active, stream);
   a.down_split = (int)down_split(a.H);
   a.n_counters = a.down_split > 1 ? a.H / 16 : 0;
-  // chosen experts at most; K split over 1, 2 or 4 wavefronts until the
-  // wavefronts fill the GPU (sixteen for each of 256 compute units)
-  const int64_t active = std::min<int64_t>(a.E, P), tiles = a.I / 16;
+  // K split over 1, 2 or 4 wavefronts until the wavefronts fill the GPU
+  // (sixteen for each of 256 compute units)
   const int64_t nch = (a.H + kMdChunk - 1) / kMdChunk;
   int splitk = 1;
   while (splitk < kMdWaves && active * tiles * splitk < 4096 && 2 * splitk <= nch) splitk *= 2;

@@ -217,8 +217,8 @@ int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk);
 hipError_t launch_logprobs(LogprobsArgs a, int dtype, int64_t M, void* workspace, hipStream_t stream);
 hipError_t launch_logprobs_backward(LogprobsBackwardArgs a, int dtype, int64_t M, hipStream_t stream);
 
-// int4 weights with group scales (int4_gemm.hip); splitk and scale_pitch are the
-// launcher's.
+// int4 weights with group scales (int4_gemm.hip); scale_pitch and
+// tiles_per_block are the launcher's.
 struct Int4Args {
   const uint16_t* x;
   const uint8_t* packed;
@@ -228,7 +228,7 @@ struct Int4Args {
   uint16_t* y;
   int32_t M, K, N, group, groups;
   int32_t scale_f16;
-  int32_t splitk, scale_pitch;
+  int32_t scale_pitch, tiles_per_block;
 };
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream);
 
@@ -257,11 +257,12 @@ struct MoeDecodeArgs {
   float* weights;
   int32_t* list;
   int32_t* active;
+  float* act;
   uint16_t* a_hi;
   uint16_t* a_lo;
   int32_t* counters;
   float* parts;
-  int32_t splitk, down_split, n_counters;
+  int32_t splitk, down_split, slices, n_counters;
 };
 int64_t moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t H, int64_t I);
 hipError_t launch_moe_decode(MoeDecodeArgs a, void* workspace, hipStream_t stream);

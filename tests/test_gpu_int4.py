@@ -110,3 +110,13 @@ def test_graph_replays():
         torch.cuda.synchronize()
         got = y.clone()
         assert torch.equal(got, B.nvfp4_int4_gemm(x, packed, scales, zp, b))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(16, 700, 5120), (3, 5000, 8192), (20, 300, 5120), (40, 600, 4352), (64, 4500, 2336),
+                                   (1, 100, 9216)])
+def test_long_rows_in_phases(m, n, k, group):
+    """K split over more wavefronts, chunks and phases than one pass holds (2336 = 9 x 256 + 32)."""
+    if k % group:
+        group = 32
+    check(m, n, k, group, group != 128, seed=m + n + k + group)

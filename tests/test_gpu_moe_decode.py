@@ -45,7 +45,10 @@ def check(T, E, topk, H, I, seed, scoring="softmax", renormalize=True, bias=None
 @pytest.mark.parametrize("T,E,topk,H,I", [
     (1, 1, 1, 16, 16), (1, 8, 2, 512, 256), (2, 8, 2, 48, 272), (3, 4, 4, 272, 48), (16, 8, 2, 1024, 512),
     (5, 64, 6, 256, 128), (4, 65, 8, 128, 64), (7, 128, 8, 304, 80), (16, 256, 8, 64, 32), (2, 300, 10, 32, 48),
-    (16, 1024, 3, 16, 16), (9, 32, 32, 64, 64), (16, 16, 16, 528, 1040), (1, 8, 2, 2048, 4096), (11, 3, 1, 4112, 256)])
+    (16, 1024, 3, 16, 16), (9, 32, 32, 64, 64), (16, 16, 16, 528, 1040), (1, 8, 2, 2048, 4096), (11, 3, 1, 4112, 256),
+    # H and I multiples of 32: rows that end inside a chunk, one to several chunks and passes over K
+    (2, 4, 2, 32, 32), (16, 8, 3, 96, 160), (5, 8, 2, 1056, 288), (3, 5, 2, 4128, 512), (2, 3, 2, 512, 4640),
+    (4, 20, 4, 64, 8224), (7, 300, 6, 288, 96), (1, 2, 1, 8224, 64)])
 def test_sizes(T, E, topk, H, I):
     check(T, E, topk, H, I, seed=T + E + topk + H + I)
 
