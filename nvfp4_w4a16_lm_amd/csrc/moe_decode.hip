@@ -523,6 +523,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
   __shared__ int32_t sh_flag[64 * NI];
   __shared__ int32_t sh_list[kMdMaxPairs];
   __shared__ int32_t sh_active;
+  __shared__ float sh_gs[kMdMaxPairs];                    // of the chosen experts: no load in the loop but the stream's
   constexpr int D = kMdDepth;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int W = blockDim.x >> 6;
@@ -537,14 +538,41 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
   float* const held = reinterpret_cast<float*>(scl + 32 * spitch);                       // [units][512], several phases
 
   const int active = route_all<NI>(a, sh_ids, sh_w, sh_flag, sh_list, &sh_active);
+  for (int s = tid; s < active; s += blockDim.x) sh_gs[s] = a.w13_gs[sh_list[s]];
   const int tiles = a.I >> 4, units = active * tiles;
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   if (u0 >= u1) return;
   const int s0 = 2 * u0, s1 = 2 * u1;                     // steps: tile 2 u is gate, 2 u + 1 is up
-  // first weight row of step s's tile
-  auto row_of = [&](int s) {
-    const int u = s >> 1, slot = u / tiles;
-    return (int64_t)sh_list[slot] * 2 * a.I + (s & 1) * a.I + 16 * (u - slot * tiles);
+  // where the stream stands: a step, its unit's expert and tile, the tile's first
+  // row; kept by counting (divisions and LDS reads only where the expert changes)
+  struct Pos {
+    int s, slot, tile;
+    int64_t row;
+  };
+  auto set_row = [&](Pos& p) {
+    const int e = __builtin_amdgcn_readfirstlane(sh_list[p.slot]);
+    p.row = (int64_t)e * 2 * a.I + (p.s & 1 ? a.I : 0) + 16 * p.tile;
+  };
+  auto pos_of = [&](int s) {
+    Pos p;
+    p.s = s;
+    p.slot = (s >> 1) / tiles;
+    p.tile = (s >> 1) - p.slot * tiles;
+    set_row(p);
+    return p;
+  };
+  auto advance = [&](Pos& p) {                            // stays at the last step
+    if (p.s + 1 >= s1) return;
+    ++p.s;
+    if (p.s & 1) {
+      p.row += a.I;
+    } else if (++p.tile < tiles) {
+      p.row += 16 - (int64_t)a.I;
+    } else {
+      p.tile = 0;
+      ++p.slot;
+      set_row(p);
+    }
   };
 
   for (int ph = 0; ph < phases; ++ph) {
@@ -557,8 +585,8 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       sword[i] = it - srow[i] * words;
     }
     uint32_t sv[D][NC];
-    auto load_scales = [&](int s, int slot) {
-      const uint8_t* const base = a.w13_scales + row_of(min(s, s1 - 1)) * nb;
+    auto load_scales = [&](const Pos& p, int slot) {
+      const uint8_t* const base = a.w13_scales + p.row * nb;
 #pragma unroll
       for (int i = 0; i < NC; ++i)
         sv[slot][i] = load_scale_word(base + (int64_t)srow[i] * nb, 4 * ph * W * NC + sword[i], nb);
@@ -567,18 +595,21 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) scl[((s & 1) * 16 + srow[i]) * spitch + sword[i]] = sv[slot][i];
     };
-    auto copy_tile = [&](int s, int slot) {
-      const uint8_t* const base = a.w13_packed + row_of(min(s, s1 - 1)) * pitch;
+    auto copy_tile = [&](const Pos& p, int slot) {
+      const uint8_t* const base = a.w13_packed + p.row * pitch;
 #pragma unroll
       for (int q = 0; q < NC; ++q) st4_copy(base, pitch, 15, c0 + q, ring + (slot * NC + q) * kSt4Bytes, lane);
     };
     // the scales travel one tile ahead of the copies (see int4_gemm.hip)
-    load_scales(s0, 0);
+    Pos next = pos_of(s0);                                // the step whose scales are fetched next
+    load_scales(next, 0);
     store_scales(s0, 0);
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      load_scales(s0 + d + 1, d);
-      copy_tile(s0 + d, d);
+      const Pos here = next;
+      advance(next);
+      load_scales(next, d);
+      copy_tile(here, d);
     }
     // activations: column r is token r
     f16x8 xb[NC][8];
@@ -629,8 +660,10 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       __builtin_amdgcn_s_waitcnt(kSt4Lgkm0);
       __asm__ volatile("" ::: "memory");
       store_scales(s + 1, slot);
-      load_scales(s + D + 1, slot);
-      copy_tile(s + D, slot);
+      const Pos here = next;
+      advance(next);
+      load_scales(next, slot);
+      copy_tile(here, slot);
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int q = 0; q < NC; ++q) acc = chunk_product(w[q][0], w[q][1], sw[q], xb[q], acc);
@@ -647,10 +680,18 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       st4_barrier();
     };
     // the unit's sums: element 4 l + v is lane l's v: token l % 16, column 4 (l / 16) + v of the tile
+    int fslot = s0 / 2 / tiles, ftile = s0 / 2 - fslot * tiles, pair = -2;
     auto finish = [&](int u) {
-      const int slot = u / tiles, e = sh_list[slot];
+      // this thread's token keeps its pair while the expert stays (threads i and i + 64 k have one token)
+      if (pair == -2) {
+        pair = -1;
+        const int t = (tid >> 2) & 15, e = sh_list[fslot];
+        if (t < a.T)
+          for (int j = 0; j < a.topk; ++j)
+            if (sh_ids[t * a.topk + j] == e) pair = t * a.topk + j;
+      }
       for (int i = tid; i < 256; i += blockDim.x) {
-        const int t = (i >> 2) & 15, n = 4 * (i >> 6) + (i & 3);
+        const int n = 4 * (i >> 6) + (i & 3);
         float sum[2] = {0.0f, 0.0f};
         for (int v = 0; v < W; v += 4) {
           float q[4][2];
@@ -677,14 +718,15 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
             continue;
           }
         }
-        if (t >= a.T) continue;
-        int pair = -1;
-        for (int j = 0; j < a.topk; ++j)
-          if (sh_ids[t * a.topk + j] == e) pair = t * a.topk + j;
         if (pair < 0) continue;
-        const float gs = a.w13_gs[e];
+        const float gs = sh_gs[fslot];
         const float gv = sum[0] * gs, uv = sum[1] * gs;
-        a.act[(int64_t)pair * a.I + 16 * (u - slot * tiles) + n] = gv / (1.0f + expf(-gv)) * uv;
+        a.act[(int64_t)pair * a.I + 16 * ftile + n] = gv / (1.0f + expf(-gv)) * uv;
+      }
+      if (++ftile == tiles) {
+        ftile = 0;
+        ++fslot;
+        pair = -2;
       }
     };
     // two steps a unit, D in flight: the pattern repeats every 2 D steps
@@ -740,11 +782,35 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     return;
   }
   if (u0 >= u1) return;
-  auto row_of = [&](int u) {                               // first weight row of a unit's tile
-    const int c = u / tiles;
-    return (int64_t)sh_list[c / slices] * a.H + 16 * (u - c * tiles);
+  // where the stream stands (see the up kernel); combo = (expert slot, slice)
+  struct Pos {
+    int u, combo, slice, tile;
+    int64_t row;
   };
-  auto slice_of = [&](int u) { return (u / tiles) % slices; };
+  auto set_row = [&](Pos& p) {
+    const int slot = p.combo / slices;
+    p.slice = p.combo - slot * slices;
+    p.row = (int64_t)__builtin_amdgcn_readfirstlane(sh_list[slot]) * a.H + 16 * p.tile;
+  };
+  auto pos_of = [&](int u) {
+    Pos p;
+    p.u = u;
+    p.combo = u / tiles;
+    p.tile = u - p.combo * tiles;
+    set_row(p);
+    return p;
+  };
+  auto advance = [&](Pos& p) {
+    if (p.u + 1 >= u1) return;
+    ++p.u;
+    if (++p.tile < tiles) {
+      p.row += 16;
+    } else {
+      p.tile = 0;
+      ++p.combo;
+      set_row(p);
+    }
+  };
   const int words = 4 * W * NC;
   int srow[NC], sword[NC];
 #pragma unroll
@@ -754,44 +820,50 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     sword[i] = it - srow[i] * words;
   }
   uint32_t sv[D][NC];
-  auto load_scales = [&](int u, int slot) {
-    const int uc = min(u, u1 - 1);
-    const uint8_t* const base = a.w2_scales + row_of(uc) * nb;
+  auto load_scales = [&](const Pos& p, int slot) {
+    const uint8_t* const base = a.w2_scales + p.row * nb;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      sv[slot][i] = load_scale_word(base + (int64_t)srow[i] * nb, words * slice_of(uc) + sword[i], nb);
+      sv[slot][i] = load_scale_word(base + (int64_t)srow[i] * nb, words * p.slice + sword[i], nb);
   };
   auto store_scales = [&](int u, int slot) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) scl[((u & 1) * 16 + srow[i]) * spitch + sword[i]] = sv[slot][i];
   };
-  auto copy_tile = [&](int u, int slot) {
-    const int uc = min(u, u1 - 1);
-    const uint8_t* const base = a.w2_packed + row_of(uc) * pitch;
+  auto copy_tile = [&](const Pos& p, int slot) {
+    const uint8_t* const base = a.w2_packed + p.row * pitch;
 #pragma unroll
     for (int q = 0; q < NC; ++q)
-      st4_copy(base, pitch, 15, (slice_of(uc) * W + wave) * NC + q, ring + (slot * NC + q) * kSt4Bytes, lane);
+      st4_copy(base, pitch, 15, (p.slice * W + wave) * NC + q, ring + (slot * NC + q) * kSt4Bytes, lane);
   };
-  load_scales(u0, 0);
+  Pos next = pos_of(u0), now = next;                       // fetched next; computed now
+  load_scales(next, 0);
   store_scales(u0, 0);
 #pragma unroll
   for (int d = 0; d < D; ++d) {
-    load_scales(u0 + d + 1, d);
-    copy_tile(u0 + d, d);
+    const Pos here = next;
+    advance(next);
+    load_scales(next, d);
+    copy_tile(here, d);
   }
   st4_barrier();
 
   f16x8 xb[NC][8];
   float back = 0.0f;
-  int combo = -1, pair = -1;
+  int combo = -1, out_pair = -1;                           // out_pair: of this thread's token in the sums
   // the activations of (expert, slice) c: column r is token r's pair with the expert, or zeros
-  auto load_act = [&](int c) {
-    combo = c;
-    const int e = sh_list[c / slices], c0 = ((c % slices) * W + wave) * NC;
-    pair = -1;
+  auto load_act = [&](const Pos& at) {
+    combo = at.combo;
+    const int e = sh_list[at.combo / slices], c0 = (at.slice * W + wave) * NC;
+    int pair = -1;
+    out_pair = -1;
     if (r < a.T)
       for (int j = 0; j < a.topk; ++j)
         if (sh_ids[r * a.topk + j] == e) pair = r * a.topk + j;
+    const int ot = (tid >> 2) & 15;
+    if (ot < a.T)
+      for (int j = 0; j < a.topk; ++j)
+        if (sh_ids[ot * a.topk + j] == e) out_pair = ot * a.topk + j;
     const float* const row = a.act + (int64_t)max(pair, 0) * K;
     uint32_t mag = 0;
     float f[NC][8][8];
@@ -822,8 +894,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
   };
 
   auto step = [&](int u, int slot) {
-    const int c = u / tiles;
-    if (c != combo) load_act(c);                           // uniform over the workgroup
+    if (now.combo != combo) load_act(now);                 // uniform over the workgroup
     __builtin_amdgcn_s_waitcnt(st4_vm((D - 1) * 3 * NC));
     __asm__ volatile("" ::: "memory");
     u32x4 w[NC][2];
@@ -837,8 +908,10 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     __builtin_amdgcn_s_waitcnt(kSt4Lgkm0);
     __asm__ volatile("" ::: "memory");
     store_scales(u + 1, slot);
-    load_scales(u + D + 1, slot);
-    copy_tile(u + D, slot);
+    const Pos here = next;
+    advance(next);
+    load_scales(next, slot);
+    copy_tile(here, slot);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < NC; ++q) acc = chunk_product(w[q][0], w[q][1], sw[q], xb[q], acc);
@@ -847,8 +920,8 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     *reinterpret_cast<f32x4*>(red + ((u & 1) * W + wave) * 256 + 4 * lane) = acc;
     st4_barrier();
     for (int i = tid; i < 256; i += blockDim.x) {
-      const int t = (i >> 2) & 15, n = 4 * (i >> 6) + (i & 3);
-      if (t >= a.T) continue;
+      if (out_pair < 0) break;                             // threads i and i + 64 k have one token
+      const int n = 4 * (i >> 6) + (i & 3);
       const float* const part = red + (u & 1) * W * 256 + i;
       float sum = 0.0f;
       for (int v = 0; v < W; v += 4) {
@@ -858,14 +931,10 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
 #pragma unroll
         for (int b = 0; b < 4; ++b) sum += v + b < W ? q[b] : 0.0f;
       }
-      const int e = sh_list[c / slices];
-      int p = -1;
-      for (int j = 0; j < a.topk; ++j)
-        if (sh_ids[t * a.topk + j] == e) p = t * a.topk + j;
-      if (p >= 0)
-        __hip_atomic_store(a.parts + ((int64_t)(c % slices) * P + p) * a.H + 16 * (u - c * tiles) + n, sum,
-                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(a.parts + ((int64_t)now.slice * P + out_pair) * a.H + 16 * now.tile + n, sum,
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    advance(now);
   };
   for (int u = u0; u < u1; u += D) {
 #pragma unroll
