@@ -537,6 +537,41 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
   uint32_t* const scl = reinterpret_cast<uint32_t*>(red + W * 512);                      // [2][16][spitch]
   float* const held = reinterpret_cast<float*>(scl + 32 * spitch);                       // [units][512], several phases
 
+  // activations of the wavefront's chunks: column r is token r (the first ones
+  // before the routing, whose latency covers theirs)
+  f16x8 xb[NC][8];
+  float back;
+  auto load_tokens = [&](int c0) {
+    u32x4 xv[NC][8];
+    uint32_t mag = 0;
+    const uint16_t* const xrow = a.x + (int64_t)min(r, a.T - 1) * K;
+#pragma unroll
+    for (int q = 0; q < NC; ++q) {
+      load_x(xrow, true, c0 + q, g, K, xv[q]);
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mag = pk_max_u16(mag, xv[q][s][e] & 0x7FFF7FFFu);
+    }
+    mag = max(mag & 0xFFFFu, mag >> 16) << 16;
+    const int p = scale_exponent(column_max(mag));
+    back = pow2(p);
+    const float down = pow2(-p);
+#pragma unroll
+    for (int q = 0; q < NC; ++q)
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = xv[q][s][e];
+          f[2 * e] = bf16_lo(w);
+          f[2 * e + 1] = bf16_hi(w);
+        }
+        xb[q][s] = pack_f16(f, down);
+      }
+  };
+  load_tokens(wave * NC);
   const int active = route_all<NI>(a, sh_ids, sh_w, sh_flag, sh_list, &sh_active);
   for (int s = tid; s < active; s += blockDim.x) sh_gs[s] = a.w13_gs[sh_list[s]];
   const int tiles = a.I >> 4, units = active * tiles;
@@ -611,38 +646,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       load_scales(next, d);
       copy_tile(here, d);
     }
-    // activations: column r is token r
-    f16x8 xb[NC][8];
-    float back;
-    {
-      u32x4 xv[NC][8];
-      uint32_t mag = 0;
-      const uint16_t* const xrow = a.x + (int64_t)min(r, a.T - 1) * K;
-#pragma unroll
-      for (int q = 0; q < NC; ++q) {
-        load_x(xrow, true, c0 + q, g, K, xv[q]);
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mag = pk_max_u16(mag, xv[q][s][e] & 0x7FFF7FFFu);
-      }
-      mag = max(mag & 0xFFFFu, mag >> 16) << 16;
-      const int p = scale_exponent(column_max(mag));
-      back = pow2(p);
-      const float down = pow2(-p);
-#pragma unroll
-      for (int q = 0; q < NC; ++q)
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[2 * e] = bf16_lo(xv[q][s][e]);
-            f[2 * e + 1] = bf16_hi(xv[q][s][e]);
-          }
-          xb[q][s] = pack_f16(f, down);
-        }
-    }
+    if (ph > 0) load_tokens(c0);
     st4_barrier();
 
     f32x4 gate;
@@ -955,19 +959,34 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
       sh_done[i] = before + 1 == active * slices ? tile : -1;
     }
     __syncthreads();
-    for (int i = wave; i < n; i += W) {
-      const int tile = sh_done[i];
+    // the complete tiles' outputs, two columns a thread, read past the caches as
+    // they were written (a fence that empties the caches instead: 20 us more)
+    const int halves = 8 * a.T, terms = a.topk * slices;
+    for (int o = tid; o < n * halves; o += blockDim.x) {
+      const int i = o / halves, q = o - i * halves, t = q >> 3, tile = sh_done[i];
       if (tile < 0) continue;
-      for (int o = lane; o < 16 * a.T; o += 64) {
-        const int t = o >> 4, n0 = 16 * tile + (o & 15);
-        float sum = 0.0f;
-        for (int j = 0; j < a.topk; ++j)
-          if (sh_ids[t * a.topk + j] >= 0)
-            for (int sl = 0; sl < slices; ++sl)
-              sum += __hip_atomic_load(a.parts + ((int64_t)sl * P + t * a.topk + j) * a.H + n0, __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-        a.out[(int64_t)t * a.H + n0] = __builtin_bit_cast(uint16_t, (__bf16)sum);
+      const int n0 = 16 * tile + 2 * (q & 7);
+      float sum[2] = {0.0f, 0.0f};
+      for (int c = 0; c < terms; c += 8) {                // eight loads at a time, added in order
+        uint64_t v[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const int k = min(c + b, terms - 1), j = k / slices, p = t * a.topk + j;
+          v[b] = __hip_atomic_load(
+              reinterpret_cast<const uint64_t*>(a.parts + ((int64_t)(k - j * slices) * P + p) * a.H + n0),
+              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const int k = min(c + b, terms - 1);
+          if (c + b < terms && sh_ids[t * a.topk + k / slices] >= 0) {
+            sum[0] += __uint_as_float((uint32_t)v[b]);
+            sum[1] += __uint_as_float((uint32_t)(v[b] >> 32));
+          }
+        }
       }
+      *reinterpret_cast<uint32_t*>(a.out + (int64_t)t * a.H + n0) =
+          __builtin_bit_cast(uint32_t, bf16x2{(__bf16)sum[0], (__bf16)sum[1]});
     }
     __syncthreads();
   }
