@@ -128,7 +128,7 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
       scol[i] = it - srow[i] * gn;
     }
     // loads are unconditional (clamped): a branch would make the compiler wait
-    uint32_t sv[D][SI], zv[D][SI];
+    uint32_t sv[D + 1][SI], zv[D + 1][SI];              // the last entry: the first tile's
     auto load_scales = [&](int t, int slot) {
       const int last = min(15, N - 1 - 16 * t);
 #pragma unroll
@@ -159,13 +159,13 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
     // the scales travel one tile ahead of the copies, so that the wait for a
     // tile's copies covers the next tile's scales
     if (t0 < t1) {
-      load_scales(t0, 0);
-      store_scales(t0, 0);
+      load_scales(t0, D);
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         load_scales(min(t0 + d + 1, t1 - 1), d);
         copy_tile(t0 + d, d);
       }
+      store_scales(t0, D);
     }
     // x fragments, in the order of the codes: MFMA step s of sub-chunk h (128 k)
     // is k = 32 s + 8 g + [0, 8), or k = 32 g + 8 s + [0, 8) where the whole

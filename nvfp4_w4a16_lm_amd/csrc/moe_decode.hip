@@ -505,7 +505,7 @@ __device__ __forceinline__ f32x4 chunk_product(u32x4 w0, u32x4 w1, uint32_t sw, 
   return acc;
 }
 
-constexpr int kMdDepth = 3;                  // tiles in flight per wavefront
+constexpr int kMdDepth = 2;                  // tiles in flight per wavefront
 
 // LDS words of a row's scales for W wavefronts of NC chunks, padded to spread the rows.
 __device__ __host__ constexpr int md_scale_pitch(int slots) { return 4 * slots + 1; }
@@ -515,7 +515,7 @@ __device__ __host__ constexpr int md_scale_pitch(int slots) { return 4 * slots +
 // Up: a[pair, i] = silu(gate) * up, float32.  Units (expert, 16 columns of I) are
 // dealt to the workgroups in contiguous runs; each is two tiles, the gate's and
 // the up's.
-template <int NI, int NC>
+template <int NI, int NC, bool PASSES>
 __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
   __shared__ int32_t sh_ids[kMdMaxPairs];
@@ -530,7 +530,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
   const int r = lane & 15, g = lane >> 4;
   const int K = a.H, nb = K >> 4, nch = (K + kSt4Chunk - 1) / kSt4Chunk;
   const int64_t pitch = K >> 1;
-  const int phases = (nch + W * NC - 1) / (W * NC);
+  const int phases = PASSES ? (nch + W * NC - 1) / (W * NC) : 1;
   uint8_t* const ring = lds8 + wave * (D * NC * kSt4Bytes);
   float* const red = reinterpret_cast<float*>(lds8 + W * (D * NC * kSt4Bytes));          // [W][2][256]
   const int spitch = md_scale_pitch(W * NC);
@@ -573,7 +573,6 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
   };
   load_tokens(wave * NC);
   const int active = route_all<NI>(a, sh_ids, sh_w, sh_flag, sh_list, &sh_active);
-  for (int s = tid; s < active; s += blockDim.x) sh_gs[s] = a.w13_gs[sh_list[s]];
   const int tiles = a.I >> 4, units = active * tiles;
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
   if (u0 >= u1) return;
@@ -619,7 +618,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       srow[i] = it / words;
       sword[i] = it - srow[i] * words;
     }
-    uint32_t sv[D][NC];
+    uint32_t sv[D + 1][NC];                               // the last entry: the first step's
     auto load_scales = [&](const Pos& p, int slot) {
       const uint8_t* const base = a.w13_scales + p.row * nb;
 #pragma unroll
@@ -637,8 +636,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
     };
     // the scales travel one tile ahead of the copies (see int4_gemm.hip)
     Pos next = pos_of(s0);                                // the step whose scales are fetched next
-    load_scales(next, 0);
-    store_scales(s0, 0);
+    load_scales(next, D);
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       const Pos here = next;
@@ -646,7 +644,11 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       load_scales(next, d);
       copy_tile(here, d);
     }
-    if (ph > 0) load_tokens(c0);
+    store_scales(s0, D);
+    if (PASSES && ph > 0)
+      load_tokens(c0);
+    else
+      for (int s = tid; s < active; s += blockDim.x) sh_gs[s] = a.w13_gs[sh_list[s]];
     st4_barrier();
 
     f32x4 gate;
@@ -710,7 +712,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
             sum[1] += v + b < W ? q[b][1] : 0.0f;
           }
         }
-        if (phases > 1) {
+        if (PASSES) {
           float* const h = held + (u - u0) * 512 + i;
           if (ph > 0) {
             sum[0] += h[0];
@@ -733,16 +735,11 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
         pair = -2;
       }
     };
-    // two steps a unit, D in flight: the pattern repeats every 2 D steps
-    for (int s = s0; s < s1; s += 2 * D) {
-#pragma unroll
-      for (int d = 0; d < 2 * D; d += 2) {
-        if (s + d < s1) {
-          step(s + d, d % D);
-          step(s + d + 1, (d + 1) % D);
-          finish((s + d) >> 1);
-        }
-      }
+    static_assert(D == 2, "two steps a unit and two tiles in flight");
+    for (int s = s0; s < s1; s += 2) {
+      step(s, 0);
+      step(s + 1, 1);
+      finish(s >> 1);
     }
     __builtin_amdgcn_s_waitcnt(st4_vm(0));
     __syncthreads();
@@ -772,11 +769,11 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
   uint32_t* const scl = reinterpret_cast<uint32_t*>(red + 2 * W * 256);                  // [2][16][spitch]
 
   const int active = *a.active, slices = a.slices, tiles = a.H >> 4;
-  for (int p = tid; p < P; p += blockDim.x) {
+  for (int p = tid; p < P; p += blockDim.x) {             // of the list, the first `active` hold experts
     sh_ids[p] = a.ids[p];
     sh_w[p] = a.weights[p];
+    sh_list[p] = a.list[p];
   }
-  for (int s = tid; s < active; s += blockDim.x) sh_list[s] = a.list[s];
   __syncthreads();
   const int units = active * slices * tiles;
   const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
@@ -823,7 +820,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     srow[i] = it / words;
     sword[i] = it - srow[i] * words;
   }
-  uint32_t sv[D][NC];
+  uint32_t sv[D + 1][NC];                                 // the last entry: the first unit's
   auto load_scales = [&](const Pos& p, int slot) {
     const uint8_t* const base = a.w2_scales + p.row * nb;
 #pragma unroll
@@ -841,8 +838,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
       st4_copy(base, pitch, 15, (p.slice * W + wave) * NC + q, ring + (slot * NC + q) * kSt4Bytes, lane);
   };
   Pos next = pos_of(u0), now = next;                       // fetched next; computed now
-  load_scales(next, 0);
-  store_scales(u0, 0);
+  load_scales(next, D);
 #pragma unroll
   for (int d = 0; d < D; ++d) {
     const Pos here = next;
@@ -850,6 +846,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     load_scales(next, d);
     copy_tile(here, d);
   }
+  store_scales(u0, D);
   st4_barrier();
 
   f16x8 xb[NC][8];
@@ -1033,20 +1030,20 @@ template <int NI>
 hipError_t launch_stream_up(const MoeDecodeArgs& a, int64_t active, hipStream_t stream) {
   const StreamPlan p = stream_plan(a.H);
   const int dev = current_device();
-  const void* const fn = (const void*)moe_stream_up_kernel<NI, 1>;
+  const void* const fn = p.passes > 1 ? (const void*)moe_stream_up_kernel<NI, 1, true>
+                                      : (const void*)moe_stream_up_kernel<NI, 1, false>;
   int64_t lds = (int64_t)p.waves * (kMdDepth * kSt4Bytes + 2048) + 128 * md_scale_pitch(p.waves);
-  const int per_cu = std::max(1, 16 / p.waves);
   const int64_t units = active * (a.I / 16);
-  int64_t grid = std::min<int64_t>(units, (int64_t)device_cus(dev) * std::min(per_cu, 4));
-  if (p.passes > 1) {                                     // the held sums of a workgroup's units fit beside
-    const int64_t room = std::max<int64_t>(1, (120 * 1024 / per_cu + 24 * 1024 - lds) / 2048);
-    grid = std::max<int64_t>(grid, (units + room - 1) / room);
+  int64_t grid;
+  if (p.passes > 1) {                                     // one workgroup a compute unit; its units' held sums fit beside
+    const int64_t room = std::max<int64_t>(1, (144 * 1024 - lds) / 2048);
+    grid = std::max<int64_t>(std::min<int64_t>(units, device_cus(dev)), (units + room - 1) / room);
     lds += (units + grid - 1) / grid * 2048;
   }
-  if (lds > 32768) {
-    const hipError_t e = ensure_dynamic_lds(fn, dev, (int)lds);
-    if (e != hipSuccess) return e;
-  }
+  const hipError_t e = ensure_dynamic_lds(fn, dev, (int)lds);
+  if (e != hipSuccess) return e;
+  if (p.passes == 1)
+    grid = std::min<int64_t>(units, (int64_t)device_cus(dev) * blocks_per_cu(fn, dev, 64 * p.waves, (size_t)lds));
   return launch_kernel_lds(fn, dim3((unsigned)grid), dim3(64 * p.waves), (size_t)lds, stream, a);
 }
 
@@ -1061,13 +1058,11 @@ hipError_t launch_stream(MoeDecodeArgs a, int64_t active, hipStream_t stream) {
   const int dev = current_device();
   const void* const fn = (const void*)moe_stream_down_kernel<1>;
   const int64_t lds = (int64_t)p.waves * (kMdDepth * kSt4Bytes + 2048) + 128 * md_scale_pitch(p.waves);
-  const int per_cu = std::max(1, 16 / p.waves);
+  e = ensure_dynamic_lds(fn, dev, (int)lds);
+  if (e != hipSuccess) return e;
   const int64_t units = active * p.passes * (a.H / 16);
-  const int64_t grid = std::min<int64_t>(units, (int64_t)device_cus(dev) * std::min(per_cu, 4));
-  if (lds > 32768) {
-    e = ensure_dynamic_lds(fn, dev, (int)lds);
-    if (e != hipSuccess) return e;
-  }
+  const int64_t grid =
+      std::min<int64_t>(units, (int64_t)device_cus(dev) * blocks_per_cu(fn, dev, 64 * p.waves, (size_t)lds));
   return launch_kernel_lds(fn, dim3((unsigned)grid), dim3(64 * p.waves), (size_t)lds, stream, a);
 }
 
