@@ -14,8 +14,12 @@
 // lane, sorted, key = (order-preserving image of the logit, ~index), so equal
 // logits order by the lower index and every comparison is exact.  A group of
 // 16 logits per lane is only looked at when some lane's maximum reaches the
-// k-th best so far.  Lists of two wavefronts or segments merge by a bitonic
-// step: max(a[i], b[63 - i]), then six compare-exchanges.
+// bound so far; when many do, a bisection over the lanes' maxima raises the
+// bound first (of 128 maxima about as many logits pass as are wanted).  What
+// passes is appended to a buffer that is sorted when it fills (one insertion at
+// a time into a sorted register list instead: 333 x 32003 with 64 alternatives
+// 123 us).  Lists of two wavefronts or segments merge by a bitonic step:
+// max(a[i], b[63 - i]), then six compare-exchanges.
 //
 // With few rows a row is split into segments, one workgroup each; a second
 // kernel joins the segments' sums, counts and lists in segment order (no
@@ -51,7 +55,7 @@ struct __attribute__((packed, aligned(4))) Vec16A4 { u32x4 v; };
 
 template <int DT> struct Elem;
 template <> struct Elem<kBf16> {
-  static constexpr int kBytes = 2, kPerVec = 8;
+  static constexpr int kBytes = 2, kPerVec = 8, kLowBits = 16;   // image bits below are alike
   static constexpr uint32_t kNegInf = 0xFF80FF80u;
   static __device__ __forceinline__ u32x4 load(const uint8_t* p) { return reinterpret_cast<const Vec16A2*>(p)->v; }
   static __device__ __forceinline__ void store(uint8_t* p, u32x4 v) { reinterpret_cast<Vec16A2*>(p)->v = v; }
@@ -72,7 +76,7 @@ template <> struct Elem<kBf16> {
   }
 };
 template <> struct Elem<kF16> {
-  static constexpr int kBytes = 2, kPerVec = 8;
+  static constexpr int kBytes = 2, kPerVec = 8, kLowBits = 13;
   static constexpr uint32_t kNegInf = 0xFC00FC00u;
   static __device__ __forceinline__ u32x4 load(const uint8_t* p) { return reinterpret_cast<const Vec16A2*>(p)->v; }
   static __device__ __forceinline__ void store(uint8_t* p, u32x4 v) { reinterpret_cast<Vec16A2*>(p)->v = v; }
@@ -96,7 +100,7 @@ template <> struct Elem<kF16> {
   }
 };
 template <> struct Elem<kF32> {
-  static constexpr int kBytes = 4, kPerVec = 4;
+  static constexpr int kBytes = 4, kPerVec = 4, kLowBits = 0;
   static constexpr uint32_t kNegInf = 0xFF800000u;
   static __device__ __forceinline__ u32x4 load(const uint8_t* p) { return reinterpret_cast<const Vec16A4*>(p)->v; }
   static __device__ __forceinline__ void store(uint8_t* p, u32x4 v) { reinterpret_cast<Vec16A4*>(p)->v = v; }
@@ -156,17 +160,22 @@ __device__ __forceinline__ float key_value(uint32_t h) {
   return __uint_as_float((h >> 31) ? (h & 0x7FFFFFFFu) : ~h);
 }
 
-// Insert the (wavefront-uniform) key c; the last lane's key falls out.
-__device__ __forceinline__ void list_insert(Key& k, Key c, int lane) {
-  const bool ahead = key_gt(k, c);
-  const int pos = __popcll(__ballot(ahead));
-  Key up;
-  up.hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)k.hi, 0x138, 0xF, 0xF, false);   // wave_shr:1
-  up.lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)k.lo, 0x138, 0xF, 0xF, false);
-  if (!ahead) {
-    k.hi = lane == pos ? c.hi : up.hi;
-    k.lo = lane == pos ? c.lo : up.lo;
+__device__ __forceinline__ Key key_xor(Key k, int d) {
+  return Key{(uint32_t)__shfl_xor((int)k.hi, d, 64), (uint32_t)__shfl_xor((int)k.lo, d, 64)};
+}
+
+// 64 keys in any order, one per lane -> sorted, best first (bitonic).
+__device__ __forceinline__ Key list_sort(Key k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 64; size <<= 1) {
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const Key o = key_xor(k, d);
+      const bool keep_max = ((lane & d) == 0) == ((lane & size) == 0);
+      if (key_gt(o, k) == keep_max) k = o;
+    }
   }
+  return k;
 }
 
 // Best 64 of two sorted lists, sorted.
@@ -177,14 +186,48 @@ __device__ __forceinline__ Key list_merge(Key a, Key b, int lane) {
   Key k = key_gt(a, r) ? a : r;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
-    Key o;
-    o.hi = (uint32_t)__shfl_xor((int)k.hi, d, 64);
-    o.lo = (uint32_t)__shfl_xor((int)k.lo, d, 64);
+    const Key o = key_xor(k, d);
     const bool keep_max = (lane & d) == 0;
     if (key_gt(o, k) == keep_max) k = o;
   }
   return k;
 }
+
+// A lower bound of the k-th best of the wavefront's logits: the largest T (its
+// bits below `low` zero) that at least k of the 128 images a, b (two per lane,
+// each the best of some of the lane's logits) reach; 0 if fewer than k are real.
+__device__ __forceinline__ uint32_t kth_bound(uint32_t a, uint32_t b, int k, int low) {
+  uint32_t t = 0;
+  for (int bit = 31; bit >= low; --bit) {
+    const uint32_t up = t | (1u << bit);
+    if (__popcll(__ballot(a >= up)) + __popcll(__ballot(b >= up)) >= k) t = up;
+  }
+  return t;
+}
+
+// Candidates of a wavefront for its best k: at most 256 keys in LDS, in any
+// order, and the value below which a logit need not be looked at.
+struct Candidates {
+  Key* keys;
+  int count;
+  float thr;
+
+  // Keep the best k of them, sorted, and raise thr to the k-th.
+  __device__ __forceinline__ Key compact(int k, int lane) {
+    Key best = {0u, 0u};
+    for (int c = 0; c < count; c += 64) {
+      Key o = {0u, 0u};
+      if (c + lane < count) o = keys[c + lane];
+      o = list_sort(o, lane);
+      best = c == 0 ? o : list_merge(best, o, lane);
+    }
+    const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)best.hi, k - 1);
+    count = min(count, k);
+    if (lane < k) keys[lane] = best;                     // the wavefront's own LDS: in order
+    if (kth != 0) thr = fmaxf(thr, key_value(kth));
+    return lane < k ? best : Key{0u, 0u};
+  }
+};
 
 // Softmax sums of a set of logits.
 struct Sums {
@@ -320,7 +363,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
   constexpr int VE = E::kPerVec, U = kGroup16 / VE;
   __shared__ Sums sh_sums[kLpWaves];
   __shared__ int sh_larger[kLpWaves];
-  __shared__ Key sh_keys[kLpWaves][64];
+  __shared__ Key sh_keys[kLpWaves][256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t i = blockIdx.x / a.segs;
   const int seg = (int)(blockIdx.x - i * a.segs);
@@ -336,9 +379,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
 
   float m2 = kM2Init, s = 0.0f, t = 0.0f, raw = -INFINITY;
   int larger = 0;
-  Key key = {0u, 0u}, kth = {0u, 0u};
-  float thr = kLowest;                                   // logits below it cannot enter the list
   const int kk = a.topk;
+  Candidates cand = {sh_keys[wave], 0, kLowest};         // -inf and NaN never pass
 
   auto load = [&](int v) -> u32x4 {
     if (v < min(v1, full)) return E::load(row + (int64_t)v * 16);
@@ -367,9 +409,13 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
         for (int e = 0; e < VE; ++e) f[VE * u + e] = ((w >> e) & 1u) ? f[VE * u + e] : -INFINITY;
       }
     }
-    float g = f[0];
+    float ga = f[0], gb = f[kGroup16 / 2];
 #pragma unroll
-    for (int e = 1; e < kGroup16; ++e) g = fmaxf(g, f[e]);
+    for (int e = 1; e < kGroup16 / 2; ++e) {
+      ga = fmaxf(ga, f[e]);
+      gb = fmaxf(gb, f[kGroup16 / 2 + e]);
+    }
+    const float g = fmaxf(ga, gb);
     raw = fmaxf(raw, g);
     const float top = g * c;
     if (top > m2) rescale(m2, s, t, top);
@@ -381,25 +427,28 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
       t = __builtin_fmaf(p, fmaxf(y, -1000.0f), t);      // 2^y is 0 there; a NaN stays in s
       larger += __popcll(__ballot(f[e] > xt));
     }
-    if (kk > 0 && __ballot(g >= thr) != 0) {
+    if (kk > 0 && __ballot(g >= cand.thr) != 0) {
+      const float before = cand.thr;
+      if (__popcll(__ballot(ga >= before)) + __popcll(__ballot(gb >= before)) > kk) {
+        const uint32_t t = kth_bound(ga > -INFINITY ? key_image(ga) : 0u, gb > -INFINITY ? key_image(gb) : 0u, kk,
+                                     E::kLowBits);
+        if (t > key_image(before)) cand.thr = key_value(t);
+      }
 #pragma unroll
       for (int e = 0; e < kGroup16; ++e) {
-        const int j = (vb + kLpThreads * (e / VE) + tid) * VE + e % VE;
-        const Key mine = {key_image(f[e]), ~(uint32_t)j};
-        uint64_t todo = __ballot(f[e] >= thr && key_gt(mine, kth));
-        while (todo != 0) {
-          const int src = __ffsll((unsigned long long)todo) - 1;
-          todo &= todo - 1;
-          Key cand;
-          cand.hi = (uint32_t)__builtin_amdgcn_readlane((int)mine.hi, src);
-          cand.lo = (uint32_t)__builtin_amdgcn_readlane((int)mine.lo, src);
-          if (!key_gt(cand, kth)) continue;
-          list_insert(key, cand, lane);
-          kth.hi = (uint32_t)__builtin_amdgcn_readlane((int)key.hi, kk - 1);
-          kth.lo = (uint32_t)__builtin_amdgcn_readlane((int)key.lo, kk - 1);
-          if (kth.hi != 0) thr = key_value(kth.hi);
+        const uint64_t pass = __ballot(f[e] >= cand.thr);
+        if (pass != 0) {
+          if (f[e] >= cand.thr) {
+            const int j = (vb + kLpThreads * (e / VE) + tid) * VE + e % VE;
+            const int at = cand.count + __popcll(pass & (((uint64_t)1 << lane) - 1));
+            cand.keys[at] = Key{key_image(f[e]), ~(uint32_t)j};
+          }
+          cand.count += __popcll(pass);
+          if (cand.count > 192) cand.compact(kk, lane);   // the next 64 fit
         }
       }
+      // later groups have higher indices: of equal logits the k here stay ahead
+      if (cand.thr > before) cand.thr = key_value(key_image(cand.thr) + 1);
     }
     if (more) {
 #pragma unroll
@@ -413,8 +462,11 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
     sh_sums[wave] = q;
     sh_larger[wave] = larger;
   }
-  if (lane >= kk) key = Key{0u, 0u};
-  if (kk > 0) sh_keys[wave][lane] = key;
+  Key key = {0u, 0u};
+  if (kk > 0) {
+    key = cand.compact(kk, lane);
+    sh_keys[wave][lane] = key;
+  }
   __syncthreads();
   if (wave != 0) return;
   Sums total = sh_sums[0];
