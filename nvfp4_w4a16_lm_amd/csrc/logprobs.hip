@@ -309,13 +309,13 @@ __device__ void extreme_row(const LogprobsArgs& a, const uint8_t* row, int64_t i
   *t_out = t;
 }
 
-// The row's outputs from its sums, count and list (one wavefront).
+// The row's outputs from its sums, count and list (one wavefront); xt = the
+// given token's logit, if there is one.
 template <int DT>
-__device__ __forceinline__ void finish_row(const LogprobsArgs& a, int64_t i, Sums q, int larger, Key k, int lane) {
+__device__ __forceinline__ void finish_row(const LogprobsArgs& a, int64_t i, Sums q, int larger, Key k, bool given,
+                                           float xt, float invt, int lane) {
   const uint8_t* const row = a.x + i * a.row_stride * Elem<DT>::kBytes;
-  const float invt = inv_temperature(a.temps, i), c = invt * kLog2e;
-  bool given;
-  const float xt = token_logit<DT>(a, row, i, &given);
+  const float c = invt * kLog2e;
   const bool empty = q.raw == -INFINITY && !(q.s != q.s);     // nothing allowed or finite, and no NaN
   float m = q.m2 * kLn2;                                       // the maximum of z
   float s = q.s, t = q.t;
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
   bool given;
   const float xt_lane = token_logit<DT>(a, row, i, &given);
   const float xt = given ? xt_lane : INFINITY;           // without a token nothing is larger
-  const float c = inv_temperature(a.temps, i) * kLog2e;
+  const float invt = inv_temperature(a.temps, i), c = invt * kLog2e;
 
   float m2 = kM2Init, s = 0.0f, t = 0.0f, raw = -INFINITY;
   int larger = 0;
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
     for (int w = 1; w < kLpWaves; ++w) key = list_merge(key, sh_keys[w][lane], lane);
   }
   if (a.segs == 1) {
-    finish_row<DT>(a, i, total, count, key, lane);
+    finish_row<DT>(a, i, total, count, key, given, xt_lane, invt, lane);
     return;
   }
   LogprobsPart* const part = a.parts + blockIdx.x;
@@ -497,6 +497,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t i = blockIdx.x;
   const int kk = a.topk;
+  bool given;                                            // looked up now, used at the end
+  const float xt = token_logit<DT>(a, a.x + i * a.row_stride * Elem<DT>::kBytes, i, &given);
+  const float invt = inv_temperature(a.temps, i);
   Key key = {0u, 0u};
   if (kk > 0) {
     const Key* const lists = reinterpret_cast<const Key*>(a.part_keys) + i * a.segs * kk;
@@ -526,7 +529,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
   q = wave_combine(q);
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) count += __shfl_xor(count, d, 64);
-  finish_row<DT>(a, i, q, count, key, lane);
+  finish_row<DT>(a, i, q, count, key, given, xt, invt, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -628,12 +631,14 @@ int elem_bytes(int dtype) { return dtype == kF32 ? 4 : 2; }
 
 }  // namespace
 
-// Segments per row: rows alone fill the GPU from about four workgroups per
-// compute unit (256 CUs); below that a row is cut, in pieces of at least one
-// step of a workgroup (16 logits per thread).
+// Segments per row: 2048 workgroups fill the GPU (eight on each of 256 compute
+// units); with fewer rows a row is cut, in pieces of at least one step of a
+// workgroup (16 logits per thread).  64 x 151936 masked, 20 alternatives: aiming
+// at 512 / 1024 / 2048 / 4096 workgroups 29.8 / 28.3 / 25.9 / 30.1 us.
 int64_t logprobs_segments(int64_t M, int64_t V) {
+  const int64_t rows = std::max<int64_t>(M, 1);
   const int64_t steps = (V + kLpThreads * kGroup16 - 1) / (kLpThreads * kGroup16);
-  const int64_t want = (1024 + std::max<int64_t>(M, 1) - 1) / std::max<int64_t>(M, 1);
+  const int64_t want = (2048 + rows - 1) / rows;
   const int64_t per = std::max<int64_t>(1, (steps + want - 1) / want);   // steps per segment
   return (steps + per - 1) / per;
 }
