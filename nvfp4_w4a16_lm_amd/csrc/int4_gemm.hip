@@ -10,11 +10,12 @@
 // holds codes i and i + 4, so the activations are taken in the same order
 // (0, 4, 1, 5, ...).  The MFMA's A operand is x (16 rows), B is 16 weight rows, so
 // a lane's accumulators all belong to its own weight row (lane % 16) and the
-// row's scale is one value of that lane.  A product of x with a tile of ones
-// gives sum x over the same k in the same places, and per group
-//   total += s (acc - (128 + z) ones)
-// in float32: every product is exact, the only roundings are float32 sums and
-// that step.
+// row's scale is one value of that lane.  The offset 128 + z goes through the
+// MFMA as well: where a group has 128 k or more, x times a tile of ones, once,
+// gives sum x in the accumulator's places, and -(128 + z) sum x starts each group's
+// sum; with smaller groups a tile of the constant -(128 + z) (exact in bf16) is
+// multiplied along.  Per group then total += s acc in float32: every product is
+// exact, the only roundings are float32 sums and that step.
 //
 // A lane (r, g) = (lane % 16, lane / 16) reads row r's codes of k = 128 c + 32 g + [0, 32)
 // as 16 bytes; its word s and those of the other three g make an MFMA step of
@@ -83,18 +84,25 @@ __device__ __forceinline__ float scale_value(uint32_t bits16, bool f16) {
 // scales (and zero points) together, whole rows of them, D + 1 tiles ahead into
 // registers, and leave them in LDS one tile ahead as float32 words whose four
 // low bits, zero in any bf16 or f16 value, hold the zero point.  The
-// wavefronts' sums of a tile meet in LDS (two buffers, one barrier a tile).  K
+// wavefronts' sums of a tile meet in LDS (two buffers and one barrier a tile up
+// to 16 rows; one buffer and two barriers beyond, where LDS is short).  K
 // beyond W NC chunks is taken in phases over the same tiles, whose sums wait in
 // LDS meanwhile.  NG: scales per 128 k (4, 2: groups of 32, 64; 1: groups of a
 // multiple of 128, or one group per row).
 // ---------------------------------------------------------------------------
 // Wavefronts per workgroup: the x fragments take 32 MT NC registers of each lane.
+// Sum buffers, and tiles in flight per wavefront: LDS that the sums held from
+// phase to phase need is worth more there (M = 64, 128256 x 4096: 209 us with two
+// buffers and three tiles).
+constexpr int i4_buffers(int mt) { return mt == 1 ? 2 : 1; }
+constexpr int i4_depth(int mt) { return mt == 1 ? 3 : 2; }
 constexpr int i4_max_waves(int mt, int nc) { return mt * nc == 1 ? 16 : mt * nc == 2 ? 11 : 8; }
 
 template <int MT, int NC, int NG, bool ZP, int D>
 __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) void int4_stream_kernel(Int4Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
   constexpr int SI = (NC * NG + 1) / 2;                 // scales per thread and tile
+  constexpr int RB = i4_buffers(MT);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int W = blockDim.x >> 6;
   const int r = lane & 15, g = lane >> 4;
@@ -105,8 +113,8 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
   const int t0 = (int)((int64_t)tiles * blockIdx.x / gridDim.x), t1 = (int)((int64_t)tiles * (blockIdx.x + 1) / gridDim.x);
   const int phases = (nchunks + W * NC - 1) / (W * NC);
   uint8_t* const ring = lds8 + wave * (D * NC * kSt4Bytes);
-  float* const red = reinterpret_cast<float*>(lds8 + W * (D * NC * kSt4Bytes));   // [2][W][MT][256]
-  uint32_t* const scl = reinterpret_cast<uint32_t*>(red + 2 * W * MT * 256);      // [2][16][a.scale_pitch]
+  float* const red = reinterpret_cast<float*>(lds8 + W * (D * NC * kSt4Bytes));   // [RB][W][MT][256]
+  uint32_t* const scl = reinterpret_cast<uint32_t*>(red + RB * W * MT * 256);      // [2][16][a.scale_pitch]
   float* const bias = reinterpret_cast<float*>(scl + 2 * 16 * a.scale_pitch);     // [t1 - t0][16]
   float* const held = bias + 16 * a.tiles_per_block;                              // [t1 - t0][MT][256], several phases
   const int spitch = a.scale_pitch;
@@ -131,11 +139,13 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
     uint32_t sv[D + 1][SI], zv[D + 1][SI];              // the last entry: the first tile's
     auto load_scales = [&](int t, int slot) {
       const int last = min(15, N - 1 - 16 * t);
+      const uint16_t* const sb = a.scales + (int64_t)16 * t * a.groups + j0;
+      const uint32_t* const zb = ZP ? a.zeros + (int64_t)2 * t * a.groups + j0 : nullptr;
 #pragma unroll
       for (int i = 0; i < SI; ++i) {
-        const int row = 16 * t + min(srow[i], last);
-        sv[slot][i] = a.scales[(int64_t)row * a.groups + j0 + scol[i]];
-        if (ZP) zv[slot][i] = (uint32_t)a.zeros[(int64_t)(row >> 3) * a.groups + j0 + scol[i]];
+        const int row = min(srow[i], last);
+        sv[slot][i] = sb[(uint32_t)(row * a.groups + scol[i])];
+        if (ZP) zv[slot][i] = zb[(uint32_t)((row >> 3) * a.groups + scol[i])];
       }
     };
     auto store_scales = [&](int t, int slot) {
@@ -231,7 +241,7 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (NG > 1) transpose4(w[q][h]);
-          f32x4 acc[MT], ones[MT];
+          f32x4 acc[MT];
           const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
           if (NG == 1) {
             const float off = 128.0f + (float)(sw[q][h][0] & 15u);
@@ -245,34 +255,37 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
             constexpr int kSteps = 4 / NG;              // MFMA steps per group
             const bool fresh = NG > 1 && s % kSteps == 0;
             const bf16x8 wb = codes_bf16(w[q][h][s]);
+            // small groups: -(128 + z) of the lane's row as a tile of its own, exact in bf16
+            const uint32_t ob = ZP ? (0xC300u | (sw[q][h][s / kSteps] & 15u)) * 0x10001u : 0xC308C308u;
+            const u32x4 obits = {ob, ob, ob, ob};
+            const bf16x8 off = __builtin_bit_cast(bf16x8, obits);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-              if (NG > 1) ones[i] = mfma_i4(xa[q][h][s][i], one, fresh ? zero : ones[i]);
               acc[i] = mfma_i4(xa[q][h][s][i], wb, fresh ? zero : acc[i]);
+              if (NG > 1) acc[i] = mfma_i4(xa[q][h][s][i], off, acc[i]);
             }
             if (s % kSteps == kSteps - 1) {
               const uint32_t sb = sw[q][h][s / kSteps];
               const float sc = __uint_as_float(ZP ? sb & ~15u : sb);
-              const float off = 128.0f + (ZP ? (float)(sb & 15u) : 8.0f);
 #pragma unroll
               for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  total[i][v] = __builtin_fmaf(sc, NG == 1 ? acc[i][v] : __builtin_fmaf(-off, ones[i][v], acc[i][v]),
-                                               total[i][v]);
+                for (int v = 0; v < 4; ++v) total[i][v] = __builtin_fmaf(sc, acc[i][v], total[i][v]);
             }
           }
         }
       }
+      const int buf = RB == 2 ? t & 1 : 0;
+      if (RB == 1) st4_barrier();                       // the tile before has been summed
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<f32x4*>(red + (((t & 1) * W + wave) * MT + i) * 256 + 4 * lane) = total[i];
+        *reinterpret_cast<f32x4*>(red + ((buf * W + wave) * MT + i) * 256 + 4 * lane) = total[i];
       st4_barrier();
       // element 4 l + v is lane l's v: row 4 (l / 16) + v of x, weight row l % 16
       for (int i = tid; i < 256 * MT; i += blockDim.x) {
         const int m = mb + 16 * (i >> 8) + 4 * ((i >> 6) & 3) + (i & 3), n = 16 * t + ((i >> 2) & 15);
         if (m >= a.M || n >= N) continue;
-        const float* const part = red + (t & 1) * W * MT * 256 + i;
+        const float* const part = red + buf * W * MT * 256 + i;
         float sum = 0.0f;
         for (int v = 0; v < W; v += 4) {                // four reads at a time, added in order
           float q[4];
@@ -305,11 +318,9 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
 
 namespace {
 
-constexpr int kI4Depth = 3;                  // tiles in flight per wavefront
-
 template <int MT, int NC>
 const void* int4_stream(int ng, bool zp) {
-  constexpr int D = kI4Depth;
+  constexpr int D = i4_depth(MT);
   if (zp)
     return ng == 4   ? (const void*)int4_stream_kernel<MT, NC, 4, true, D>
            : ng == 2 ? (const void*)int4_stream_kernel<MT, NC, 2, true, D>
@@ -329,7 +340,7 @@ hipError_t launch_int4_stream(Int4Args a, hipStream_t stream) {
   // groups of a phase: at most its k / group, two more where they straddle
   auto pitch_of = [&](int64_t slots) { return std::min<int64_t>(a.groups, slots * kSt4Chunk / a.group + 2) | 1; };
   auto lds_of = [&](int64_t w, int64_t c) {
-    return w * (kI4Depth * c * kSt4Bytes + 2048 * MT) + 128 * pitch_of(w * c);
+    return w * (i4_depth(MT) * c * kSt4Bytes + i4_buffers(MT) * 1024 * MT) + 128 * pitch_of(w * c);
   };
   int nc = 1, waves = 1;
   int64_t best = INT64_MAX;
@@ -356,8 +367,8 @@ hipError_t launch_int4_stream(Int4Args a, hipStream_t stream) {
   // a workgroup's tiles: their biases and, with several phases, their held sums fit beside
   const int64_t per_tile = 64 + (phases > 1 ? 1024 * MT : 0);
   const int64_t room = (158 * 1024 / per_cu - lds) / per_tile;
-  const int64_t grid = std::max<int64_t>(std::min<int64_t>(tiles, (int64_t)device_cus(dev) * per_cu),
-                                         (tiles + room - 1) / room);
+  const int64_t slots = (int64_t)device_cus(dev) * per_cu;
+  const int64_t grid = std::min<int64_t>(tiles, slots * ((tiles + slots * room - 1) / (slots * room)));
   a.tiles_per_block = (int)((tiles + grid - 1) / grid);
   lds += a.tiles_per_block * per_tile;
   const void* fn = int4_stream<MT, 1>(ng, a.zeros != nullptr);
