@@ -78,6 +78,121 @@ __device__ __forceinline__ float scale_value(uint32_t bits16, bool f16) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
+// One or two activation rows: whole rows of the weight past the wavefront, 64
+// consecutive 16-byte segments (32 k each) a load, each lane always the same
+// segments, so that its x stays in registers: no LDS, no barrier.  A code's
+// bf16 128 + q goes into v_dot2_f32_bf16 (float32 sum of exact products) with its
+// neighbour four codes on; a segment lies in one group.  Four rows a batch, the
+// next batch on its way meanwhile.  VALU and HBM about balance.  128256 x 4096,
+// M = 1: groups of 128 / 32 with zero points 53 / 55 us (5.1 TB/s), 58 / 86 us in the
+// streamed form below; 8192 x 2048 4.5 against 7.9 us; 128256 x 8192 116 against 141.
+// ---------------------------------------------------------------------------
+template <int MR, int SEG, bool ZP>
+__global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
+  const int lane = threadIdx.x & 63, wave = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = gridDim.x * 4, N = a.N, K = a.K;
+  const int nseg = K >> 5;
+  u32x4 xr[MR][SEG][4];
+  float sumx[MR][SEG];
+  int seg[SEG], grp[SEG];
+#pragma unroll
+  for (int j = 0; j < SEG; ++j) {
+    seg[j] = min(lane + 64 * j, nseg - 1);               // beyond the row: a repeat, against x = 0
+    grp[j] = seg[j] * 32 / a.group;
+  }
+  struct Batch {
+    u32x4 w[4][SEG];
+    uint32_t s[4][SEG], z[4][SEG];
+  };
+  auto load = [&](int r0, Batch& b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = min(r0 + i, N - 1);             // repeats are computed, not stored
+      const uint8_t* const wp = a.packed + row * (K >> 1);
+      const uint16_t* const sp = a.scales + row * a.groups;
+      const uint32_t* const zp = ZP ? a.zeros + (row >> 3) * a.groups : nullptr;
+#pragma unroll
+      for (int j = 0; j < SEG; ++j) {
+        b.w[i][j] = load_stream16(wp + (uint32_t)(16 * seg[j]));
+        b.s[i][j] = sp[(uint32_t)grp[j]];
+        if (ZP) b.z[i][j] = zp[(uint32_t)grp[j]];
+      }
+    }
+  };
+  auto compute = [&](int r0, const Batch& b) {
+    float p[MR][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int m = 0; m < MR; ++m) p[m][i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < SEG; ++j) {
+        const float sc = scale_value(b.s[i][j], a.scale_f16);
+        const float off = ZP ? 128.0f + (float)((b.z[i][j] >> (4 * (min(r0 + i, N - 1) & 7))) & 15u) : 136.0f;
+        float blk[MR];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) blk[m] = -off * sumx[m][j];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t word = b.w[i][j][q];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t c = ((word >> (4 * e)) & 0x000F000Fu) | 0x43004300u;
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+              const uint32_t xe = xr[m][j][q][e];
+              blk[m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, c), __builtin_bit_cast(bf16x2, xe),
+                                                       blk[m], false);
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < MR; ++m) p[m][i] = __builtin_fmaf(sc, blk[m], p[m][i]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      const float tot = wave_sum4(p[m], lane);
+      const int row = r0 + ((lane >> 5) & 1) * 2 + ((lane >> 4) & 1);
+      if ((lane & 15) == 0 && row < N && m < a.M) {
+        const float bias = a.bias ? __uint_as_float((uint32_t)a.bias[row] << 16) : 0.0f;
+        a.y[(int64_t)m * N + row] = __builtin_bit_cast(uint16_t, (__bf16)(tot + bias));
+      }
+    }
+  };
+  Batch b0, b1;
+  const int first = 4 * wave, step = 4 * waves;
+  if (first < N) load(first, b0);
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int j = 0; j < SEG; ++j) {
+      const bool in = lane + 64 * j < nseg;
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(a.x + (int64_t)min(m, a.M - 1) * K + 32 * seg[j] + 8 * q);
+        const u32x4 o = __builtin_bit_cast(u32x4, reorder_x(v));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = in ? o[e] : 0u;
+          xr[m][j][q][e] = w;
+          s += bf16_lo(w) + bf16_hi(w);
+        }
+      }
+      sumx[m][j] = s;
+    }
+  for (int r0 = first; r0 < N; r0 += 2 * step) {
+    const bool more = r0 + step < N;
+    if (more) load(r0 + step, b1);
+    compute(r0, b0);
+    if (!more) break;
+    if (r0 + 2 * step < N) load(r0 + 2 * step, b0);
+    compute(r0 + step, b1);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // stream4.hpp's scheme for 16 MT activation rows.  Wavefront w of a workgroup
 // keeps the x fragments of its NC chunks of 256 k, and the workgroup streams the
 // 16-row tiles that it owns past them.  The workgroup's threads fetch a tile's
@@ -384,7 +499,32 @@ hipError_t launch_int4_stream(Int4Args a, hipStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+template <int MR, int SEG>
+hipError_t launch_int4_dot(const Int4Args& a, hipStream_t stream) {
+  const void* const fn = a.zeros ? (const void*)int4_dot_kernel<MR, SEG, true> : (const void*)int4_dot_kernel<MR, SEG, false>;
+  const int dev = current_device();
+  const int64_t blocks = ((int64_t)a.N + 15) / 16;
+  const int64_t grid = std::min<int64_t>(blocks, (int64_t)device_cus(dev) * blocks_per_cu(fn, dev, 256, 0));
+  return launch_kernel(fn, dim3((unsigned)grid), dim3(256), stream, a);
+}
+
+}  // namespace
+
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
+  // One or two rows whose x fits in the lanes' registers (K to 8192, and 2048),
+  // where the row fills nine tenths of the lanes' segments.  The dot kernel
+  // against the streamed one: 151936 x 5120 (M = 1, 83 % filled) 88 and 86 us; 128256
+  // x 4096 at M = 2, K beyond the limit, 79 and 58 us.
+  const int64_t seg = ((int64_t)a.K + 2047) / 2048;
+  if (10 * (int64_t)a.K >= 9 * 2048 * seg) {
+    if (a.M == 1 && seg == 1) return launch_int4_dot<1, 1>(a, stream);
+    if (a.M == 1 && seg == 2) return launch_int4_dot<1, 2>(a, stream);
+    if (a.M == 1 && seg == 3) return launch_int4_dot<1, 3>(a, stream);
+    if (a.M == 1 && seg == 4) return launch_int4_dot<1, 4>(a, stream);
+    if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
+  }
   if (a.M <= 16) return launch_int4_stream<1>(a, stream);
   if (a.M <= 32) return launch_int4_stream<2>(a, stream);
   if (a.M <= 48) return launch_int4_stream<3>(a, stream);

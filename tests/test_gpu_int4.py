@@ -120,3 +120,13 @@ def test_long_rows_in_phases(m, n, k, group):
     if k % group:
         group = 32
     check(m, n, k, group, group != 128, seed=m + n + k + group)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [(1, 1, 1536, 32), (1, 70, 2048, 64), (2, 133, 1600, 32), (1, 515, 4096, 128),
+                                         (2, 1001, 4096, 1024), (1, 99, 6144, 128), (1, 37, 8192, 8192),
+                                         (1, 30011, 2048, 128), (2, 2000, 1984, 64),
+                                         (1, 333, 1856, 32), (1, 10, 3776, 64), (2, 31, 2048, 2048)])
+def test_one_and_two_rows(m, n, k, group, zeros):
+    """The dot kernel: rows that fill a lane's one to four segments, wholly or partly."""
+    check(m, n, k, group, zeros, seed=m + n + k + group, bias=(n % 2 == 1))
