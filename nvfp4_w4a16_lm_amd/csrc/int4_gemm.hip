@@ -52,11 +52,21 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
   w = u32x4{a, b, p[0], p[1]};
 }
 
+// Codes i and i + 4 of a word shifted by 4 i.  The constants are hidden from the
+// compiler in a scalar and a vector register, or it spends two instructions
+// (v_and_or_b32 takes one scalar operand and no literal).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  uint32_t mask = 0x000F000Fu, one = 0x43004300u;
+  __asm__("" : "+s"(mask));
+  __asm__("" : "+v"(one));
+  return (w & mask) | one;
+}
+
 // Eight codes -> 128 + code in bf16, codes (0, 4, 1, 5, 2, 6, 3, 7).
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
   u32x4 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+  for (int i = 0; i < 4; ++i) o[i] = code_pair(w >> (4 * i));
   return __builtin_bit_cast(bf16x8, o);
 }
 
@@ -84,7 +94,7 @@ __device__ __forceinline__ float scale_value(uint32_t bits16, bool f16) {
 // bf16 128 + q goes into v_dot2_f32_bf16 (float32 sum of exact products) with its
 // neighbour four codes on; a segment lies in one group.  Four rows a batch, the
 // next batch on its way meanwhile.  VALU and HBM about balance.  128256 x 4096,
-// M = 1: groups of 128 / 32 with zero points 53 / 55 us (5.1 TB/s), 58 / 86 us in the
+// M = 1, groups of 128: 49 us (5.5 TB/s), 58 us in the
 // streamed form below; 8192 x 2048 4.5 against 7.9 us; 128256 x 8192 116 against 141.
 // ---------------------------------------------------------------------------
 template <int MR, int SEG, bool ZP>
@@ -137,7 +147,7 @@ __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
           const uint32_t word = b.w[i][j][q];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t c = ((word >> (4 * e)) & 0x000F000Fu) | 0x43004300u;
+            const uint32_t c = code_pair(word >> (4 * e));
 #pragma unroll
             for (int m = 0; m < MR; ++m) {
               const uint32_t xe = xr[m][j][q][e];
