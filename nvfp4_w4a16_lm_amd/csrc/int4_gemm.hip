@@ -94,8 +94,8 @@ __device__ __forceinline__ float scale_value(uint32_t bits16, bool f16) {
 // bf16 128 + q goes into v_dot2_f32_bf16 (float32 sum of exact products) with its
 // neighbour four codes on; a segment lies in one group.  Four rows a batch, the
 // next batch on its way meanwhile.  VALU and HBM about balance.  128256 x 4096,
-// M = 1, groups of 128: 49 us (5.5 TB/s), 58 us in the
-// streamed form below; 8192 x 2048 4.5 against 7.9 us; 128256 x 8192 116 against 141.
+// M = 1, groups of 128: 49 us (5.5 TB/s), 58 us in the streamed form below; 8192 x
+// 2048 4.5 against 7.9 us; 128256 x 8192 116 against 141.
 // ---------------------------------------------------------------------------
 template <int MR, int SEG, bool ZP>
 __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
       for (int m = 0; m < MR; ++m) p[m][i] = 0.0f;
 #pragma unroll
       for (int j = 0; j < SEG; ++j) {
-        const float sc = scale_value(b.s[i][j], a.scale_f16);
+        float sc = scale_value(b.s[i][j], a.scale_f16);
+        if (j == SEG - 1 && lane + 64 * j >= nseg) sc = 0.0f;   // lest an infinite scale meet x = 0
         const float off = ZP ? 128.0f + (float)((b.z[i][j] >> (4 * (min(r0 + i, N - 1) & 7))) & 15u) : 136.0f;
         float blk[MR];
 #pragma unroll
@@ -348,8 +349,9 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
             const int j = NG == 1 ? k / a.group : NG * (k / 128) + i;
-            // beyond the row's groups the activations are zero
-            sw[q][h][i] = scl[((t & 1) * 16 + r) * spitch + min(j - j0, gn - 1)];
+            // beyond the row's groups the activations are zero; 0, lest an infinite scale meet them
+            const uint32_t word = scl[((t & 1) * 16 + r) * spitch + min(j - j0, gn - 1)];
+            sw[q][h][i] = j - j0 < gn ? word : 0u;
           }
         }
       __builtin_amdgcn_s_waitcnt(kSt4Lgkm0);            // the region may now be refilled
@@ -522,6 +524,288 @@ hipError_t launch_int4_dot(const Int4Args& a, hipStream_t stream) {
 
 }  // namespace
 
+// ---------------------------------------------------------------------------
+// More than 16 activation rows on enough weight rows: a wavefront owns NT 16-row tiles
+// for all of K, so its sums stay in its registers.  The eight wavefronts of a
+// workgroup share x, 256 k a step in two LDS buffers, in the order that the MFMA
+// reads it; the weights come through each wavefront's own ring of two chunks, its
+// scales and zero points through its own piece of LDS.  x and scales are loaded
+// three steps ahead into registers and stored one step ahead.  One barrier a
+// step.  Where a group has 128 k or more, the sums of x that the offset needs fall
+// out of the x stores.  The vector units bound it, LDS reads of x come next (half
+// of either at 33 x 32000 x 4096 before the unpacking was cut from 11 to 7
+// instructions a word): two tiles share each x fragment where the grid still fills the
+// card.  33 x 32003 x 2080, groups of 32 with zero points: 27 us, 44 in the streamed
+// form; 64 x 128256 x 4096: 113 us (2.4 TB/s, 600 TFLOP/s) against 153, one tile 148.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int NG, bool ZP>
+__global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds8[];
+  constexpr int D = 2;                                  // chunks of weights in flight; three are no faster
+  constexpr int XB = MT * 8192;                         // bytes of an x buffer
+  constexpr int COLS = 2 * NG, SP = COLS + 1;           // scales per row and step, and their LDS pitch
+  constexpr int SI = (16 * NT * COLS + 63) / 64;        // scales per lane and step
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int K = a.K, N = a.N;
+  const int64_t pitch = K >> 1;
+  const int nch = (K + kSt4Chunk - 1) / kSt4Chunk;
+  const int tiles = (N + 15) >> 4;
+  const int mb = 16 * MT * blockIdx.y;
+  uint8_t* const ring = lds8 + 2 * XB + wave * (D * NT * kSt4Bytes);
+  float* const sums = reinterpret_cast<float*>(lds8 + 2 * XB + 8 * (D * NT * kSt4Bytes));   // [2][2][16 MT], NG == 1
+  uint32_t* const scl = reinterpret_cast<uint32_t*>(sums + (NG == 1 ? 64 * MT : 0)) + wave * (16 * NT * SP);
+  int tile[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) tile[t] = min(((int)blockIdx.x * 8 + wave) * NT + t, tiles - 1);   // a repeat is not stored
+
+  // one base per tile and 32-bit offsets beside it
+  const int piece = (lane & 7) ^ (lane >> 3);
+  uint32_t roff[NT][2];
+  const uint8_t* wbase[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    wbase[t] = a.packed + (int64_t)16 * tile[t] * pitch;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) roff[t][j] = (uint32_t)min(8 * j + (lane >> 3), N - 1 - 16 * tile[t]) * (uint32_t)pitch;
+  }
+  auto copy = [&](int c, int slot) {                    // as st4_copy
+    const uint32_t off = (uint32_t)min(kSt4Chunk / 2 * c + 16 * piece, (int)pitch - 16);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_global_load_lds((const void*)(wbase[t] + (roff[t][j] + off)),
+                                         (st4_lds_t)(ring + (slot * NT + t) * kSt4Bytes + 1024 * j), 16, 0, 2 /* nontemporal */);
+  };
+  // scale e = lane + 64 i of a step: row e / COLS of the NT tiles, column e % COLS
+  uint32_t sv[2][SI], zv[2][SI];
+  // (2 c + col) / (128-k blocks per group), by a multiplication: exact to K = 2^22
+  const uint32_t blocks = ((uint32_t)a.group + 127) / 128, per = (0x80000000u + blocks - 1) / blocks;
+  auto scale_group = [&](int c, int col) {
+    return NG == 1 ? (int)__umulhi(2u * (uint32_t)(2 * c + col), per) : COLS * c + col;
+  };
+  const int row0 = 16 * tile[0], last = N - 1 - row0;
+  const uint8_t* const sbase = reinterpret_cast<const uint8_t*>(a.scales + (int64_t)row0 * a.groups);
+  const uint8_t* const zbase = reinterpret_cast<const uint8_t*>(ZP ? a.zeros + (int64_t)(row0 >> 3) * a.groups : nullptr);
+  uint32_t soff[SI], zoff[SI];
+#pragma unroll
+  for (int i = 0; i < SI; ++i) {
+    const int row = min(min(lane + 64 * i, 16 * NT * COLS - 1) / COLS, last);
+    soff[i] = (uint32_t)row * (uint32_t)a.groups;
+    zoff[i] = (uint32_t)(row >> 3) * (uint32_t)a.groups;
+  }
+  auto load_scales = [&](int c, int set) {
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      const uint32_t j = (uint32_t)min(scale_group(c, min(lane + 64 * i, 16 * NT * COLS - 1) % COLS), a.groups - 1);
+      sv[set][i] = *reinterpret_cast<const uint16_t*>(sbase + 2 * (soff[i] + j));
+      if (ZP) zv[set][i] = *reinterpret_cast<const uint32_t*>(zbase + 4 * (zoff[i] + j));
+    }
+  };
+  auto store_scales = [&](int c, int set) {
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      const int e = min(lane + 64 * i, 16 * NT * COLS - 1);
+      uint32_t w = __float_as_uint(scale_value(sv[set][i], a.scale_f16));
+      if (ZP) w |= (zv[set][i] >> (4 * (e / COLS & 7))) & 15u;
+      if (scale_group(c, e % COLS) >= a.groups) w = 0;  // 0, lest an infinite scale meet x = 0
+      scl[e / COLS * SP + e % COLS] = w;
+    }
+  };
+  // x octet tid + 512 i of a step: row (tid + 512 i) / 32, k = 256 c + 8 ((tid + 512 i) % 32)
+  u32x4 xv[2][MT];
+  const int oct = tid & 31, o = oct & 15;
+  const uint8_t* const xbase = reinterpret_cast<const uint8_t*>(a.x + (int64_t)mb * K);
+  uint32_t xoff[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xoff[i] = (uint32_t)min(16 * i + (tid >> 5), a.M - 1 - mb) * (uint32_t)K;
+  auto load_x = [&](int c, int set) {
+    const uint32_t k = (uint32_t)min(kSt4Chunk * c + 8 * oct, K - 8);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xv[set][i] = *reinterpret_cast<const u32x4*>(xbase + 2 * (xoff[i] + k));
+  };
+  // MFMA step s, lane quarter g of octet o of a 128-k half; the slot is swizzled
+  // by o so that 16 octets of a row spread over the banks
+  const int xw = ((oct >> 4) * 4 + (NG == 1 ? o & 3 : o >> 2)) * 1024 + ((NG == 1 ? o >> 2 : o & 3) * 16 + ((tid >> 5) ^ o)) * 16;
+  auto store_x = [&](int c, int set) {
+    uint8_t* const b = lds8 + (c & 1) * XB + xw;
+    const bool in = kSt4Chunk * c + 8 * oct < K;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const u32x4 v = in ? xv[set][i] : u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<bf16x8*>(b + i * 8192) = reorder_x(v);
+      if (NG == 1) {
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = v[e];
+          s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, 0x3F803F80u), s, false);
+        }
+        s = dpp_row_sum(s);
+        if (o == 0) sums[((c & 1) * 2 + (oct >> 4)) * 16 * MT + 16 * i + (tid >> 5)] = s;
+      }
+    }
+  };
+
+  load_x(0, 0);
+  load_scales(0, 0);
+  __asm__ volatile("" ::: "memory");
+  load_x(min(1, nch - 1), 1);
+  load_scales(min(1, nch - 1), 1);
+  __asm__ volatile("" ::: "memory");
+  copy(0, 0);
+  __asm__ volatile("" ::: "memory");
+  store_x(0, 0);
+  store_scales(0, 0);
+  load_x(min(2, nch - 1), 0);
+  load_scales(min(2, nch - 1), 0);
+  __asm__ volatile("" ::: "memory");
+  copy(min(1, nch - 1), 1);
+  __asm__ volatile("" ::: "memory");
+
+  f32x4 total[NT][MT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) total[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int xr[4];                                            // the lane's slot in step s's 64
+#pragma unroll
+  for (int s = 0; s < 4; ++s) xr[s] = s * 1024 + (g * 16 + (r ^ (NG == 1 ? 4 * g + s : 4 * s + g))) * 16;
+
+  int slot = 0;
+  auto step = [&](int c, int set) {                     // set: (c + 1) % 2
+    st4_barrier();
+    // chunk c's copies, and the x and scales of c + 1: one step's loads and copies are younger
+    __builtin_amdgcn_s_waitcnt(st4_vm(2 * NT + MT + SI * (ZP ? 2 : 1)));
+    __builtin_amdgcn_sched_barrier(0);                  // no use of those moves above the wait
+    __asm__ volatile("" ::: "memory");
+    u32x4 w[NT][2];
+    uint32_t sw[NT][COLS];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[t][h] = st4_read(ring + (slot * NT + t) * kSt4Bytes, r, 4 * h + g);
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) sw[t][j] = scl[(16 * t + r) * SP + j];
+    }
+    __builtin_amdgcn_s_waitcnt(kSt4Lgkm0);              // the region may now be refilled
+    __asm__ volatile("" ::: "memory");
+    store_x(c + 1, set);
+    store_scales(c + 1, set);
+    load_x(min(c + 3, nch - 1), set);
+    load_scales(min(c + 3, nch - 1), set);
+    __asm__ volatile("" ::: "memory");
+    copy(min(c + D, nch - 1), slot);
+    __asm__ volatile("" ::: "memory");                  // issued now, not at the step's end
+    slot ^= 1;
+
+    const uint8_t* const xb = lds8 + (c & 1) * XB;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f32x4 acc[NT][MT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (NG > 1) transpose4(w[t][h]);
+      if (NG == 1) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const f32x4 sx = *reinterpret_cast<const f32x4*>(sums + ((c & 1) * 2 + h) * 16 * MT + 16 * i + 4 * g);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float off = ZP ? -128.0f - (float)(sw[t][h] & 15u) : -136.0f;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[t][i][v] = off * sx[v];
+          }
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        constexpr int kSteps = 4 / NG;                  // MFMA steps per group
+        const bool fresh = NG > 1 && s % kSteps == 0;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        bf16x8 xa[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xa[i] = *reinterpret_cast<const bf16x8*>(xb + i * 8192 + h * 4096 + xr[s]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t sb = sw[t][h * NG + s / kSteps];
+          const bf16x8 wb = codes_bf16(w[t][h][s]);
+          const uint32_t ob = ZP ? (0xC300u | (sb & 15u)) * 0x10001u : 0xC308C308u;
+          const u32x4 obits = {ob, ob, ob, ob};
+          const bf16x8 off = __builtin_bit_cast(bf16x8, obits);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            acc[t][i] = mfma_i4(xa[i], wb, fresh ? zero : acc[t][i]);
+            if (NG > 1) acc[t][i] = mfma_i4(xa[i], off, acc[t][i]);
+          }
+          if (s % kSteps == kSteps - 1) {
+            const float sc = __uint_as_float(ZP ? sb & ~15u : sb);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) total[t][i][v] = __builtin_fmaf(sc, acc[t][i][v], total[t][i][v]);
+          }
+        }
+      }
+    }
+  };
+  // whole pairs of steps: a step past K adds 0, and one block keeps the compiler's waits out
+  for (int c = 0; c < nch; c += 2) {
+    step(c, 1);
+    step(c + 1, 0);
+  }
+  __builtin_amdgcn_s_waitcnt(st4_vm(0));                // trailing copies land before the LDS is given up
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int n = 16 * (((int)blockIdx.x * 8 + wave) * NT + t) + r;
+    if (n >= N) continue;
+    const float bias = a.bias ? __uint_as_float((uint32_t)a.bias[n] << 16) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int m = mb + 16 * i + 4 * g + v;
+        if (m < a.M) a.y[(int64_t)m * N + n] = __builtin_bit_cast(uint16_t, (__bf16)(total[t][i][v] + bias));
+      }
+  }
+}
+
+namespace {
+
+template <int MT, int NT>
+hipError_t launch_int4_tiles(const Int4Args& a, const dim3& blocks, hipStream_t stream) {
+  const int ng = a.group == 32 && a.K > 32 ? 4 : a.group == 64 && a.K > 64 ? 2 : 1;
+  const void* fn;
+  if (a.zeros)
+    fn = ng == 4   ? (const void*)int4_tile_kernel<MT, NT, 4, true>
+         : ng == 2 ? (const void*)int4_tile_kernel<MT, NT, 2, true>
+                   : (const void*)int4_tile_kernel<MT, NT, 1, true>;
+  else
+    fn = ng == 4   ? (const void*)int4_tile_kernel<MT, NT, 4, false>
+         : ng == 2 ? (const void*)int4_tile_kernel<MT, NT, 2, false>
+                   : (const void*)int4_tile_kernel<MT, NT, 1, false>;
+  const int lds = 2 * MT * 8192 + 8 * 2 * NT * kSt4Bytes + (ng == 1 ? 256 * MT : 0) + 8 * 64 * NT * (2 * ng + 1);
+  const hipError_t e = ensure_dynamic_lds(fn, current_device(), lds);
+  if (e != hipSuccess) return e;
+  return launch_kernel_lds(fn, blocks, dim3(512), (size_t)lds, stream, a);
+}
+
+// Two tiles a wavefront where that takes fewer rounds of workgroups, a round
+// counted 1.6 times as long (64 x 128256 x 4096: 57 and 37 us a round; 1.1 to 1.5
+// times where one round is all, so that one tile is right there).
+template <int MT>
+hipError_t launch_int4_tile(const Int4Args& a, hipStream_t stream) {
+  const int64_t cus = device_cus(current_device());
+  const int64_t mblocks = ((int64_t)a.M + 16 * MT - 1) / (16 * MT);
+  const int64_t one = ((int64_t)a.N + 127) / 128, two = ((int64_t)a.N + 255) / 256;
+  const int64_t rounds1 = (one * mblocks + cus - 1) / cus, rounds2 = (two * mblocks + cus - 1) / cus;
+  if (8 * rounds2 < 5 * rounds1) return launch_int4_tiles<MT, 2>(a, dim3((unsigned)two, (unsigned)mblocks), stream);
+  return launch_int4_tiles<MT, 1>(a, dim3((unsigned)one, (unsigned)mblocks), stream);
+}
+
+}  // namespace
+
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
   // One or two rows whose x fits in the lanes' registers (K to 8192, and 2048),
   // where the row fills nine tenths of the lanes' segments.  The dot kernel
@@ -536,6 +820,16 @@ hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
     if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
   }
   if (a.M <= 16) return launch_int4_stream<1>(a, stream);
+  // The tile kernel where one tile a wavefront gives two fifths of the compute
+  // units a workgroup (64 x 12000 x 8192: 61 us, streamed 60; 33 x 16000 x 4096 26.5 and
+  // 27; 64 x 4096 x 4096 38 and 26), and K leaves its 32-bit offsets in range.
+  const int64_t cus = device_cus(current_device());
+  const int64_t mblocks = a.M <= 48 ? 1 : ((int64_t)a.M + 63) / 64;
+  if (5 * (((int64_t)a.N + 127) / 128) * mblocks >= 2 * cus && a.K <= 1 << 22) {
+    if (a.M <= 32) return launch_int4_tile<2>(a, stream);
+    if (a.M <= 48) return launch_int4_tile<3>(a, stream);
+    return launch_int4_tile<4>(a, stream);
+  }
   if (a.M <= 32) return launch_int4_stream<2>(a, stream);
   if (a.M <= 48) return launch_int4_stream<3>(a, stream);
   return launch_int4_stream<4>(a, stream);

@@ -130,3 +130,32 @@ def test_long_rows_in_phases(m, n, k, group):
 def test_one_and_two_rows(m, n, k, group, zeros):
     """The dot kernel: rows that fill a lane's one to four segments, wholly or partly."""
     check(m, n, k, group, zeros, seed=m + n + k + group, bias=(n % 2 == 1))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [
+    (17, 13313, 96, 32), (33, 14001, 160, 32), (64, 13500, 320, 64), (48, 15007, 2080, 32), (30, 14111, 1152, 384),
+    (40, 13333, 544, 544), (65, 8200, 256, 128), (200, 3511, 768, 256), (50, 14000, 1024, 128), (128, 7000, 32, 32),
+    # more workgroups than compute units: two tiles per wavefront
+    (64, 33000, 512, 128), (20, 33011, 352, 32), (256, 16500, 320, 64), (48, 66001, 128, 128), (18, 40007, 544, 32)])
+def test_many_rows_of_both(m, n, k, group, zeros):
+    """The tile kernel: odd and even counts of 256-k steps, K that ends inside one, rows that end inside a tile."""
+    check(m, n, k, group, zeros, seed=m + n + k + group, bias=(n % 2 == 1))
+
+
+def test_many_rows_of_both_f16_scales():
+    check(33, 13999, 512, 64, True, seed=6, scale_dtype=torch.float16, bias=True)
+    check(64, 34000, 384, 128, True, seed=7, scale_dtype=torch.float16)
+
+
+@pytest.mark.parametrize("m,n,k,group", [(1, 64, 1888, 32), (1, 64, 3872, 32), (2, 64, 1888, 32), (4, 64, 160, 32),
+                                         (3, 64, 192, 64), (5, 40, 384, 128), (40, 64, 160, 32), (20, 14000, 160, 32),
+                                         (50, 13500, 384, 128), (64, 33000, 96, 96)])
+def test_infinite_scale_of_the_last_group(m, n, k, group):
+    """A step reaches past K there: what lies beyond is 0, not 0 times the scale."""
+    x, packed, scales, zp, _ = make(m, n, k, group, True, m + k)
+    scales[13, -1] = float("inf")
+    y = run(x, packed, scales, zp, None).float().cpu()
+    assert torch.isinf(y[:, 13]).all()
+    y[:, 13] = 0
+    assert torch.isfinite(y).all()
