@@ -807,18 +807,16 @@ hipError_t launch_int4_tile(const Int4Args& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
-  // One or two rows whose x fits in the lanes' registers (K to 8192, and 2048),
-  // where the row fills nine tenths of the lanes' segments.  The dot kernel
-  // against the streamed one: 151936 x 5120 (M = 1, 83 % filled) 88 and 86 us; 128256
-  // x 4096 at M = 2, K beyond the limit, 79 and 58 us.
+  // One or two rows whose x fits in the lanes' registers (K to 8192, and 2048).
+  // The dot kernel against the streamed one, M = 1: 151936 x 5120 80 and 84 us,
+  // 128256 x 6656 101 and 131, 128256 x 1280 in groups of 32 23 and 41, 1024 x 1280 3.3
+  // and 5.6; M = 2, 128256 x 2048: 32.2 and 32.7, beyond that K 128256 x 4096 75 and 53.
   const int64_t seg = ((int64_t)a.K + 2047) / 2048;
-  if (10 * (int64_t)a.K >= 9 * 2048 * seg) {
-    if (a.M == 1 && seg == 1) return launch_int4_dot<1, 1>(a, stream);
-    if (a.M == 1 && seg == 2) return launch_int4_dot<1, 2>(a, stream);
-    if (a.M == 1 && seg == 3) return launch_int4_dot<1, 3>(a, stream);
-    if (a.M == 1 && seg == 4) return launch_int4_dot<1, 4>(a, stream);
-    if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
-  }
+  if (a.M == 1 && seg == 1) return launch_int4_dot<1, 1>(a, stream);
+  if (a.M == 1 && seg == 2) return launch_int4_dot<1, 2>(a, stream);
+  if (a.M == 1 && seg == 3) return launch_int4_dot<1, 3>(a, stream);
+  if (a.M == 1 && seg == 4) return launch_int4_dot<1, 4>(a, stream);
+  if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
   if (a.M <= 16) return launch_int4_stream<1>(a, stream);
   // The tile kernel where one tile a wavefront gives two fifths of the compute
   // units a workgroup (64 x 12000 x 8192: 61 us, streamed 60; 33 x 16000 x 4096 26.5 and
