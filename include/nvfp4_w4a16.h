@@ -395,8 +395,11 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
  *   topk_weights[t, j] = score[t, e_j] (/ their sum over j, with renormalize) * weight_scale
  *   a[t, j] = silu(g) * u,  g = w1_e x[t],  u = w3_e x[t]        (w13 rows 0..I, I..2I)
  *   out[t] = bf16_rne( sum_j topk_weights[t, j] * w2_e a[t, j] )
- * float32 sums of exact products; a is kept to 16 bits (a bf16 pair), only out
- * is rounded to bf16.  A chosen expert's weights are read once, the others' not
+ * float32 sums of exact products.  Where H and I are multiples of 32 from 64 on, the
+ * activations enter the products as 11-bit floats scaled by powers of two: x
+ * unchanged (what is below 2^-28 of the largest value near it loses bits), a
+ * rounded to 11 bits; with other sizes x is unchanged and a is kept to 16 bits (a
+ * bf16 pair).  The only other rounding is out's to bf16.  A chosen expert's weights are read once, the others' not
  * at all.  An expert whose logit is -inf or NaN is never chosen; a slot left
  * without an expert has id -1, weight 0 and adds nothing.
  *
@@ -435,8 +438,8 @@ nvfp4_status nvfp4_moe_w4a16_decode(const void* x, int64_t T, int64_t H, const v
  * activation rows:
  *   y[m, n] = bf16_rne( sum_j scale[n, j] * sum_{k in group j} x[m, k] * (code[n, k] - zero[n, j]) + bias[n] )
  * The sums are float32 over exact products (a group's sum holds
- * sum x * (128 + code) and -(128 + zero) * sum x); summation order is
- * unspecified but deterministic.
+ * sum x * (128 + code) and -(128 + zero) * sum x, so a non-finite activation makes
+ * its row non-finite); summation order is unspecified but deterministic.
  *
  *   x            in  bf16 [M, K], 16-byte aligned; M >= 0 (M == 0 enqueues nothing, x and y may
  *                    then be NULL).  Beyond 64 rows the weight is read once per 64 rows.

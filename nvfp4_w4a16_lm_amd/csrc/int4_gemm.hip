@@ -214,12 +214,16 @@ __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
 // to 16 rows; one buffer and two barriers beyond, where LDS is short).  K
 // beyond W NC chunks is taken in phases over the same tiles, whose sums wait in
 // LDS meanwhile.  NG: scales per 128 k (4, 2: groups of 32, 64; 1: groups of a
-// multiple of 128, or one group per row).
+// multiple of 128, or one group per row).  Up to 16 rows HBM bounds it (16 x 151936 x
+// 5120, zero points: 84 us, 4.9 TB/s; weights loaded to registers in the MFMA's layout,
+// four lanes a row: 216), beyond that, where few weight rows leave this form the
+// only one that fills the card, the unpacking and the sums through LDS (64 x 8000 x
+// 8192: 53 us).
 // ---------------------------------------------------------------------------
 // Wavefronts per workgroup: the x fragments take 32 MT NC registers of each lane.
-// Sum buffers, and tiles in flight per wavefront: LDS that the sums held from
-// phase to phase need is worth more there (M = 64, 128256 x 4096: 209 us with two
-// buffers and three tiles).
+// Sum buffers, and tiles in flight per wavefront: beyond 16 rows the LDS that the
+// sums held from phase to phase need is worth more (M = 64, 128256 x 4096, before
+// the tile kernel took that size: 210 us with two buffers and three tiles, 155 so).
 constexpr int i4_buffers(int mt) { return mt == 1 ? 2 : 1; }
 constexpr int i4_depth(int mt) { return mt == 1 ? 3 : 2; }
 constexpr int i4_max_waves(int mt, int nc) { return mt * nc == 1 ? 16 : mt * nc == 2 ? 11 : 8; }

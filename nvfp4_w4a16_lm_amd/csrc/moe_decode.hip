@@ -7,17 +7,22 @@
 // equal ones by the lower index, and
 //   out[t] = sum_j w[t, j] W2_e (silu(W1_e x[t]) * (W3_e x[t])),  e = ids[t, j].
 //
-// moe_decode_up_kernel: every workgroup routes all tokens by itself (a few
-//   hundred logits, one wavefront per token; cheaper than a launch), lists the
-//   chosen experts in order and walks its share of (expert, 16 columns of I):
-//   one wavefront holds the gate and the up rows of the same 16 columns, so
-//   the activation is applied in its registers.
-// moe_decode_down_kernel: a workgroup owns 16 output columns; its wavefronts
-//   split the K = I of all chosen experts, each expert's sum is weighted by
-//   w[t, j] as it ends, so nothing per pair is written.
-//
+// Up kernels: every workgroup routes all tokens by itself (a few hundred
+// logits, one wavefront per token; cheaper than a launch), lists the chosen
+// experts in order and walks its share of (expert, 16 columns of I), gate and up
+// rows of the same columns together, so the activation is applied at once.
+// Down kernels: K = I of all chosen experts, each expert's sum weighted by w[t, j].
 // The MFMA's columns are the tokens themselves (16 at most), a token that did
 // not choose the expert is a column of zeros: no gathering, no lists of pairs.
+//
+// HBM bounds both: 0.5625 bytes per weight of the chosen experts.  The streamed form
+// (further down) serves H and I that are multiples of 32, from 64.  8 experts, 4096 x
+// 14336, top-2: T = 1 49 us (198 MB, 4.0 TB/s: 28 us up, 21 us down), T = 16 163 us
+// (785 MB, 4.8 TB/s); 64 experts of 2048 x 1024, T = 4 34 us.  The register form here
+// serves the other sizes (at T = 1, 16 of the first layer it took 65 and 211 us).
+//
+// Register form.  A workgroup of the down kernel owns 16 output columns, its
+// wavefronts split the K of all chosen experts, nothing per pair is written.
 // Weights stream straight to registers, one 256-k chunk ahead: lane (r, g) =
 // (lane % 16, lane / 16) holds row r's codes of k = 256 c + 64 g + [0, 64) (two
 // 16-byte loads) and their four block scales (one 4-byte load); MFMA step s
@@ -432,7 +437,8 @@ __global__ __launch_bounds__(64 * kMdDownWaves) void moe_decode_down_kernel(MoeD
 // A wavefront keeps the activations of its chunks as f16 MFMA operands, scaled by a power
 // of two of its own per token, chosen so that the largest magnitude among its
 // k lands in [2^14, 2^15): a bf16 value down to 2^-28 of that largest one stays
-// exact, a float32 one keeps 11 bits.  The wavefront's sums are scaled back
+// exact, a float32 one (the hidden activation, which is stored as float32) is
+// rounded to 11 bits, three more than the output keeps.  The wavefront's sums are scaled back
 // before they meet the others', so the scales need not agree.  In f16 a code
 // times its block scale costs half of what it costs in bf16 (and is as exact).
 // ---------------------------------------------------------------------------

@@ -41,8 +41,9 @@ def layer(x_bits, ids, w, w13, w2):
     """(out [T, H], bound [T, H]) for given routing; ids of -1 add nothing.
 
     Bound: h = float32 sums of K exact products (MFMA may truncate: 2 u each);
-    through silu'(g) u and silu(g); a's float32 evaluation (2^-20) and its bf16
-    pair (2^-17); the second product's float32 sum; the weights (48 u: a
+    through silu'(g) u and silu(g); a's float32 evaluation (2^-20) and its rounding
+    to 11 bits (2^-11) where the sizes take the f16 operands, to a bf16 pair
+    (2^-17) elsewhere; the second product's float32 sum; the weights (48 u: a
     softmax and a division) and the weighted sum; half a bf16 step, 2^-8."""
     live = ids >= 0
     ref = MO.moe_ref(x_bits, np.where(live, ids, 0), np.where(live, w, 0.0).astype(np.float32), w13, w2)
@@ -50,6 +51,7 @@ def layer(x_bits, ids, w, w13, w2):
     h, a, o = ref["h"], ref["a"], ref["o"]
     i = h.shape[1] // 2
     K1 = x_bits.shape[1]
+    round_a = 2.0 ** -11 if K1 % 32 == i % 32 == 0 and min(K1, i) >= 64 else 2.0 ** -17
     wl = np.where(live, w, 0.0)
     out = np.einsum("tj,tjh->th", wl, o.reshape(T, k, -1))
     dh = (K1 + 4) * 2 * U * ref["h_abs"]
@@ -57,7 +59,7 @@ def layer(x_bits, ids, w, w13, w2):
     g, u = h[:, :i], h[:, i:]
     sg = 1.0 / (1.0 + np.exp(-np.clip(g, -700, 700)))
     slope = np.abs(sg * (1.0 + g * (1.0 - sg))) + 0.1 * dg
-    da = slope * np.abs(u) * dg + np.abs(MO.silu(g)) * du + dg * du + (2.0 ** -17 + 2.0 ** -20) * np.abs(a)
+    da = slope * np.abs(u) * dg + np.abs(MO.silu(g)) * du + dg * du + (round_a + 2.0 ** -20) * np.abs(a)
     do, mag = np.zeros_like(o), np.zeros_like(o)
     for e, rows in enumerate(ref["groups"]):
         if rows.size:
