@@ -529,7 +529,7 @@ hipError_t launch_int4_dot(const Int4Args& a, hipStream_t stream) {
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// More than 16 activation rows on enough weight rows: a wavefront owns NT 16-row tiles
+// Enough weight rows, more than 16 activation rows or as the launcher says: a wavefront owns NT 16-row tiles
 // for all of K, so its sums stay in its registers.  The eight wavefronts of a
 // workgroup share x, 256 k a step in two LDS buffers, in the order that the MFMA
 // reads it; the weights come through each wavefront's own ring of two chunks, its
@@ -540,7 +540,8 @@ hipError_t launch_int4_dot(const Int4Args& a, hipStream_t stream) {
 // of either at 33 x 32000 x 4096 before the unpacking was cut from 11 to 7
 // instructions a word): two tiles share each x fragment where the grid still fills the
 // card.  33 x 32003 x 2080, groups of 32 with zero points: 27 us, 44 in the streamed
-// form; 64 x 128256 x 4096: 113 us (2.4 TB/s, 600 TFLOP/s) against 153, one tile 148.
+// form; 64 x 128256 x 4096: 113 us (2.4 TB/s, 600 TFLOP/s) against 153, one tile 148;
+// 16 x 151936 x 5120 in groups of 32 with zero points 122 (4.0 TB/s) against 198.
 // ---------------------------------------------------------------------------
 template <int MT, int NT, int NG, bool ZP>
 __global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
@@ -790,8 +791,10 @@ hipError_t launch_int4_tiles(const Int4Args& a, const dim3& blocks, hipStream_t 
          : ng == 2 ? (const void*)int4_tile_kernel<MT, NT, 2, false>
                    : (const void*)int4_tile_kernel<MT, NT, 1, false>;
   const int lds = 2 * MT * 8192 + 8 * 2 * NT * kSt4Bytes + (ng == 1 ? 256 * MT : 0) + 8 * 64 * NT * (2 * ng + 1);
-  const hipError_t e = ensure_dynamic_lds(fn, current_device(), lds);
-  if (e != hipSuccess) return e;
+  if (lds > 65536) {
+    const hipError_t e = ensure_dynamic_lds(fn, current_device(), lds);
+    if (e != hipSuccess) return e;
+  }
   return launch_kernel_lds(fn, blocks, dim3(512), (size_t)lds, stream, a);
 }
 
@@ -821,17 +824,25 @@ hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
   if (a.M == 1 && seg == 3) return launch_int4_dot<1, 3>(a, stream);
   if (a.M == 1 && seg == 4) return launch_int4_dot<1, 4>(a, stream);
   if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
-  if (a.M <= 16) return launch_int4_stream<1>(a, stream);
   // The tile kernel where one tile a wavefront gives two fifths of the compute
   // units a workgroup (64 x 12000 x 8192: 61 us, streamed 60; 33 x 16000 x 4096 26.5 and
-  // 27; 64 x 4096 x 4096 38 and 26), and K leaves its 32-bit offsets in range.
+  // 27; 64 x 4096 x 4096 38 and 26; 16 x 14000 x 4096 15.7 and 16.8), and K leaves its
+  // 32-bit offsets in range.  Up to 16 rows in groups of 128 or more the streamed
+  // form, whose work divides evenly, keeps the sizes that would leave a second or
+  // later round of workgroups (two a compute unit) less than three quarters full:
+  // 16 x 151936 x 5120 97 us, tiles 106; 3 x 128256 x 2048, two full rounds, 31 and 27.
   const int64_t cus = device_cus(current_device());
-  const int64_t mblocks = a.M <= 48 ? 1 : ((int64_t)a.M + 63) / 64;
-  if (5 * (((int64_t)a.N + 127) / 128) * mblocks >= 2 * cus && a.K <= 1 << 22) {
-    if (a.M <= 32) return launch_int4_tile<2>(a, stream);
-    if (a.M <= 48) return launch_int4_tile<3>(a, stream);
-    return launch_int4_tile<4>(a, stream);
+  const int64_t nblocks = ((int64_t)a.N + 127) / 128, mblocks = a.M <= 48 ? 1 : ((int64_t)a.M + 63) / 64;
+  if (5 * nblocks * mblocks >= 2 * cus && a.K <= 1 << 22) {
+    const int64_t over = nblocks % (2 * cus);
+    const bool uneven = nblocks > 2 * cus && over != 0 && 2 * over < 3 * cus;
+    const bool small_groups = a.group < 128 && a.K > a.group;
+    if (a.M <= 16 && (small_groups || !uneven)) return launch_int4_tiles<1, 1>(a, dim3((unsigned)nblocks), stream);
+    if (a.M > 16 && a.M <= 32) return launch_int4_tile<2>(a, stream);
+    if (a.M > 32 && a.M <= 48) return launch_int4_tile<3>(a, stream);
+    if (a.M > 48) return launch_int4_tile<4>(a, stream);
   }
+  if (a.M <= 16) return launch_int4_stream<1>(a, stream);
   if (a.M <= 32) return launch_int4_stream<2>(a, stream);
   if (a.M <= 48) return launch_int4_stream<3>(a, stream);
   return launch_int4_stream<4>(a, stream);

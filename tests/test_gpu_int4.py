@@ -159,3 +159,12 @@ def test_infinite_scale_of_the_last_group(m, n, k, group):
     assert torch.isinf(y[:, 13]).all()
     y[:, 13] = 0
     assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("m,n,k,group", [(2, 13201, 2336, 32), (3, 13313, 96, 32), (16, 14001, 160, 32), (9, 13500, 320, 64),
+                                         (5, 16384, 1152, 384), (4, 20011, 544, 544), (16, 40001, 288, 32),
+                                         (8, 99999, 128, 128), (8, 66000, 256, 128)])
+def test_few_rows_on_many(m, n, k, group, zeros):
+    """Up to 16 activation rows: the tile kernel, and the streamed one where its rounds would be uneven (66000)."""
+    check(m, n, k, group, zeros, seed=m + n + k + group, bias=(n % 2 == 1))
