@@ -500,12 +500,32 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
 template <int DT>
 __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(LogprobsArgs a) {
   __shared__ Key sh_keys[kJoinWaves][64];
+  __shared__ Sums sh_sums;
+  __shared__ int sh_larger;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t i = blockIdx.x;
   const int kk = a.topk;
   bool given;                                            // looked up now, used at the end
   const float xt = token_logit<DT>(a, a.x + i * a.row_stride * Elem<DT>::kBytes, i, &given);
   const float invt = inv_temperature(a.temps, i);
+  // the last wavefront adds the sums while the others merge lists, or the first where there are none
+  const bool adds = wave == (kk > 0 ? kJoinWaves - 1 : 0);
+  LogprobsPart first = {kM2Init, 0.0f, 0.0f, -INFINITY, 0, {0, 0, 0}};
+  if (adds && lane < a.segs) first = a.parts[i * a.segs + lane];
+  Sums q;
+  int count;
+  auto add_parts = [&]() {
+    q = Sums{first.m2, first.s, first.t, first.raw};
+    count = first.larger;
+    for (int g = lane + 64; g < a.segs; g += 64) {
+      const LogprobsPart p = a.parts[i * a.segs + g];
+      q = combine(q, Sums{p.m2, p.s, p.t, p.raw});
+      count += p.larger;
+    }
+    q = wave_combine(q);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) count += __shfl_xor(count, d, 64);
+  };
   Key key = {0u, 0u};
   if (kk > 0) {
     const Key* const lists = reinterpret_cast<const Key*>(a.part_keys) + i * a.segs * kk;
@@ -521,20 +541,20 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
       if (wave < half) {
         key = list_merge(key, sh_keys[wave + half][lane], lane);
         sh_keys[wave][lane] = key;
+      } else if (half == kJoinWaves / 2 && adds) {
+        add_parts();
+        if (lane == 0) {
+          sh_sums = q;
+          sh_larger = count;
+        }
       }
     }
+    q = sh_sums;
+    count = sh_larger;
+  } else if (adds) {
+    add_parts();
   }
   if (wave != 0) return;
-  Sums q = {kM2Init, 0.0f, 0.0f, -INFINITY};
-  int count = 0;
-  for (int g = lane; g < a.segs; g += 64) {
-    const LogprobsPart p = a.parts[i * a.segs + g];
-    q = combine(q, Sums{p.m2, p.s, p.t, p.raw});
-    count += p.larger;
-  }
-  q = wave_combine(q);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) count += __shfl_xor(count, d, 64);
   finish_row<DT>(a, i, q, count, key, given, xt, invt, lane);
 }
 
