@@ -27,8 +27,8 @@
 //
 // Many rows: 2048 x 128256 bf16 110 us (4.8 TB/s; the vector units are 80 % busy with
 // about 15 operations a logit, HBM close behind).  Few rows: launches and the
-// lists; one row 14 us (9 us the segments, of which most is the first loads and the
-// sort, 6 us the join), 64 x 151936 masked with 20 alternatives 25 us, 333 x 32003
+// lists; one row 13 us (9 us the segments, of which most is the first loads and the
+// sort, 5 us the join), 64 x 151936 masked with 20 alternatives 25 us, 333 x 32003
 // float32 with 64 alternatives 35 us (1.2 TB/s; most of it the lists).
 //
 // Backward.  d logprob / dz_j = 1[j = id] - p_j, dH / dz_j = -p_j (log p_j + H),
