@@ -168,3 +168,29 @@ def test_infinite_scale_of_the_last_group(m, n, k, group):
 def test_few_rows_on_many(m, n, k, group, zeros):
     """Up to 16 activation rows: the tile kernel, and the streamed one where its rounds would be uneven (66000)."""
     check(m, n, k, group, zeros, seed=m + n + k + group, bias=(n % 2 == 1))
+
+
+@pytest.mark.parametrize("m,n,k,group", [(1, 1003, 1024, 128), (40, 13999, 544, 32), (16, 16000, 1024, 64), (64, 33000, 256, 128)])
+def test_graph_replays_of_each_kernel(m, n, k, group):
+    x, packed, scales, zp, b = (None if t is None else (t if torch.is_tensor(t) else torch.from_numpy(t)).to(DEV)
+                                for t in make(m, n, k, group, True, 15, bias=True))
+    y = torch.empty((m, n), dtype=torch.bfloat16, device=DEV)
+    graph = capture(lambda: B.nvfp4_int4_gemm(x, packed, scales, zp, b, out=y))
+    for seed in (1, 2, 3):
+        x.copy_(torch.randn((m, k), generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        assert torch.equal(got, B.nvfp4_int4_gemm(x, packed, scales, zp, b))
+
+
+def test_another_stream():
+    x, packed, scales, zp, b = make(40, 14000, 512, 32, True, 16, bias=True)
+    want = run(x, packed, scales, zp, b)
+    dev = [(t if torch.is_tensor(t) else torch.from_numpy(t)).to(DEV) for t in (x, packed, scales, zp, b)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = B.nvfp4_int4_gemm(*dev)
+    side.synchronize()
+    assert torch.equal(got, want)
