@@ -673,7 +673,7 @@ int64_t logprobs_segments(int64_t M, int64_t V) {
 int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk) {
   const int64_t segs = logprobs_segments(M, V);
   if (segs == 1) return 16;
-  return M * segs * ((int64_t)sizeof(LogprobsPart) + 8 * topk);
+  return std::max<int64_t>(16, M * segs * ((int64_t)sizeof(LogprobsPart) + 8 * topk));   // 0 would be a refusal
 }
 
 hipError_t launch_logprobs(LogprobsArgs a, int dtype, int64_t M, void* workspace, hipStream_t stream) {

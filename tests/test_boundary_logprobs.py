@@ -111,3 +111,13 @@ def test_oracle_gradient_against_differences():
         d[:, j] = 1e-5
         assert np.allclose((loss(x + d) - loss(x - d)) / 2e-5, g[:, j], atol=1e-8)
     assert np.all(mag >= np.abs(g) - 1e-12)
+
+
+def test_workspace_of_every_accepted_size(lib):
+    """0 means a refusal, also through logprobs_buffers: an empty batch is none, whatever the vocabulary."""
+    for m in (0, 1, 2, 300, 1 << 23):
+        for v in (1, 3000, 4096, 4097, 128256, 1 << 30):
+            for topk in (0, 1, 64):
+                assert lib.nvfp4_logprobs_workspace_bytes(m, v, topk) >= 16, (m, v, topk)
+    b = B.logprobs_buffers(0, 128256, 5, "cpu")
+    assert b.lse.shape == (0,) and b.top_ids.shape == (0, 5)

@@ -304,3 +304,13 @@ def test_logprobs_graph_replays():
         torch.cuda.synchronize()
         for a, b in zip(got, [*eager[:6], edx]):
             assert torch.equal(a, b), f"replay {seed}"
+
+
+@pytest.mark.parametrize("v", [4097, 128256])
+def test_forward_empty_batch_of_a_long_vocabulary(v):
+    """V beyond one segment of a row, where an empty batch's workspace has no segments."""
+    x = torch.empty((0, v), dtype=BF16, device=DEV)
+    r = B.nvfp4_logprobs(x, torch.empty((0,), dtype=torch.int32, device=DEV), topk=3)
+    assert r.lse.shape == (0,) and r.top_ids.shape == (0, 3)
+    g = B.nvfp4_logprobs_backward(x, torch.empty((0,), dtype=torch.int32, device=DEV), r.lse, r.entropy)
+    assert g.shape == (0, v)
