@@ -24,6 +24,7 @@
 // step s covers the consecutive k = 128 c + 32 s + [0, 32) and lies in one group.
 #include <algorithm>
 
+#include "int4_groups.hpp"
 #include "nvfp4_device.hpp"
 #include "nvfp4_launch.hpp"
 #include "stream4.hpp"
@@ -256,8 +257,8 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
   for (int ph = 0; ph < phases; ++ph) {
     const int c0 = (ph * W + wave) * NC;                // this wavefront's first chunk
     // the phase's groups: [j0, j0 + gn) of each row
-    const int j0 = ph * W * NC * kSt4Chunk / a.group;
-    const int gn = min(a.groups, ((ph + 1) * W * NC * kSt4Chunk + a.group - 1) / a.group) - j0;
+    const I4Groups of = i4_groups(ph * W * NC * kSt4Chunk, W * NC * kSt4Chunk, K, a.group);
+    const int j0 = of.first, gn = of.count;
     int srow[SI], scol[SI];
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
