@@ -241,8 +241,10 @@ struct Sums {
   float raw;                                 // largest logit
 };
 
+// Beyond 2^-1000 the factor is 0 in float32; bounded there, since an infinite
+// distance, or one that overflows times s, would make t NaN.  A NaN stays in s.
 __device__ __forceinline__ void rescale(float& m2, float& s, float& t, float to) {
-  const float d = m2 - to;                   // <= 0
+  const float d = fmaxf(m2 - to, -1000.0f);  // <= 0
   const float a = __builtin_amdgcn_exp2f(d);
   t = __builtin_fmaf(s, d, t) * a;
   s *= a;

@@ -314,3 +314,21 @@ def test_forward_empty_batch_of_a_long_vocabulary(v):
     assert r.lse.shape == (0,) and r.top_ids.shape == (0, 3)
     g = B.nvfp4_logprobs_backward(x, torch.empty((0,), dtype=torch.int32, device=DEV), r.lse, r.entropy)
     assert g.shape == (0, v)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("v", [9, 1000, 5001, 40000])
+@pytest.mark.parametrize("temp", [None, 4.0])         # at 0.5 the log probability of -2^126 is -2^128, no float32
+def test_forward_sums_far_below_the_maximum(dtype, v, temp):
+    """Logits of +-2^126, whose scaling to base 2 is exact: the distance of an empty lane's sums, or
+    of many low logits', to a later maximum passes float32, and they count as zero."""
+    top = 2.0 ** 126
+    x = torch.full((4, v), -top, dtype=dtype, device=DEV)
+    x[0] = top                                           # uniform
+    x[1, v - 1] = 0.0                                    # all the others at -top
+    x[2, :v // 2] = 1.0
+    x[3, 0] = top
+    temps = None if temp is None else np.full(4, temp, np.float32)
+    for topk in (0, 5):
+        check_forward(x, np.int32([0, v - 1, 0, v - 1]), topk, temps)
+        check_forward(x, np.int32([1, 0, v - 1, 0]), topk, temps)
