@@ -4,10 +4,14 @@
 //
 // Forward.  For a row x[0..V) with temperature T, z = x / T, over the allowed
 // tokens: lse = log sum_j exp(z_j), logprob = z_id - lse, H = -sum_j p_j log p_j.
-// One pass over the row keeps, per lane, the running maximum and the two sums
-//   s = sum 2^(y_j),  t = sum 2^(y_j) y_j,   y_j = z_j log2(e) - m2,
-// rescaled when the maximum m2 grows (s' = s a, t' = (t + s (m2 - m2')) a with
-// a = 2^(m2 - m2')); then lse = m2 ln 2 + log s and H = log s - (t / s) ln 2.
+// One pass over the row keeps, per lane, the running maximum m and the two sums
+//   s = sum 2^(y_j),  t = sum 2^(y_j) y_j,   y_j = (x_j - m) log2(e) / T,
+// rescaled when the maximum grows (s' = s a, t' = (t + s d) a with d = (m - m') log2(e) / T
+// and a = 2^d); then lse = m / T + log s and H = log s - (t / s) ln 2.  The difference
+// comes first: scaled logits rounded on their own would leave up to |z| 2^-24 between a
+// logit and its own maximum, which no float32 power holds from |z| of 2^31 on (one
+// instruction a logit less, and NaN there).  Logits go to float32's largest, so half
+// the difference is taken, and twice the scale: no finite pair overflows.
 // The rank is a count of larger logits in the same pass.
 //
 // Top alternatives: each wavefront keeps its best 64 as one 64-bit key per
@@ -51,8 +55,8 @@ constexpr int kGroup16 = 16;                 // logits per lane and step
 constexpr int kJoinWaves = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLowest = -3.40282346638528859812e38f;
-constexpr float kM2Init = -3.0e38f;          // below every finite scaled maximum that matters, itself finite
+constexpr float kLargest = 3.40282346638528859812e38f;
+constexpr float kLowest = -kLargest;         // a maximum of nothing: s = 0 tells it from a row of this value
 
 constexpr int kBf16 = 0, kF16 = 1, kF32 = 2;
 
@@ -148,6 +152,17 @@ __device__ __forceinline__ float inv_temperature(const float* temps, int64_t row
   return t > 0.0f ? 1.0f / t : 1.0f;
 }
 
+// Twice log2(e) / T, from one division; a T so small that this overflows still
+// leaves every other logit 2^-1000 behind.
+__device__ __forceinline__ float base2_scale(const float* temps, int64_t row) {
+  if (!temps) return 2.0f * kLog2e;
+  const float t = temps[row];
+  return t > 0.0f ? fminf(2.0f * kLog2e / t, kLargest) : 2.0f * kLog2e;
+}
+
+// Half of x - m without overflow, given m / 2.
+__device__ __forceinline__ float half_difference(float x, float half_m) { return __builtin_fmaf(x, 0.5f, -half_m); }
+
 // ---------------------------------------------------------------------------
 // Sorted lists of 64 keys, one per lane, best first; 0 = empty.
 // ---------------------------------------------------------------------------
@@ -237,36 +252,34 @@ struct Candidates {
 
 // Softmax sums of a set of logits.
 struct Sums {
-  float m2, s, t;                            // scaled maximum, sum 2^y, sum 2^y y
-  float raw;                                 // largest logit
+  float raw, s, t;                           // largest logit, sum 2^y, sum 2^y y
 };
 
 // Beyond 2^-1000 the factor is 0 in float32; bounded there, since an infinite
 // distance, or one that overflows times s, would make t NaN.  A NaN stays in s.
-__device__ __forceinline__ void rescale(float& m2, float& s, float& t, float to) {
-  const float d = fmaxf(m2 - to, -1000.0f);  // <= 0
+__device__ __forceinline__ void rescale(Sums& q, float to, float c2) {
+  const float d = fmaxf(half_difference(q.raw, 0.5f * to) * c2, -1000.0f);  // <= 0
   const float a = __builtin_amdgcn_exp2f(d);
-  t = __builtin_fmaf(s, d, t) * a;
-  s *= a;
-  m2 = to;
+  q.t = __builtin_fmaf(q.s, d, q.t) * a;
+  q.s *= a;
+  q.raw = to;
 }
 
-__device__ __forceinline__ Sums combine(Sums a, Sums b) {
-  const float to = fmaxf(a.m2, b.m2);
-  rescale(a.m2, a.s, a.t, to);
-  rescale(b.m2, b.s, b.t, to);
-  return Sums{to, a.s + b.s, a.t + b.t, fmaxf(a.raw, b.raw)};
+__device__ __forceinline__ Sums combine(Sums a, Sums b, float c2) {
+  const float to = fmaxf(a.raw, b.raw);
+  rescale(a, to, c2);
+  rescale(b, to, c2);
+  return Sums{to, a.s + b.s, a.t + b.t};
 }
 
-__device__ __forceinline__ Sums wave_combine(Sums a) {
+__device__ __forceinline__ Sums wave_combine(Sums a, float c2) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
     Sums b;
-    b.m2 = __shfl_xor(a.m2, d, 64);
+    b.raw = __shfl_xor(a.raw, d, 64);
     b.s = __shfl_xor(a.s, d, 64);
     b.t = __shfl_xor(a.t, d, 64);
-    b.raw = __shfl_xor(a.raw, d, 64);
-    a = combine(a, b);
+    a = combine(a, b, c2);
   }
   return a;
 }
@@ -292,69 +305,22 @@ __device__ __forceinline__ float token_logit(const LogprobsArgs& a, const uint8_
   return x;
 }
 
-// A row whose scaled maximum overflows although its logits are finite (only
-// logits of about the type's largest magnitude): the differences to the
-// maximum are taken before the scaling, and z in the units of raw / T.
-// One wavefront walks the row; rare, so it is plain.
-template <int DT>
-__device__ void extreme_row(const LogprobsArgs& a, const uint8_t* row, int64_t i, float raw, float c, int lane,
-                            float* s_out, float* t_out) {
-  float s = 0.0f, t = 0.0f;
-  for (int j = lane; j < a.V; j += 64) {
-    const float x = Elem<DT>::value(Elem<DT>::bits(row + (int64_t)j * Elem<DT>::kBytes));
-    if (a.allowed && !((a.allowed[i * a.mask_words + (j >> 5)] >> (j & 31)) & 1u)) continue;
-    const float y = (x - raw) * c;
-    const float e = __builtin_amdgcn_exp2f(y);
-    s += e;
-    t = __builtin_fmaf(e, fmaxf(y, -1000.0f), t);
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    s += __shfl_xor(s, d, 64);
-    t += __shfl_xor(t, d, 64);
-  }
-  *s_out = s;
-  *t_out = t;
-}
-
 // The row's outputs from its sums, count and list (one wavefront); xt = the
 // given token's logit, if there is one.
-template <int DT>
 __device__ __forceinline__ void finish_row(const LogprobsArgs& a, int64_t i, Sums q, int larger, Key k, bool given,
                                            float xt, float invt, int lane) {
-  const uint8_t* const row = a.x + i * a.row_stride * Elem<DT>::kBytes;
-  const float c = invt * kLog2e;
-  const bool empty = q.raw == -INFINITY && !(q.s != q.s);     // nothing allowed or finite, and no NaN
-  float m = q.m2 * kLn2;                                       // the maximum of z
-  float s = q.s, t = q.t;
-  // relative to m2, as the sums are; a logit that overflows once scaled to
-  // base 2 is far below the maximum and is taken relative to it as it stands
-  auto logprob = [&](float x, float logs) {
-    if (!(fabsf(x * c) < INFINITY)) return (x - q.raw) * invt - logs;
-    return __builtin_fmaf(__builtin_fmaf(x, c, -q.m2), kLn2, -logs);
-  };
-  float logs, lse, ent;
-  const bool extreme = fabsf(q.raw) < INFINITY && !(fabsf(q.raw * c) < 3.0e38f);
-  if (extreme) {
-    extreme_row<DT>(a, row, i, q.raw, c, lane, &s, &t);
-    m = q.raw * invt;
-  }
-  logs = logf(s);
-  lse = m + logs;
-  ent = logs - t / s * kLn2;
-  if (empty) {
-    lse = -INFINITY;
-    ent = 0.0f;
-  }
+  const bool empty = q.s == 0.0f;            // nothing allowed or finite, and no NaN: a maximum adds 1
+  const float logs = logf(q.s);
   auto lp_of = [&](float x) {
     if (empty) return -INFINITY;
-    return extreme ? (x - q.raw) * invt - logs : logprob(x, logs);
+    const float z = x == -INFINITY ? x : 2.0f * (half_difference(x, 0.5f * q.raw) * invt);
+    return z - logs;
   };
   if (lane == 0) {
     if (a.token_logprob) a.token_logprob[i] = given ? lp_of(xt) : 0.0f;
     if (a.token_rank) a.token_rank[i] = given ? larger + 1 : 0;
-    if (a.lse) a.lse[i] = lse;
-    if (a.entropy) a.entropy[i] = ent;
+    if (a.lse) a.lse[i] = empty ? -INFINITY : __builtin_fmaf(q.raw, invt, logs);
+    if (a.entropy) a.entropy[i] = empty ? 0.0f : logs - q.t / q.s * kLn2;
   }
   if (lane < a.topk) {
     const bool some = k.hi != 0;
@@ -383,9 +349,10 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
   bool given;
   const float xt_lane = token_logit<DT>(a, row, i, &given);
   const float xt = given ? xt_lane : INFINITY;           // without a token nothing is larger
-  const float invt = inv_temperature(a.temps, i), c = invt * kLog2e;
+  const float c2 = base2_scale(a.temps, i);
 
-  float m2 = kM2Init, s = 0.0f, t = 0.0f, raw = -INFINITY;
+  Sums q = {kLowest, 0.0f, 0.0f};
+  float half = 0.5f * kLowest;
   int larger = 0;
   const int kk = a.topk;
   Candidates cand = {sh_keys[wave], 0, kLowest};         // -inf and NaN never pass
@@ -424,15 +391,16 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
       gb = fmaxf(gb, f[kGroup16 / 2 + e]);
     }
     const float g = fmaxf(ga, gb);
-    raw = fmaxf(raw, g);
-    const float top = g * c;
-    if (top > m2) rescale(m2, s, t, top);
+    if (g > q.raw) {
+      rescale(q, g, c2);
+      half = 0.5f * g;
+    }
 #pragma unroll
     for (int e = 0; e < kGroup16; ++e) {
-      const float y = __builtin_fmaf(f[e], c, -m2);
+      const float y = half_difference(f[e], half) * c2;
       const float p = __builtin_amdgcn_exp2f(y);
-      s += p;
-      t = __builtin_fmaf(p, fmaxf(y, -1000.0f), t);      // 2^y is 0 there; a NaN stays in s
+      q.s += p;
+      q.t = __builtin_fmaf(p, fmaxf(y, -1000.0f), q.t);  // 2^y is 0 there; a NaN stays in s
       larger += __popcll(__ballot(f[e] > xt));
     }
     if (kk > 0 && __ballot(g >= cand.thr) != 0) {
@@ -465,7 +433,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
   }
 
   // wavefronts -> workgroup
-  const Sums q = wave_combine(Sums{m2, s, t, raw});
+  q = wave_combine(q, c2);
   if (lane == 0) {
     sh_sums[wave] = q;
     sh_larger[wave] = larger;
@@ -481,7 +449,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
   int count = sh_larger[0];
 #pragma unroll
   for (int w = 1; w < kLpWaves; ++w) {
-    total = combine(total, sh_sums[w]);
+    total = combine(total, sh_sums[w], c2);
     count += sh_larger[w];
   }
   if (kk > 0) {
@@ -489,11 +457,11 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_kernel(LogprobsArgs a) {
     for (int w = 1; w < kLpWaves; ++w) key = list_merge(key, sh_keys[w][lane], lane);
   }
   if (a.segs == 1) {
-    finish_row<DT>(a, i, total, count, key, given, xt_lane, invt, lane);
+    finish_row(a, i, total, count, key, given, xt_lane, inv_temperature(a.temps, i), lane);
     return;
   }
   LogprobsPart* const part = a.parts + blockIdx.x;
-  if (lane == 0) *part = LogprobsPart{total.m2, total.s, total.t, total.raw, count, {0, 0, 0}};
+  if (lane == 0) *part = LogprobsPart{total.raw, total.s, total.t, count};
   if (lane < kk) reinterpret_cast<Key*>(a.part_keys)[(int64_t)blockIdx.x * kk + lane] = key;
 }
 
@@ -509,22 +477,22 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
   const int kk = a.topk;
   bool given;                                            // looked up now, used at the end
   const float xt = token_logit<DT>(a, a.x + i * a.row_stride * Elem<DT>::kBytes, i, &given);
-  const float invt = inv_temperature(a.temps, i);
+  const float invt = inv_temperature(a.temps, i), c2 = base2_scale(a.temps, i);
   // the last wavefront adds the sums while the others merge lists, or the first where there are none
   const bool adds = wave == (kk > 0 ? kJoinWaves - 1 : 0);
-  LogprobsPart first = {kM2Init, 0.0f, 0.0f, -INFINITY, 0, {0, 0, 0}};
+  LogprobsPart first = {kLowest, 0.0f, 0.0f, 0};
   if (adds && lane < a.segs) first = a.parts[i * a.segs + lane];
   Sums q;
   int count;
   auto add_parts = [&]() {
-    q = Sums{first.m2, first.s, first.t, first.raw};
+    q = Sums{first.raw, first.s, first.t};
     count = first.larger;
     for (int g = lane + 64; g < a.segs; g += 64) {
       const LogprobsPart p = a.parts[i * a.segs + g];
-      q = combine(q, Sums{p.m2, p.s, p.t, p.raw});
+      q = combine(q, Sums{p.raw, p.s, p.t}, c2);
       count += p.larger;
     }
-    q = wave_combine(q);
+    q = wave_combine(q, c2);
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) count += __shfl_xor(count, d, 64);
   };
@@ -557,7 +525,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
     add_parts();
   }
   if (wave != 0) return;
-  finish_row<DT>(a, i, q, count, key, given, xt, invt, lane);
+  finish_row(a, i, q, count, key, given, xt, invt, lane);
 }
 
 // ---------------------------------------------------------------------------

@@ -172,9 +172,8 @@ hipError_t launch_moe_combine(const void* o, const float* w, int64_t T, int64_t 
 // Log probabilities of logits (logprobs.hip).  dtype: 0 bf16, 1 f16, 2 f32;
 // strides in elements; segs, seg_vecs, parts and part_keys are the launcher's.
 struct LogprobsPart {                       // one segment of a row
-  float m2, s, t, raw;
+  float raw, s, t;
   int32_t larger;
-  int32_t pad[3];
 };
 struct LogprobsArgs {
   const uint8_t* x;

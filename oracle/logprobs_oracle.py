@@ -68,10 +68,9 @@ def forward_bounds(x, temps=None, allowed=None):
     """Error bounds per row of the float32 computation: of log S (S = the sum
     relative to the maximum), of lse and of the entropy.
 
-    u = 2^-24 is float32's unit rounding.  1/T, log2(e) and their product
-    leave 3 u on each scaled difference to the maximum and the fused
-    multiply-add one more (the maximum's own rounding is the same in every
-    term and in lse, and cancels); a hardware 2^y is within 2 u; a lane adds
+    u = 2^-24 is float32's unit rounding.  The difference to the maximum, the
+    quotient log2(e) / T and their product leave 3 u on each scaled
+    difference, the constant a quarter more, 4 u in all; a hardware 2^y is within 2 u; a lane adds
     ceil(V / 256) terms one by one (at worst u each), may rescale its sums at
     every 16th (4 u), and the lanes join in fewer than 20 steps."""
     u = 2.0 ** -24

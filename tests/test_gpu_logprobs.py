@@ -332,3 +332,43 @@ def test_forward_sums_far_below_the_maximum(dtype, v, temp):
     for topk in (0, 5):
         check_forward(x, np.int32([0, v - 1, 0, v - 1]), topk, temps)
         check_forward(x, np.int32([1, 0, v - 1, 0]), topk, temps)
+
+
+LARGE = [3e9, 1e10, 1e15, 1e20, 1e30, 1e37, 5e37, 1.5e38]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("v", [9, 1000, 5001, 40000])
+@pytest.mark.parametrize("top", LARGE)
+def test_forward_logits_of_large_magnitude(dtype, v, top):
+    """Finite maxima and finite mask or padding values of any size, lanes full of them among the rows:
+    a sum is relative to its own maximum exactly, not to the rounded product of it and log2(e) / T."""
+    rng = np.random.default_rng(v)
+    x = make_logits(7, v, dtype, v + 5).contiguous()
+    x[0] = top                                           # uniform
+    x[1, :v - 1] = -top                                  # one ordinary logit
+    x[2, v // 2:] = -top
+    x[3] = -top
+    x[4, 0] = top
+    x[4, 1:] = -top
+    x[5][torch.from_numpy(rng.random(v) < 0.9).to(DEV)] = -top
+    x[6] = x[6] * (top / 16)
+    x[6, v // 3] = top
+    ids = rng.integers(0, v, 7).astype(np.int32)
+    for topk in (0, 5):
+        check_forward(x, ids, topk)
+        check_forward(x, ids, topk, np.float32([1.4, 0.8, 0.7, 2.0, 1.1, 0.9, 1.3]))
+    check_forward(x, ids, 3, np.float32([1.4, 0.8, 0.7, 2.0, 1.1, 0.9, 1.3]), rng.random((7, v)) < 0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("v", [9, 5001, 40000])
+@pytest.mark.parametrize("temp", [1e-5, 1e-8, 1e-10, 1e-20, 1e-36])
+def test_forward_low_temperatures(dtype, v, temp):
+    """Greedy but for the name: z = logits / T passes 2^30 and every logit stays apart from the largest."""
+    x = make_logits(4, v, dtype, v + 6)
+    x[1] = torch.round(x[1])                             # many equal maxima
+    x[2] = -x[2].abs() - 1.0
+    ids = x.argmax(1).to(torch.int32).cpu().numpy()
+    ids[3] = (ids[3] + 1) % v
+    check_forward(x, ids, 4, np.full(4, temp, np.float32))
