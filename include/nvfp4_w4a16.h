@@ -490,7 +490,8 @@ typedef enum {
  *   token_ids      in  optional int32 [M] (NULL = none); a row whose id is outside [0, V)
  *                      has no given token: logprob 0, rank 0
  *   temperatures   in  optional float [M] (NULL = 1); 1 / temperature must be finite; one that
- *                      is not > 0 (a greedy row) counts as 1
+ *                      is not > 0 (a greedy row) counts as 1; at +inf every allowed finite
+ *                      logit has z = 0
  *   allowed        in  optional uint32 [M, ceil(V / 32)]: token j is allowed if bit j % 32 of
  *                      word j / 32 is set; logits of the others are not looked at, whatever
  *                      they hold (NULL = all allowed)

@@ -56,6 +56,7 @@ constexpr int kJoinWaves = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLargest = 3.40282346638528859812e38f;
+constexpr float kLeast = 1.40129846432481707092e-45f;    // 2^-149
 constexpr float kLowest = -kLargest;         // a maximum of nothing: s = 0 tells it from a row of this value
 
 constexpr int kBf16 = 0, kF16 = 1, kF32 = 2;
@@ -153,11 +154,12 @@ __device__ __forceinline__ float inv_temperature(const float* temps, int64_t row
 }
 
 // Twice log2(e) / T, from one division; a T so small that this overflows still
-// leaves every other logit 2^-1000 behind.
+// leaves every other logit 2^-1000 behind.  At T = +inf it is float32's least value,
+// not 0: finite differences come to 2^-20 at most, and -inf stays -inf.
 __device__ __forceinline__ float base2_scale(const float* temps, int64_t row) {
   if (!temps) return 2.0f * kLog2e;
   const float t = temps[row];
-  return t > 0.0f ? fminf(2.0f * kLog2e / t, kLargest) : 2.0f * kLog2e;
+  return t > 0.0f ? fmaxf(fminf(2.0f * kLog2e / t, kLargest), kLeast) : 2.0f * kLog2e;
 }
 
 // Half of x - m without overflow, given m / 2.

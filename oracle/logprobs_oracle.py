@@ -25,7 +25,9 @@ def scaled(x: np.ndarray, temps, allowed):
     z = raw
     if temps is not None:
         t = np.asarray(temps, np.float64)
-        z = raw / np.where(t > 0, t, 1.0)[:, None]
+        z = np.full_like(raw, -np.inf)                   # -inf stays so under any temperature, +inf too
+        np.divide(raw, np.where(t > 0, t, 1.0)[:, None], out=z, where=raw > -np.inf)
+        z[np.isnan(raw)] = np.nan
     return raw, z
 
 

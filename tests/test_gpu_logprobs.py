@@ -372,3 +372,28 @@ def test_forward_low_temperatures(dtype, v, temp):
     ids = x.argmax(1).to(torch.int32).cpu().numpy()
     ids[3] = (ids[3] + 1) % v
     check_forward(x, ids, 4, np.full(4, temp, np.float32))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("v", [5, 1000, 4096, 5001, 40000])
+def test_forward_infinite_temperature(dtype, v):
+    """z = 0 for every finite logit, whether or not the row fills its last step: lse = log(count); what
+    is not allowed, or -inf, still counts for nothing."""
+    rng = np.random.default_rng(v)
+    m = 5
+    x = make_logits(m, v, dtype, v + 7).contiguous()
+    x[1, ::2] = float("-inf")
+    x[2] = float("-inf")
+    x[3, v // 2:] = torch.finfo(dtype).min
+    bits = rng.random((m, v)) < 0.5
+    bits[4] = False
+    temps = np.float32([np.inf, np.inf, np.inf, np.inf, 1.0])
+    ids = rng.integers(0, v, m).astype(np.int32)
+    for b in (None, bits):
+        r = check_forward(x, ids, 5, temps, b)
+        count = ((x > float("-inf")) & (True if b is None else torch.from_numpy(b).to(DEV)))[:2].sum(1)
+        assert torch.allclose(r.lse[:2].double(), count.double().log(), rtol=1e-6, atol=1e-6)
+        g = check_backward(x[:4], ids[:4], np.ones(4), np.full(4, 0.5), np.full(4, 0.25), temps[:4],
+                           None if b is None else b[:4])
+        assert not g.any()                               # 1 / T of anything
+    check_forward(x, ids, 5, np.full(m, 3e38, np.float32), bits)
