@@ -4,11 +4,20 @@ Each function keeps the name of the C entry point it wraps.  torch is used for
 device memory (allocating outputs, taking data pointers) and for the current
 HIP stream; every step of the computation runs in the library's kernels.
 There is no fallback: a missing library raises at first use.
+
+``stream`` is a torch stream or a raw HIP stream handle, the current stream if
+None.  With a stream given, what a call copies or allocates by itself (dense
+copies of its inputs, a workspace, outputs) is copied and allocated on that
+stream, and the outputs are kept from reuse until the caller's current stream
+is past them; ordering the two streams is the caller's part, as with torch's
+own operations under ``torch.cuda.stream``.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import NamedTuple
 
@@ -158,6 +167,38 @@ def _stream_of(t: torch.Tensor, stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream, device):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _on_its_stream(fn):
+    """Runs ``fn`` under the stream it is given, so that the torch work inside it
+    is on that stream: a dense copy of an input made on another one need not be
+    there yet, and a temporary of another one's pool may be handed out again, and
+    overwritten, as soon as the call returns."""
+    position = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[position] if len(args) > position else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        device = next((a.device for a in (*args, *kwargs.values()) if torch.is_tensor(a) and a.is_cuda), None)
+        if device is None:                               # refused below
+            return fn(*args, **kwargs)
+        caller = torch.cuda.current_stream(device)
+        with torch.cuda.stream(_torch_stream(stream, device)):
+            result = fn(*args, **kwargs)
+        for t in (result if isinstance(result, tuple) else (result,)):
+            if t is not None:
+                t.record_stream(caller)
+        return result
+    return call
+
+
 def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
@@ -178,6 +219,7 @@ def _check_out(t: torch.Tensor, shape, dtypes, device, what: str) -> None:
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
+@_on_its_stream
 def nvfp4_quantize(weight: torch.Tensor, stream=None):
     """bf16 [N, K] -> (packed uint8 [N, K/2], scales float8_e4m3fn [N, K/16], global_scale fp32 [])."""
     w = _as_bf16_2d(weight, "weight")
@@ -192,6 +234,7 @@ def nvfp4_quantize(weight: torch.Tensor, stream=None):
     return packed, scales, gs
 
 
+@_on_its_stream
 def nvfp4_refresh_inplace(weight: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                           global_scale: torch.Tensor, stream=None) -> None:
     """Re-quantize ``weight`` into the existing buffers (pointers unchanged)."""
@@ -208,6 +251,7 @@ def nvfp4_refresh_inplace(weight: torch.Tensor, packed: torch.Tensor, scales: to
                                      _stream_of(w, stream)))
 
 
+@_on_its_stream
 def nvfp4_w4a16_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                      global_scale: torch.Tensor, bias: torch.Tensor | None = None,
                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -239,6 +283,7 @@ class NVFP4NotLoadedError(RuntimeError):
     """Block scales still hold the NaN sentinel: the checkpoint never wrote them."""
 
 
+@_on_its_stream
 def nvfp4_fill_scale_sentinel(scales: torch.Tensor, k: int, stream=None) -> None:
     """Fill a [N, K/16] block-scale buffer with the e4m3fn NaN sentinel 0x7F."""
     if scales.dim() != 2 or scales.shape[1] * 16 != k:
@@ -250,6 +295,7 @@ def nvfp4_fill_scale_sentinel(scales: torch.Tensor, k: int, stream=None) -> None
            lib.nvfp4_fill_scale_sentinel(_ptr(scales), n, k, _stream_of(scales, stream)))
 
 
+@_on_its_stream
 def nvfp4_import_checkpoint(partition_scales: torch.Tensor, scales: torch.Tensor, k: int,
                             convention: str, global_scale: torch.Tensor | None = None,
                             flags: torch.Tensor | None = None, stream=None):
@@ -296,6 +342,7 @@ def check_import_flags(flags: torch.Tensor, what: str = "lm_head") -> int:
     return f
 
 
+@_on_its_stream
 def nvfp4_fp8_quantize_rows(a: torch.Tensor, q: torch.Tensor | None = None,
                             scales: torch.Tensor | None = None, stream=None):
     """bf16 [R, K] -> (float8_e4m3fn [R, K], float32 [R]): one E4M3 scale per
@@ -317,6 +364,7 @@ def nvfp4_fp8_quantize_rows(a: torch.Tensor, q: torch.Tensor | None = None,
     return q, scales
 
 
+@_on_its_stream
 def nvfp4_fp8_gemm(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor,
                    bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
@@ -343,6 +391,7 @@ def nvfp4_fp8_gemm(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w
     return out
 
 
+@_on_its_stream
 def nvfp4_quantize_activations(x: torch.Tensor, input_global_scale: torch.Tensor, stream=None):
     """bf16 [M, K] -> (packed uint8 [M, K/2], scales float8_e4m3fn [M, K/16]) with a
     given global scale (fp32 [] on the device, dequantization direction)."""
@@ -361,6 +410,7 @@ def nvfp4_quantize_activations(x: torch.Tensor, input_global_scale: torch.Tensor
     return packed, scales
 
 
+@_on_its_stream
 def nvfp4_w4a4_gemm(x_packed: torch.Tensor, x_scales: torch.Tensor, input_global_scale: torch.Tensor,
                     packed: torch.Tensor, scales: torch.Tensor, global_scale: torch.Tensor,
                     bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -401,6 +451,7 @@ def nvfp4_w4a4_gemm(x_packed: torch.Tensor, x_scales: torch.Tensor, input_global
 W4A4_SCRATCH_BYTES = 4 << 20
 
 
+@_on_its_stream
 def nvfp4_w4a4_gemm_noalloc(x_packed: torch.Tensor, x_scales: torch.Tensor, input_global_scale: torch.Tensor,
                             packed: torch.Tensor, scales: torch.Tensor, global_scale: torch.Tensor,
                             out: torch.Tensor, bias: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -462,6 +513,7 @@ def moe_collapse_w13_scale2(w13_weight_scale_2: torch.Tensor) -> torch.Tensor:
     return s[:, 0].contiguous()
 
 
+@_on_its_stream
 def nvfp4_moe_w4a16_gemm(x: torch.Tensor, topk_ids: torch.Tensor, row_div: int, packed: torch.Tensor,
                          scales: torch.Tensor, global_scales: torch.Tensor, out: torch.Tensor | None = None,
                          invalid_pairs: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -493,6 +545,7 @@ def nvfp4_moe_w4a16_gemm(x: torch.Tensor, topk_ids: torch.Tensor, row_div: int, 
     return out
 
 
+@_on_its_stream
 def nvfp4_moe_silu_and_mul(h: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """bf16 [P, 2I] -> bf16 [P, I]: silu(h[:, :I]) * h[:, I:]."""
     h = _as_bf16_2d(h, "h")
@@ -507,6 +560,7 @@ def nvfp4_moe_silu_and_mul(h: torch.Tensor, out: torch.Tensor | None = None, str
     return out
 
 
+@_on_its_stream
 def nvfp4_moe_combine(o: torch.Tensor, topk_weights: torch.Tensor, out: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """bf16 [T*topk, H] with float32 weights [T, topk] -> bf16 [T, H]."""
@@ -528,6 +582,7 @@ def nvfp4_moe_combine(o: torch.Tensor, topk_weights: torch.Tensor, out: torch.Te
     return out
 
 
+@_on_its_stream
 def nvfp4_moe_w4a16_forward(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
                             w13: tuple, w2: tuple, out: torch.Tensor | None = None,
                             invalid_pairs: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
@@ -586,6 +641,7 @@ def moe_decode_workspace(t: int, topk: int, e: int, h: int, i: int, device) -> t
     return torch.empty((need,), dtype=torch.uint8, device=device)
 
 
+@_on_its_stream
 def nvfp4_moe_w4a16_decode(x: torch.Tensor, router_logits: torch.Tensor, topk: int, w13: tuple, w2: tuple,
                            scoring: str = "softmax", renormalize: bool = True,
                            correction_bias: torch.Tensor | None = None, weight_scale: float = 1.0,
@@ -635,6 +691,7 @@ def nvfp4_moe_w4a16_decode(x: torch.Tensor, router_logits: torch.Tensor, topk: i
 # int4 weights with group scales
 # ---------------------------------------------------------------------------
 
+@_on_its_stream
 def nvfp4_int4_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                     zero_points: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -729,6 +786,7 @@ def _check_allowed(t, m: int, v: int, dev):
         _check_out(t, (m, (v + 31) // 32), (torch.int32, torch.uint32), dev, "allowed")
 
 
+@_on_its_stream
 def nvfp4_logprobs(logits: torch.Tensor, token_ids: torch.Tensor | None = None, topk: int = 0,
                    temperatures: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
                    out: Logprobs | None = None, stream=None) -> Logprobs:
@@ -762,6 +820,7 @@ def nvfp4_logprobs(logits: torch.Tensor, token_ids: torch.Tensor | None = None, 
     return out
 
 
+@_on_its_stream
 def nvfp4_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor | None, lse: torch.Tensor,
                             entropy: torch.Tensor | None = None, dlogprob: torch.Tensor | None = None,
                             dentropy: torch.Tensor | None = None, dlse: torch.Tensor | None = None,
