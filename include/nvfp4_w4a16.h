@@ -397,9 +397,9 @@ nvfp4_status nvfp4_moe_w4a16_forward(const void* x, int64_t T, int64_t H, const 
  *   out[t] = bf16_rne( sum_j topk_weights[t, j] * w2_e a[t, j] )
  * float32 sums of exact products.  Where H and I are multiples of 32 from 64 on, the
  * activations enter the products as 11-bit floats scaled by powers of two: x
- * unchanged (what is below 2^-28 of the largest value near it loses bits), a
- * rounded to 11 bits; with other sizes x is unchanged and a is kept to 16 bits (a
- * bf16 pair).  The only other rounding is out's to bf16.  A chosen expert's weights are read once, the others' not
+ * unchanged, a as a pair of them that keeps 20 bits (of either, what is below 2^-28
+ * of the largest value near it loses bits); with other sizes x is unchanged and a is
+ * kept to 16 bits (a bf16 pair).  The only other rounding is out's to bf16.  A chosen expert's weights are read once, the others' not
  * at all.  An expert whose logit is -inf or NaN is never chosen; a slot left
  * without an expert has id -1, weight 0 and adds nothing.
  *

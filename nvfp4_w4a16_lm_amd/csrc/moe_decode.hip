@@ -437,8 +437,12 @@ __global__ __launch_bounds__(64 * kMdDownWaves) void moe_decode_down_kernel(MoeD
 // A wavefront keeps the activations of its chunks as f16 MFMA operands, scaled by a power
 // of two of its own per token, chosen so that the largest magnitude among its
 // k lands in [2^14, 2^15): a bf16 value down to 2^-28 of that largest one stays
-// exact, a float32 one (the hidden activation, which is stored as float32) is
-// rounded to 11 bits, three more than the output keeps.  The wavefront's sums are scaled back
+// exact; a float32 one (the hidden activation, which is stored as float32) takes two
+// operands, its first 11 bits and the next, which HBM hides (T = 16, 8 experts of 4096 x
+// 14336: 164 us, 167 with the first operand alone and the loop as it was; 64 experts of
+// 2048 x 1024 36.3 and 35.1).  Their registers leave none to spare: the activations are
+// loaded once for each run of tiles, not inside its steps, and addresses are 32-bit
+// offsets.  The wavefront's sums are scaled back
 // before they meet the others', so the scales need not agree.  In f16 a code
 // times its block scale costs half of what it costs in bf16 (and is as exact).
 // ---------------------------------------------------------------------------
@@ -470,12 +474,34 @@ __device__ __forceinline__ f16x8 pack_f16(const float* v, float down) {
   return h;
 }
 
+// The same as two parts of 11 bits each, the first cut (one conversion for two
+// values) and the second what that left, cut too: 20 bits at least.  What an infinite
+// value leaves is NaN; the minimum, which no finite rest (below 16) reaches, makes it a
+// number.
+__device__ __forceinline__ f16x8 pack_f16_pair(const float* v, float down, f16x8* rest) {
+  f16x8 h;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const auto hi = __builtin_amdgcn_cvt_pkrtz(v[e] * down, v[e + 1] * down);
+    h[e] = (_Float16)hi[0];
+    h[e + 1] = (_Float16)hi[1];
+    const auto lo = __builtin_amdgcn_cvt_pkrtz(fminf(__builtin_fmaf(v[e], down, -(float)h[e]), 16.0f),
+                                               fminf(__builtin_fmaf(v[e + 1], down, -(float)h[e + 1]), 16.0f));
+    (*rest)[e] = (_Float16)lo[0];
+    (*rest)[e + 1] = (_Float16)lo[1];
+  }
+  return h;
+}
+
 // Block scales of rows for the workgroup: thread `it` holds word it % words of row
 // it / words of a 16-row tile; nb = bytes of a row's scales.
+__device__ __forceinline__ int scale_word_offset(int word, int nb) { return min(4 * word, nb - 4); }
+__device__ __forceinline__ uint32_t scale_word(uint32_t loaded, int word, int nb) {
+  const int shift = 8 * (4 * word - scale_word_offset(word, nb));
+  return shift < 32 ? loaded >> shift : 0u;              // blocks past the row's end have scale 0
+}
 __device__ __forceinline__ uint32_t load_scale_word(const uint8_t* row, int word, int nb) {
-  const int off = min(4 * word, nb - 4), shift = 8 * (4 * word - off);
-  const uint32_t w = reinterpret_cast<const Word4A1*>(row + off)->v;
-  return shift < 32 ? w >> shift : 0u;                   // blocks past the row's end have scale 0
+  return scale_word(reinterpret_cast<const Word4A1*>(row + scale_word_offset(word, nb))->v, word, nb);
 }
 
 struct ScaleSplit {
@@ -493,14 +519,19 @@ __device__ __forceinline__ ScaleSplit split4(uint32_t w) {
   return o;
 }
 
-// acc += (tile chunk) x (activations of the chunk), k = 64 g + 8 s + [0, 8).
-__device__ __forceinline__ f32x4 chunk_product(u32x4 w0, u32x4 w1, uint32_t sw, const f16x8* xb, f32x4 acc) {
+// acc += (tile chunk) x (activations of the chunk, with their rests where PAIR),
+// k = 64 g + 8 s + [0, 8).
+template <bool PAIR>
+__device__ __forceinline__ f32x4 chunk_product(u32x4 w0, u32x4 w1, uint32_t sw, const f16x8* xb, const f16x8* rest,
+                                               f32x4 acc) {
   const ScaleSplit q = split4(sw);
   f32x4 odd = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
     const uint32_t w = s < 4 ? w0[s & 3] : w1[s & 3];
     const f16x8 a = dequant8_f16(w, q.s[s >> 1], q.mu[s >> 1]);
+    if (PAIR && (s & 1)) odd = mfma_md16(a, rest[s], odd);
+    if (PAIR && !(s & 1)) acc = mfma_md16(a, rest[s], acc);
     if (s & 1)
       odd = mfma_md16(a, xb[s], odd);
     else
@@ -512,6 +543,9 @@ __device__ __forceinline__ f32x4 chunk_product(u32x4 w0, u32x4 w1, uint32_t sw, 
 }
 
 constexpr int kMdDepth = 2;                  // tiles in flight per wavefront
+
+// Floats between two rows of the hidden activation: whole chunks.
+__device__ __host__ constexpr int64_t act_pitch(int64_t I) { return (I + kSt4Chunk - 1) / kSt4Chunk * kSt4Chunk; }
 
 // LDS words of a row's scales for W wavefronts of NC chunks, padded to spread the rows.
 __device__ __host__ constexpr int md_scale_pitch(int slots) { return 4 * slots + 1; }
@@ -678,7 +712,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
       copy_tile(here, slot);
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int q = 0; q < NC; ++q) acc = chunk_product(w[q][0], w[q][1], sw[q], xb[q], acc);
+      for (int q = 0; q < NC; ++q) acc = chunk_product<false>(w[q][0], w[q][1], sw[q], xb[q], nullptr, acc);
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[v] *= back;
       // the gate's sums wait in registers: between two units' writes to red lies
@@ -733,7 +767,7 @@ __global__ __launch_bounds__(1024) void moe_stream_up_kernel(MoeDecodeArgs a) {
         if (pair < 0) continue;
         const float gs = sh_gs[fslot];
         const float gv = sum[0] * gs, uv = sum[1] * gs;
-        a.act[(int64_t)pair * a.I + 16 * ftile + n] = gv / (1.0f + expf(-gv)) * uv;
+        a.act[(int64_t)pair * act_pitch(a.I) + 16 * ftile + n] = gv / (1.0f + expf(-gv)) * uv;
       }
       if (++ftile == tiles) {
         ftile = 0;
@@ -767,7 +801,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int W = blockDim.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int K = a.I, nb = K >> 4, P = a.T * a.topk;
+  const int K = a.I, nb = K >> 4, nch = (K + kSt4Chunk - 1) / kSt4Chunk, P = a.T * a.topk;
   const int64_t pitch = K >> 1;
   uint8_t* const ring = lds8 + wave * (D * NC * kSt4Bytes);
   float* const red = reinterpret_cast<float*>(lds8 + W * (D * NC * kSt4Bytes));          // [2][W][256]
@@ -827,21 +861,36 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     sword[i] = it - srow[i] * words;
   }
   uint32_t sv[D + 1][NC];                                 // the last entry: the first unit's
+  int sslice[D + 1];
+  // 32-bit offsets from the tile's first row: 16 rows of I / 2 bytes, I <= 2^29
   auto load_scales = [&](const Pos& p, int slot) {
     const uint8_t* const base = a.w2_scales + p.row * nb;
+    sslice[slot] = p.slice;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      sv[slot][i] = load_scale_word(base + (int64_t)srow[i] * nb, words * p.slice + sword[i], nb);
+      sv[slot][i] = reinterpret_cast<const Word4A1*>(
+                        base + (uint32_t)(srow[i] * nb + scale_word_offset(words * p.slice + sword[i], nb)))->v;
   };
+  // the word is cut when it is stored, a step later: here it would have to be waited for
   auto store_scales = [&](int u, int slot) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) scl[((u & 1) * 16 + srow[i]) * spitch + sword[i]] = sv[slot][i];
+    for (int i = 0; i < NC; ++i)
+      scl[((u & 1) * 16 + srow[i]) * spitch + sword[i]] = scale_word(sv[slot][i], words * sslice[slot] + sword[i], nb);
   };
-  auto copy_tile = [&](const Pos& p, int slot) {
+  const int piece = (lane & 7) ^ (lane >> 3);
+  const uint32_t roff = (uint32_t)(lane >> 3) * (uint32_t)pitch;
+  auto copy_tile = [&](const Pos& p, int slot) {           // as st4_copy
     const uint8_t* const base = a.w2_packed + p.row * pitch;
 #pragma unroll
-    for (int q = 0; q < NC; ++q)
-      st4_copy(base, pitch, 15, (p.slice * W + wave) * NC + q, ring + (slot * NC + q) * kSt4Bytes, lane);
+    for (int q = 0; q < NC; ++q) {
+      const int c = (p.slice * W + wave) * NC + q;
+      const uint32_t off = roff + (uint32_t)min(kSt4Chunk / 2 * c + 16 * piece, (int)pitch - 16);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_global_load_lds((const void*)(base + 8 * j * pitch + off),
+                                         (st4_lds_t)(ring + (slot * NC + q) * kSt4Bytes + 1024 * j), 16, 0,
+                                         2 /* nontemporal */);
+    }
   };
   Pos next = pos_of(u0), now = next;                       // fetched next; computed now
   load_scales(next, D);
@@ -855,12 +904,11 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
   store_scales(u0, D);
   st4_barrier();
 
-  f16x8 xb[NC][8];
+  f16x8 xb[NC][8], xr[NC][8];
   float back = 0.0f;
-  int combo = -1, out_pair = -1;                           // out_pair: of this thread's token in the sums
+  int out_pair = -1;                           // out_pair: of this thread's token in the sums
   // the activations of (expert, slice) c: column r is token r's pair with the expert, or zeros
   auto load_act = [&](const Pos& at) {
-    combo = at.combo;
     const int e = sh_list[at.combo / slices], c0 = (at.slice * W + wave) * NC;
     int pair = -1;
     out_pair = -1;
@@ -871,37 +919,35 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     if (ot < a.T)
       for (int j = 0; j < a.topk; ++j)
         if (sh_ids[ot * a.topk + j] == e) out_pair = ot * a.topk + j;
-    const float* const row = a.act + (int64_t)max(pair, 0) * K;
+    const float* const act = a.act + (int64_t)max(pair, 0) * act_pitch(K) + 64 * g;
     uint32_t mag = 0;
     float f[NC][8][8];
 #pragma unroll
-    for (int q = 0; q < NC; ++q)
+    for (int q = 0; q < NC; ++q) {
+      // rows are padded to whole chunks: what lies past K, or belongs to no pair, is replaced by zeros
+      const float* const row = act + (int64_t)kSt4Chunk * min(c0 + q, nch - 1);
+      const int have = pair >= 0 ? K - kSt4Chunk * (c0 + q) - 64 * g : 0;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const int k = kSt4Chunk * (c0 + q) + 64 * g + 8 * s;
-        f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-        if (pair >= 0 && k < K) {
-          lo = *reinterpret_cast<const f32x4*>(row + k);
-          hi = *reinterpret_cast<const f32x4*>(row + k + 4);
-        }
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(row + 8 * s), hi = *reinterpret_cast<const f32x4*>(row + 8 * s + 4);
 #pragma unroll
         for (int e2 = 0; e2 < 4; ++e2) {
-          f[q][s][e2] = lo[e2];
-          f[q][s][4 + e2] = hi[e2];
-          mag = max(mag, max(__float_as_uint(lo[e2]) & 0x7FFFFFFFu, __float_as_uint(hi[e2]) & 0x7FFFFFFFu));
+          f[q][s][e2] = 8 * s < have ? lo[e2] : 0.0f;
+          f[q][s][4 + e2] = 8 * s < have ? hi[e2] : 0.0f;
+          mag = max(mag, max(__float_as_uint(f[q][s][e2]) & 0x7FFFFFFFu, __float_as_uint(f[q][s][4 + e2]) & 0x7FFFFFFFu));
         }
       }
+    }
     const int p = scale_exponent(column_max(mag));
     back = pow2(p) * a.w2_gs[e] * (pair >= 0 ? sh_w[pair] : 0.0f);
     const float down = pow2(-p);
 #pragma unroll
     for (int q = 0; q < NC; ++q)
 #pragma unroll
-      for (int s = 0; s < 8; ++s) xb[q][s] = pack_f16(f[q][s], down);
+      for (int s = 0; s < 8; ++s) xb[q][s] = pack_f16_pair(f[q][s], down, &xr[q][s]);
   };
 
   auto step = [&](int u, int slot) {
-    if (now.combo != combo) load_act(now);                 // uniform over the workgroup
     __builtin_amdgcn_s_waitcnt(st4_vm((D - 1) * 3 * NC));
     __asm__ volatile("" ::: "memory");
     u32x4 w[NC][2];
@@ -921,7 +967,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     copy_tile(here, slot);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int q = 0; q < NC; ++q) acc = chunk_product(w[q][0], w[q][1], sw[q], xb[q], acc);
+    for (int q = 0; q < NC; ++q) acc = chunk_product<true>(w[q][0], w[q][1], sw[q], xb[q], xr[q], acc);
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] *= back;
     *reinterpret_cast<f32x4*>(red + ((u & 1) * W + wave) * 256 + 4 * lane) = acc;
@@ -943,10 +989,16 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     }
     advance(now);
   };
-  for (int u = u0; u < u1; u += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (u + d < u1) step(u + d, d);
+  // runs of one (expert, slice); a unit's ring slot is its parity in the workgroup's run
+  for (int u = u0; u < u1;) {
+    const int end = min(u1, u + tiles - now.tile);
+    load_act(now);
+    if ((u - u0) & 1) step(u++, 1);
+    for (; u + 1 < end; u += 2) {
+      step(u, 0);
+      step(u + 1, 1);
+    }
+    if (u < end) step(u++, 0);
   }
 
   // count the units; a tile is complete with active * slices of them.  The parts
@@ -1027,7 +1079,7 @@ int64_t moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t H, int64_t I
   const int64_t P = T * topk, split = down_split(H);
   const int64_t parts = streamed(H, I) ? stream_plan(I).passes * P * H * 4
                                        : (split > 1 ? H / 16 * split * 256 * 4 : 0);
-  return 3 * up256(P * 4) + 256 + up256(P * I * 4) + up256(H / 16 * 4) + parts;
+  return 3 * up256(P * 4) + 256 + up256(P * act_pitch(I) * 4) + up256(H / 16 * 4) + parts;
 }
 
 namespace {
@@ -1086,7 +1138,7 @@ hipError_t launch_moe_decode(MoeDecodeArgs a, void* workspace, hipStream_t strea
   a.weights = reinterpret_cast<float*>(take(P * 4));
   a.list = reinterpret_cast<int32_t*>(take(P * 4));
   a.active = reinterpret_cast<int32_t*>(take(4));
-  a.act = reinterpret_cast<float*>(take(P * a.I * 4));
+  a.act = reinterpret_cast<float*>(take(P * act_pitch(a.I) * 4));
   a.a_hi = reinterpret_cast<uint16_t*>(a.act);
   a.a_lo = a.a_hi + P * a.I;
   a.counters = reinterpret_cast<int32_t*>(take(a.H / 16 * 4));

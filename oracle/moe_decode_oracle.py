@@ -42,8 +42,8 @@ def layer(x_bits, ids, w, w13, w2):
 
     Bound: h = float32 sums of K exact products (MFMA may truncate: 2 u each);
     through silu'(g) u and silu(g); a's float32 evaluation (2^-20) and its rounding
-    to 11 bits (2^-11) where the sizes take the f16 operands, to a bf16 pair
-    (2^-17) elsewhere; the second product's float32 sum; the weights (48 u: a
+    to a pair of bf16 values (2^-17; the pairs of f16 that other sizes take keep
+    20 bits); the second product's float32 sum; the weights (48 u: a
     softmax and a division) and the weighted sum; half a bf16 step, 2^-8."""
     live = ids >= 0
     ref = MO.moe_ref(x_bits, np.where(live, ids, 0), np.where(live, w, 0.0).astype(np.float32), w13, w2)
@@ -51,7 +51,7 @@ def layer(x_bits, ids, w, w13, w2):
     h, a, o = ref["h"], ref["a"], ref["o"]
     i = h.shape[1] // 2
     K1 = x_bits.shape[1]
-    round_a = 2.0 ** -11 if K1 % 32 == i % 32 == 0 and min(K1, i) >= 64 else 2.0 ** -17
+    round_a = 2.0 ** -17
     wl = np.where(live, w, 0.0)
     out = np.einsum("tj,tjh->th", wl, o.reshape(T, k, -1))
     dh = (K1 + 4) * 2 * U * ref["h_abs"]

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import oracle.moe_decode_oracle as D
+import oracle.nvfp4_moe_oracle as MO
 from nvfp4_w4a16_lm_amd import binding as B
 from nvfp4_w4a16_lm_amd import workloads as wl
 
@@ -152,3 +153,95 @@ def test_graph_replays():
         got = [t.clone() for t in (out, ids, w)]
         for a, b in zip(got, B.nvfp4_moe_w4a16_decode(x, router, topk, w13, w2)):
             assert torch.equal(a, b), f"replay {seed}"
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 64, 64), (3, 2048, 256), (16, 512, 288), (2, 1024, 4640), (5, 48, 272)])
+def test_hidden_activations_keep_their_bits(T, H, I):
+    """Pairs of nearly equal hidden activations against weights of opposite signs: the output is about
+    2^-8 of its terms, and what the hidden activation loses in rounding shows in full.  Each token has
+    two activations and each expert three pairs of columns, so no sum has more than a few terms: its
+    float32 errors stay below 2^-18 of the terms, silu's and the routing weights' too, and the hidden
+    activation may lose 2^-17 of itself."""
+    E, cols = 2, np.array([0, I // 2 // 2 * 2, I - 2])
+    rng = np.random.default_rng(T + I)
+    code = lambda: rng.integers(1, 4, (E, 3)).astype(np.uint8) * 2         # 1, 2 or 4
+    p13, p2 = np.zeros((E, 2 * I, H // 2), np.uint8), np.zeros((E, H, I // 2), np.uint8)
+    k0, k1 = 6, H - 10                                   # even: low nibbles
+    p13[:, cols, k0 // 2] = p13[:, cols + 1, k0 // 2] = code()             # w1: columns 2 j and 2 j + 1 alike
+    p13[:, I + cols, k0 // 2] = p13[:, I + cols + 1, k0 // 2] = code()     # w3: but for its second term
+    p13[:, I + cols, k1 // 2] = code()
+    n = rng.integers(1, 8, (E, H, 3)).astype(np.uint8)
+    p2[:, :, cols // 2] = n | ((n | 8) << 4)             # opposite signs
+    s13, s2 = np.full((E, 2 * I, H // 16), 0x38, np.uint8), np.full((E, H, I // 16), 0x38, np.uint8)    # 1
+    w13, w2 = (p13, s13, np.float32([0.5, 0.25])), (p2, s2, np.float32([0.5, 1.0]))
+    x = np.zeros((T, H), np.float32)
+    x[:, k0] = rng.uniform(0.5, 1.5, T)
+    x[:, k1] = x[:, k0] * rng.uniform(0.5, 1.0, T) * 2.0 ** -8
+    xb = torch.from_numpy(x).to(torch.bfloat16)
+    x_bits = xb.view(torch.int16).numpy().view(np.uint16)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    out, ids, w = B.nvfp4_moe_w4a16_decode(xb.to(DEV), torch.from_numpy(logits).to(DEV), 2, upload(w13), upload(w2))
+    torch.cuda.synchronize()
+    want_ids, want_w = D.route(logits, 2)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    ref = MO.moe_ref(x_bits, want_ids, want_w.astype(np.float32), w13, w2)
+    want, mag = np.zeros((T, H)), np.zeros((T, H))
+    for t in range(T):
+        for j in range(2):
+            e, a = want_ids[t, j], ref["a"][2 * t + j]
+            want[t] += want_w[t, j] * (ref["w2deq"][e] @ a)
+            mag[t] += want_w[t, j] * (np.abs(ref["w2deq"][e]) @ np.abs(a))
+    err = np.abs(f64(out) - want)
+    bound = mag * (2.0 ** -17 + 3 * 2.0 ** -18) + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+    assert np.all(mag > 0) and np.median(bound / np.abs(want)) < 0.05
+    assert np.all(err <= bound), f"{(err > bound).mean():.3f} of the outputs, worst {(err / bound).max():.1f}"
+
+
+def random_experts(E, N, K, seed):
+    """Any codes, block scales of 0.25 to 1.875, global scales that keep outputs near 1."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    packed = torch.randint(0, 256, (E, N, K // 2), generator=g, device=DEV, dtype=torch.int16).to(torch.uint8)
+    scales = torch.randint(0x28, 0x40, (E, N, K // 16), generator=g, device=DEV, dtype=torch.int16).to(torch.uint8)
+    return packed, scales, (0.5 + torch.rand((E,), generator=g, device=DEV)) * 0.5 / K ** 0.5
+
+
+def dequant64(w, e):
+    lut = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64, device=DEV)
+    p = w[0][e]
+    codes = lut[torch.stack((p & 15, p >> 4), -1).int()].view(p.shape[0], -1, 16)
+    return (codes * w[1][e].view(torch.float8_e4m3fn).double().unsqueeze(2)).view(p.shape[0], -1) * w[2][e].double()
+
+
+@pytest.mark.parametrize("T,E,topk,H,I", [
+    (16, 32, 4, 8192, 2400),       # two passes over H, and more units than the sums of one workgroup a unit hold
+    (16, 24, 3, 4128, 4128),       # two passes over either
+    (7, 256, 8, 5120, 512), (3, 60, 4, 7168, 2048), (16, 128, 8, 2048, 768)])
+def test_many_experts(T, E, topk, H, I):
+    """Sizes of real layers, in float64 on the device, with the oracle's bound."""
+    w13, w2 = random_experts(E, 2 * I, H, 1), random_experts(E, H, I, 2)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn((T, H), generator=g, device=DEV).to(torch.bfloat16)
+    router = torch.randn((T, E), generator=g, device=DEV)
+    out, ids, w = B.nvfp4_moe_w4a16_decode(x, router, topk, w13, w2, scoring="sigmoid")
+    want_ids, want_w = D.route(router.cpu().double().numpy(), topk, "sigmoid")
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    wt = torch.from_numpy(want_w).to(DEV)
+    want, slack, u = torch.zeros((T, H), dtype=torch.float64, device=DEV), torch.zeros((T, H), dtype=torch.float64, device=DEV), D.U
+    for e in sorted(set(want_ids.flatten())):
+        t, j = (torch.from_numpy(a).to(DEV) for a in np.nonzero(want_ids == e))
+        d13, d2, xe = dequant64(w13, e), dequant64(w2, e), x[t].double()
+        h, dh = xe @ d13.t(), (H + 4) * 2 * u * (xe.abs() @ d13.abs().t())
+        (gate, up), (dg, du) = h.split(I, 1), dh.split(I, 1)
+        sg = torch.sigmoid(gate)
+        a = gate * sg * up
+        slope = (sg * (1 + gate * (1 - sg))).abs() + 0.1 * dg
+        da = slope * up.abs() * dg + (gate * sg).abs() * du + dg * du + (2.0 ** -17 + 2.0 ** -20) * a.abs()
+        mag = (a.abs() + da) @ d2.abs().t()
+        wj = wt[t, j].unsqueeze(1)
+        want.index_add_(0, t, wj * (a @ d2.t()))
+        slack.index_add_(0, t, wj * (da @ d2.abs().t() + ((I + 8) * 2 + 48 + topk) * u * mag))
+    err = (out.double() - want).abs()
+    assert torch.all(err <= slack + 2.0 ** -8 * want.abs() * (1 + 2.0 ** -7)), (err / slack).max()
+    # worst cases aside, an output is the nearest bf16 value or, where the sums' errors (about 2^-20 of
+    # the terms' norm) cross a border, its neighbour: a twentieth at most
+    assert (out != want.to(torch.bfloat16)).double().mean() < 0.05
