@@ -438,8 +438,8 @@ nvfp4_status nvfp4_moe_w4a16_decode(const void* x, int64_t T, int64_t H, const v
  * activation rows:
  *   y[m, n] = bf16_rne( sum_j scale[n, j] * sum_{k in group j} x[m, k] * (code[n, k] - zero[n, j]) + bias[n] )
  * The sums are float32 over exact products (a group's sum holds
- * sum x * (128 + code) and -(128 + zero) * sum x, so a non-finite activation makes
- * its row non-finite); summation order is unspecified but deterministic.
+ * sum x * (16 + code) and -(16 + zero) * sum x, so a non-finite activation makes
+ * its row non-finite, and so may finite ones whose sum passes float32 / 31); summation order is unspecified but deterministic.
  *
  *   x            in  bf16 [M, K], 16-byte aligned; M >= 0 (M == 0 enqueues nothing, x and y may
  *                    then be NULL).  Beyond 64 rows the weight is read once per 64 rows.

@@ -5,15 +5,18 @@
 // eight codes per 32-bit word along K, low nibble first; scales [N, K / group]
 // in bf16 or f16; zero points eight rows per word along N, or none (z = 8).
 //
-// A code q becomes the bf16 value 128 + q by one and-or (0x4300 | q: at
-// exponent 2^7 the last mantissa bit is worth 1), two codes at a time: (w >> 4 i) & 0x000F000F
-// holds codes i and i + 4, so the activations are taken in the same order
-// (0, 4, 1, 5, ...).  The MFMA's A operand is x (16 rows), B is 16 weight rows, so
+// A code q becomes the bf16 value 16 + q by one and-or (0x4180 | q << 3: at
+// exponent 2^4 the fourth mantissa bit from below is worth 1), two codes at a time: (w >> (4 i - 3)) &
+// 0x00780078 holds codes i and i + 4, so the activations are taken in the same order
+// (0, 4, 1, 5, ...).  The offset goes out of the sums again, at the price of the bits
+// that a sum of 31 |x| needs beyond one of 8 or 15 |x|, one or two; 128 + q, which
+// saves the first pair's shift (1 to 3 % of the time), loses four or five, and overflows
+// from |x| = 2^121 on.  The MFMA's A operand is x (16 rows), B is 16 weight rows, so
 // a lane's accumulators all belong to its own weight row (lane % 16) and the
-// row's scale is one value of that lane.  The offset 128 + z goes through the
+// row's scale is one value of that lane.  The offset 16 + z goes through the
 // MFMA as well: where a group has 128 k or more, x times a tile of ones, once,
-// gives sum x in the accumulator's places, and -(128 + z) sum x starts each group's
-// sum; with smaller groups a tile of the constant -(128 + z) (exact in bf16) is
+// gives sum x in the accumulator's places, and -(16 + z) sum x starts each group's
+// sum; with smaller groups a tile of the constant -(16 + z) (exact in bf16) is
 // multiplied along.  Per group then total += s acc in float32: every product is
 // exact, the only roundings are float32 sums and that step.
 //
@@ -53,21 +56,25 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
   w = u32x4{a, b, p[0], p[1]};
 }
 
-// Codes i and i + 4 of a word shifted by 4 i.  The constants are hidden from the
+// Codes i and i + 4 of a word shifted down by 4 i - 3.  The constants are hidden from the
 // compiler in a scalar and a vector register, or it spends two instructions
 // (v_and_or_b32 takes one scalar operand and no literal).
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  uint32_t mask = 0x000F000Fu, one = 0x43004300u;
+  uint32_t mask = 0x00780078u, one = 0x41804180u;
   __asm__("" : "+s"(mask));
   __asm__("" : "+v"(one));
   return (w & mask) | one;
 }
 
-// Eight codes -> 128 + code in bf16, codes (0, 4, 1, 5, 2, 6, 3, 7).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  return code_pair(i == 0 ? w << 3 : w >> (4 * i - 3));
+}
+
+// Eight codes -> 16 + code in bf16, codes (0, 4, 1, 5, 2, 6, 3, 7).
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
   u32x4 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = code_pair(w >> (4 * i));
+  for (int i = 0; i < 4; ++i) o[i] = code_pair(w, i);
   return __builtin_bit_cast(bf16x8, o);
 }
 
@@ -92,7 +99,7 @@ __device__ __forceinline__ float scale_value(uint32_t bits16, bool f16) {
 // One or two activation rows: whole rows of the weight past the wavefront, 64
 // consecutive 16-byte segments (32 k each) a load, each lane always the same
 // segments, so that its x stays in registers: no LDS, no barrier.  A code's
-// bf16 128 + q goes into v_dot2_f32_bf16 (float32 sum of exact products) with its
+// bf16 16 + q goes into v_dot2_f32_bf16 (float32 sum of exact products) with its
 // neighbour four codes on; a segment lies in one group.  Four rows a batch, the
 // next batch on its way meanwhile.  VALU and HBM about balance.  128256 x 4096,
 // M = 1, groups of 128: 49 us (5.5 TB/s), 58 us in the streamed form below; 8192 x
@@ -140,7 +147,7 @@ __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
       for (int j = 0; j < SEG; ++j) {
         float sc = scale_value(b.s[i][j], a.scale_f16);
         if (j == SEG - 1 && lane + 64 * j >= nseg) sc = 0.0f;   // lest an infinite scale meet x = 0
-        const float off = ZP ? 128.0f + (float)((b.z[i][j] >> (4 * (min(r0 + i, N - 1) & 7))) & 15u) : 136.0f;
+        const float off = ZP ? 16.0f + (float)((b.z[i][j] >> (4 * (min(r0 + i, N - 1) & 7))) & 15u) : 24.0f;
         float blk[MR];
 #pragma unroll
         for (int m = 0; m < MR; ++m) blk[m] = -off * sumx[m][j];
@@ -149,7 +156,7 @@ __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
           const uint32_t word = b.w[i][j][q];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t c = code_pair(word >> (4 * e));
+            const uint32_t c = code_pair(word, e);
 #pragma unroll
             for (int m = 0; m < MR; ++m) {
               const uint32_t xe = xr[m][j][q][e];
@@ -333,7 +340,7 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
 #pragma unroll
               for (int s = 0; s < 4; ++s) b = mfma_i4(xa[q][h][s][i], one, b);
 #pragma unroll
-              for (int v = 0; v < 4; ++v) base[q][h][i][v] = b[v] * (ZP ? -1.0f : -136.0f);
+              for (int v = 0; v < 4; ++v) base[q][h][i][v] = b[v] * (ZP ? -1.0f : -24.0f);
             }
           }
     }
@@ -376,7 +383,7 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
           f32x4 acc[MT];
           const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
           if (NG == 1) {
-            const float off = 128.0f + (float)(sw[q][h][0] & 15u);
+            const float off = 16.0f + (float)(sw[q][h][0] & 15u);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -387,8 +394,8 @@ __global__ __launch_bounds__(MT * NC == 1 ? 1024 : MT * NC == 2 ? 768 : 512) voi
             constexpr int kSteps = 4 / NG;              // MFMA steps per group
             const bool fresh = NG > 1 && s % kSteps == 0;
             const bf16x8 wb = codes_bf16(w[q][h][s]);
-            // small groups: -(128 + z) of the lane's row as a tile of its own, exact in bf16
-            const uint32_t ob = ZP ? (0xC300u | (sw[q][h][s / kSteps] & 15u)) * 0x10001u : 0xC308C308u;
+            // small groups: -(16 + z) of the lane's row as a tile of its own, exact in bf16
+            const uint32_t ob = ZP ? (0xC180u | (sw[q][h][s / kSteps] & 15u) << 3) * 0x10001u : 0xC1C0C1C0u;
             const u32x4 obits = {ob, ob, ob, ob};
             const bf16x8 off = __builtin_bit_cast(bf16x8, obits);
 #pragma unroll
@@ -719,7 +726,7 @@ __global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
           const f32x4 sx = *reinterpret_cast<const f32x4*>(sums + ((c & 1) * 2 + h) * 16 * MT + 16 * i + 4 * g);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const float off = ZP ? -128.0f - (float)(sw[t][h] & 15u) : -136.0f;
+            const float off = ZP ? -16.0f - (float)(sw[t][h] & 15u) : -24.0f;
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[t][i][v] = off * sx[v];
           }
@@ -737,7 +744,7 @@ __global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
         for (int t = 0; t < NT; ++t) {
           const uint32_t sb = sw[t][h * NG + s / kSteps];
           const bf16x8 wb = codes_bf16(w[t][h][s]);
-          const uint32_t ob = ZP ? (0xC300u | (sb & 15u)) * 0x10001u : 0xC308C308u;
+          const uint32_t ob = ZP ? (0xC180u | (sb & 15u) << 3) * 0x10001u : 0xC1C0C1C0u;
           const u32x4 obits = {ob, ob, ob, ob};
           const bf16x8 off = __builtin_bit_cast(bf16x8, obits);
 #pragma unroll

@@ -32,7 +32,7 @@ def weight(packed, scales, zeros, n):
 
 def gemm(x, packed, scales, zeros=None, bias=None):
     """(y, bound) in float64.  The bound holds the float32 summation: within a
-    group partial sums of x * (128 + code) stay below 4 * 143 * ||x_group|| for
+    group partial sums of x * (16 + code) stay below 4 * 31 * ||x_group|| for
     zero-mean x, MFMA rounds (perhaps toward zero: 2 u) once per four products,
     sum x likewise; then three roundings of each group's term; the output's
     bf16 rounding is half a step, 2^-8 of the value."""
@@ -45,7 +45,7 @@ def gemm(x, packed, scales, zeros=None, bias=None):
     u = 2.0 ** -24
     xn = np.linalg.norm(x.reshape(m, g, size), axis=2)
     s = np.abs(scales.astype(np.float64))
-    bound = 2.0 * (size / 4.0 + 8.0) * 2.0 * u * 4.0 * 143.0 * (xn @ s.T)
+    bound = 2.0 * (size / 4.0 + 8.0) * 2.0 * u * 4.0 * 31.0 * (xn @ s.T)
     bound += (g + 4) * u * (np.abs(x) @ np.abs(w).T)
     if bias is not None:
         y = y + bias

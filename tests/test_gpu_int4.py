@@ -194,3 +194,53 @@ def test_another_stream():
         got = B.nvfp4_int4_gemm(*dev)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+KERNELS = [(1, 40, 512), (1, 30, 4096), (2, 33, 1024), (3, 50, 512), (9, 40, 4352), (16, 700, 5120), (20, 70, 1056),
+           (40, 600, 1344), (64, 100, 768), (16, 14001, 320), (33, 14001, 160), (64, 33000, 512)]
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128, None])
+@pytest.mark.parametrize("m,n,k", KERNELS)
+def test_large_activation_on_a_zero_weight(m, n, k, group, zeros):
+    """An activation of 2^18 in each group whose code is the zero point, among small whole numbers: every
+    partial sum with an offset of 16 is a whole number below 2^24, so the result is exact before its
+    one rounding to bf16, and the large activation leaves nothing."""
+    group = k if group is None or k % group else group
+    rng = np.random.default_rng(n + k)
+    g = k // group
+    codes, zp = rng.integers(0, 16, (n, k)), rng.integers(0, 16, (n, g)) if zeros else np.full((n, g), 8)
+    x = rng.integers(-1, 2, (m, k)).astype(np.float64)
+    at = group * np.arange(g) + rng.integers(0, group, g)
+    if group == k:
+        at = at[:1]
+    codes[:, at] = zp
+    x[:, at] = 2.0 ** 18 * rng.choice([-1, 1], (m, len(at)))
+    scale = 2.0 ** rng.integers(-8, -6, (n, g))
+    packed = Q.pack(codes, 1)
+    pad = np.zeros(((n + 7) // 8 * 8, g), np.int64)
+    pad[:n] = zp
+    y = run(torch.from_numpy(x).to(torch.bfloat16), packed, torch.from_numpy(scale).to(torch.bfloat16),
+            Q.pack(pad, 0) if zeros else None, None)
+    want = x @ ((codes - np.repeat(zp, group, 1)) * np.repeat(scale, group, 1)).T
+    # the groups' sums, scaled by powers of two, add exactly too
+    assert torch.equal(y.cpu(), torch.from_numpy(want).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", KERNELS)
+def test_activations_of_large_magnitude(m, n, k, group):
+    """x = one-hot rows of 2^122: each output is one dequantized weight times it, finite."""
+    if k % group:
+        group = 32
+    rng = np.random.default_rng(m + n)
+    g = k // group
+    codes, zp = rng.integers(0, 16, (n, k)), rng.integers(0, 16, ((n + 7) // 8 * 8, g))
+    pos = rng.integers(0, k, m)
+    x = torch.zeros((m, k), dtype=torch.bfloat16)
+    x[torch.arange(m), torch.from_numpy(pos)] = 2.0 ** 122
+    scale = torch.full((n, g), 2.0 ** -10, dtype=torch.bfloat16)
+    y = run(x, Q.pack(codes, 1), scale, Q.pack(zp, 0), None).cpu().double().numpy()
+    want = 2.0 ** 112 * (codes - np.repeat(zp[:n], group, 1))[:, pos].T
+    assert np.array_equal(y, want)
