@@ -519,7 +519,9 @@ nvfp4_status nvfp4_logprobs(const void* logits, int dtype, int64_t M, int64_t V,
  *   dlogits[i, j] = (1 / T) * ( dlogprob[i] * 1[j = id] + p * (dlse[i] - dlogprob[i]
  *                               - dentropy[i] * (log p + entropy[i])) ),   log p = z[i, j] - lse[i]
  * in float32, rounded once to dtype.  Tokens that are not allowed, logits of
- * -inf and rows with lse -inf get 0.
+ * -inf and rows with lse -inf get 0.  Where |lse| is 1024 or more (8192 for bf16),
+ * its rounding would show in p: there log p is taken from the row's logits again, relative to
+ * their maximum (slower, a row at a time).
  *
  *   logits, token_ids, temperatures, allowed   in  as given to nvfp4_logprobs
  *   lse, entropy   in  float [M] as nvfp4_logprobs wrote them (entropy only with dentropy)

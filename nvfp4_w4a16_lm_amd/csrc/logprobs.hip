@@ -535,7 +535,65 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
 // log p_j = x_j / T - lse; 0 where the token is not allowed or its logit is
 // -inf.  A workgroup owns a run of one row's vectors.  HBM bounds it: 1024 x 128256
 // bf16 95 us (5.5 TB/s read and written).
+//
+// lse is a float32, so p_j is off by half its last place: 2^-14 of p_j at |lse| = 1024,
+// 2^-11 at 8192, and nothing is right once |lse| passes 2^24 (low temperatures, large
+// logits).  From there on (8192 for bf16, whose own rounding is 2^-9) one of a row's
+// workgroups takes the whole row and sums it again relative to its maximum, as the
+// forward does, before it writes; the others leave.  Which one goes by the row, or
+// with a multiple of eight segments all of them would land on one XCD.
+// Such rows alone, 128256 bf16: 1 row 45 us (7 ordinary), 1024 rows 202 us (97).
 // ---------------------------------------------------------------------------
+namespace {
+
+// A row's sums by one workgroup.
+template <int DT, bool MASK>
+__device__ Sums row_sums(const uint8_t* row, const uint32_t* bits, int V, float c2, Sums* sh) {
+  using E = Elem<DT>;
+  constexpr int VE = E::kPerVec, U = 4;
+  const int tid = threadIdx.x, nv = (V + VE - 1) / VE, full = V / VE;
+  auto load = [&](int v) -> u32x4 {
+    if (v < full) return E::load(row + (int64_t)v * 16);
+    if (v < nv) return load_tail<DT>(row, v * VE, V);
+    return u32x4{E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
+  };
+  Sums q = {kLowest, 0.0f, 0.0f};
+  u32x4 cur[U], next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) cur[u] = load(kLpThreads * u + tid);
+  for (int vb = 0; vb < nv; vb += kLpThreads * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) next[u] = load(vb + kLpThreads * (U + u) + tid);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j0 = (vb + kLpThreads * u + tid) * VE;
+      const uint32_t w = MASK && j0 < V ? bits[j0 >> 5] >> (j0 & 31) : 0xFFFFFFFFu;
+      float f[VE];
+      E::unpack(cur[u], f);
+      float g = kLowest;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        if (MASK && !((w >> e) & 1u)) f[e] = -INFINITY;
+        g = fmaxf(g, f[e]);
+      }
+      if (g > q.raw) rescale(q, g, c2);
+      const float half = 0.5f * q.raw;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) q.s += __builtin_amdgcn_exp2f(half_difference(f[e], half) * c2);
+      cur[u] = next[u];
+    }
+  }
+  q = wave_combine(q, c2);
+  if ((tid & 63) == 0) sh[tid >> 6] = q;
+  __syncthreads();
+  q = sh[0];
+#pragma unroll
+  for (int w = 1; w < kLpWaves; ++w) q = combine(q, sh[w], c2);
+  return q;
+}
+
+}  // namespace
+
 template <int DT, bool MASK>
 __global__ __launch_bounds__(kLpThreads) void logprobs_backward_kernel(LogprobsBackwardArgs a) {
   using E = Elem<DT>;
@@ -548,7 +606,7 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_backward_kernel(LogprobsB
   const uint32_t* const bits = MASK ? a.allowed + i * a.mask_words : nullptr;
   const int V = a.V;
   const int nv = (V + VE - 1) / VE, full = V / VE;
-  const int v0 = seg * a.seg_vecs, v1 = min(nv, v0 + a.seg_vecs);
+  int v0 = seg * a.seg_vecs, v1 = min(nv, v0 + a.seg_vecs);
   const float invt = inv_temperature(a.temps, i);
   // what 1 / T lost in rounding, so that x / T - lse is right to its own size
   // (log p of a likely token is a small difference of the two)
@@ -556,11 +614,21 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_backward_kernel(LogprobsB
   if (!(fabsf(invt_lo) < INFINITY)) invt_lo = 0.0f;
   const float lse = a.lse[i];
   const bool empty = lse == -INFINITY;
+  float top = 0.0f, base = lse;                          // log p = (x - top) / T - base
+  __shared__ Sums sh_sums[kLpWaves];
+  if (fabsf(lse) >= (DT == kBf16 ? 8192.0f : 1024.0f) && !empty) {   // the same for every workgroup of the row
+    if (seg != (int)(i % a.segs)) return;
+    v0 = 0;
+    v1 = nv;
+    const Sums q = row_sums<DT, MASK>(row, bits, V, base2_scale(a.temps, i), sh_sums);
+    top = q.raw;
+    base = logf(q.s);
+  }
   const int id = a.tok ? a.tok[i] : -1;
   const bool given = id >= 0 && id < V;
-  const float glp = given && a.dlogprob ? a.dlogprob[i] * invt : 0.0f;
-  const float gent = a.dentropy ? a.dentropy[i] * invt : 0.0f;
-  const float glse = a.dlse ? a.dlse[i] * invt : 0.0f;
+  const float glp = given && a.dlogprob ? a.dlogprob[i] : 0.0f;
+  const float gent = a.dentropy ? a.dentropy[i] : 0.0f;
+  const float glse = a.dlse ? a.dlse[i] : 0.0f;
   const float b0 = glse - glp - (a.dentropy ? gent * a.entropy[i] : 0.0f);
 
   auto load = [&](int v) -> u32x4 {
@@ -587,7 +655,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_backward_kernel(LogprobsB
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
           if (MASK && !((w >> e) & 1u)) f[e] = -INFINITY;
-          const float lp = __builtin_fmaf(f[e], invt_lo, __builtin_fmaf(f[e], invt, -lse));
+          const float x = f[e] - top;
+          const float lp = __builtin_fmaf(x, invt_lo, __builtin_fmaf(x, invt, -base));
           const float p = __builtin_amdgcn_exp2f(lp * kLog2e);
           d[e] = p * __builtin_fmaf(fmaxf(lp, -1000.0f), -gent, b0);
           if (f[e] == -INFINITY || empty) d[e] = 0.0f;
@@ -597,6 +666,8 @@ __global__ __launch_bounds__(kLpThreads) void logprobs_backward_kernel(LogprobsB
           for (int e = 0; e < VE; ++e)
             if (id == j0 + e && f[e] != -INFINITY) d[e] += glp;
         }
+#pragma unroll
+        for (int e = 0; e < VE; ++e) d[e] *= invt;       // last: the factors times 1 / T could overflow beside p = 0
         const u32x4 o = E::pack(d);
         if (v < full) {
           E::store(out + (int64_t)v * 16, o);

@@ -397,3 +397,83 @@ def test_forward_infinite_temperature(dtype, v):
                            None if b is None else b[:4])
         assert not g.any()                               # 1 / T of anything
     check_forward(x, ids, 5, np.full(m, 3e38, np.float32), bits)
+
+
+def check_backward_relative(x, ids, temps, bits=None, out=None):
+    """The gradient against softmax relative to the row's maximum, for rows whose lse is too large for
+    z - lse in float32 (or, further out, in float64); rows below that (header) among them as in
+    check_backward, with the lse that the forward rounded."""
+    m, v = x.shape
+    rng = np.random.default_rng(v)
+    dlp, dent, dlse = (rng.standard_normal(m).astype(np.float32).astype(np.float64) for _ in range(3))
+    x64 = host(x)
+    g, lse, ent = run_backward(x, ids, dlp, dent, dlse, temps, bits, out)
+    t = np.float32(temps).astype(np.float64)[:, None]
+    raw = x64 if bits is None else np.where(bits, x64, -np.inf)
+    live = raw > -np.inf
+    z = np.where(live, (np.where(live, raw, 0.0) - raw.max(1, keepdims=True)) / t, -np.inf)
+    s = np.exp(z).sum(1, keepdims=True)
+    p = np.exp(z) / s
+    logp = np.where(live, z, 0.0) - np.log(s)
+    c = lambda a: a[:, None]
+    want = p * (c(dlse - dlp) - c(dent) * (logp + c(ent)))
+    mag = p * (c(np.abs(dlse) + np.abs(dlp)) + c(np.abs(dent)) * (np.abs(logp) + c(np.abs(ent))))
+    rows = np.arange(m)
+    given = live[rows, ids]
+    want[rows, ids] += np.where(given, dlp, 0.0)
+    mag[rows, ids] += np.where(given, np.abs(dlp), 0.0)
+    want, mag = want / t, mag / t
+    # differences, quotients and log S as in the forward bounds, then as in check_backward; 2^y of a hardware
+    # power and its argument's rounding, 3 u of |log p|
+    rel = (v / 256.0 + v / 1024.0 + 40.0) * U
+    bound = mag * (rel + 8 * U * np.abs(logp) + 16 * U) + GRAD_TYPES[x.dtype] * np.abs(want) * (1 + 2.0 ** -7)
+    tiny = {BF16: 2.0 ** -126, F16: 2.0 ** -25, F32: 2.0 ** -126}[x.dtype]
+    small = np.abs(lse) < (8192 if x.dtype == BF16 else 1024)
+    if small.any():
+        t64 = np.float32(temps).astype(np.float64)
+        with np.errstate(all="ignore"):                  # the other rows of it are not used
+            w2, m2 = L.backward(x64, ids, np.where(small, lse, 0.0), ent, dlp, dent, dlse, t64, bits)
+        _, z2 = L.scaled(x64, t64, bits)
+        z2 = np.where(np.isfinite(z2), np.abs(z2), 0.0)
+        b2 = m2 * (4 * U * (z2 + np.abs(np.where(small, lse, 0.0))[:, None]) + 16 * U) + GRAD_TYPES[x.dtype] * np.abs(w2) * (1 + 2.0 ** -7)
+        want, bound = np.where(c(small), w2, want), np.where(c(small), b2, bound)
+    got = host(g)
+    ok = np.abs(got - want) <= bound + tiny * 1.01
+    assert np.all(ok), (got[~ok][:4], want[~ok][:4], bound[~ok][:4])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("v", [1, 9, 5001, 20011, 40000])
+@pytest.mark.parametrize("offset,temp", [(0.0, 1e-3), (0.0, 3e-5), (2000.0, 1.0), (-40000.0, 0.7), (0.0, 1e-8)])
+def test_backward_of_rows_with_a_large_lse(dtype, v, offset, temp):
+    m = 4
+    if dtype == F16:
+        temp = max(temp, 1e-3)                           # 1 / T, and with it the gradient, within float16
+    x = make_logits(m, v, F32, v + 9, pad=3, offset=1)
+    if offset:
+        x = x * 8.0 if dtype == BF16 else x              # bf16 logits lie 8 and more apart there
+        x = x + offset
+        top = x.amax(1, keepdim=True)
+        x = torch.where(x > top - 30, x, torch.full_like(x, float("-inf")))
+    x = x.to(dtype)
+    if offset == 0.0:                                    # near ties: gradients that are not all 0 or 1
+        x[1] = torch.round(x[1])
+        x[2] = x.amax(1)[2]
+    ids = x.argmax(1).cpu().numpy().astype(np.int32)
+    ids[3] = (ids[3] + 1) % v
+    temps = np.float32([temp, temp, temp, temp])
+    check_backward_relative(x, ids, temps)
+    bits = np.random.default_rng(v).random((m, v)) < 0.5
+    bits[np.arange(m), x.argmax(1).cpu().numpy()] = True
+    check_backward_relative(x, ids, temps, bits)
+    check_backward_relative(x, ids, temps, bits, out=x)  # in place: the row is read before it is written
+
+
+def test_backward_mixes_rows_of_either_kind():
+    """Rows summed again beside ordinary ones, and a row whose lse overflows."""
+    m, v = 6, 30000
+    x = make_logits(m, v, F32, 3)
+    x[1] += 5000.0
+    x[4] -= 1e6
+    temps = np.float32([1.0, 1.0, 1e-3, 0.8, 1.0, 1e-38])
+    check_backward_relative(x, np.arange(m, dtype=np.int32), temps)
