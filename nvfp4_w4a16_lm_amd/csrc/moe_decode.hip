@@ -28,7 +28,8 @@
 // 16-byte loads) and their four block scales (one 4-byte load); MFMA step s
 // multiplies k = 64 g + 8 s + [0, 8) of each g.  A code times its block scale is
 // exact in bf16.  The hidden activation is kept as a bf16 pair hi + lo (16 bits
-// of it), so that the only rounding to bf16 is the output's.
+// of it, twice the output's; a third part, float32's 24 bits, takes T = 1 at 4112 x
+// 14336 from 102 to 120 us), so that the only rounding to bf16 is the output's.
 #include <algorithm>
 
 #include "nvfp4_device.hpp"
