@@ -833,17 +833,21 @@ hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
   if (a.M == 1 && seg == 4) return launch_int4_dot<1, 4>(a, stream);
   if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
   // The tile kernel where one tile a wavefront gives two fifths of the compute
-  // units a workgroup (64 x 12000 x 8192: 61 us, streamed 60; 33 x 16000 x 4096 26.5 and
-  // 27; 64 x 4096 x 4096 38 and 26; 16 x 14000 x 4096 15.7 and 16.8), and K leaves its
-  // 32-bit offsets in range.  Up to 16 rows in groups of 128 or more the streamed
-  // form, whose work divides evenly, keeps the sizes that would leave a second or
-  // later round of workgroups (two a compute unit) less than three quarters full:
-  // 16 x 151936 x 5120 97 us, tiles 106; 3 x 128256 x 2048, two full rounds, 31 and 27.
+  // units a workgroup (64 x 12000 x 8192: 61 us, streamed 60; 33 x 16000 x 4096 26 and
+  // 27; 64 x 4096 x 4096 38 and 26; 16 x 13000 x 2048 9 and 13, x 8192 27 and 30), and K
+  // leaves its 32-bit offsets in range.  Up to 16 rows in groups of 128 or more the
+  // streamed form, whose work divides evenly, keeps the sizes that would leave a
+  // second or later round of workgroups (two a compute unit) less than three quarters
+  // full, if K is 16 to 20 chunks, one phase of eight to ten wavefronts.  Streamed and
+  // tiles, N = 70000, 98304, 140000 at K = 5120: 3 rows 45 57 78, 51 56 86 us; 16 rows 48 62
+  // 85, 59 66 102; at 4096: 35 44 60, 36 41 63; 37 49 63, 41 47 73.  At other K it
+  // loses: 2560 16 rows 37 46 60, 28 32 49; 6144 62 98 120, 65 74 113; 8192 about even.
   const int64_t cus = device_cus(current_device());
   const int64_t nblocks = ((int64_t)a.N + 127) / 128, mblocks = a.M <= 48 ? 1 : ((int64_t)a.M + 63) / 64;
   if (5 * nblocks * mblocks >= 2 * cus && a.K <= 1 << 22) {
     const int64_t over = nblocks % (2 * cus);
-    const bool uneven = nblocks > 2 * cus && over != 0 && 2 * over < 3 * cus;
+    const int64_t nchunks = ((int64_t)a.K + kSt4Chunk - 1) / kSt4Chunk;
+    const bool uneven = nblocks > 2 * cus && over != 0 && 2 * over < 3 * cus && nchunks >= 16 && nchunks <= 20;
     const bool small_groups = a.group < 128 && a.K > a.group;
     if (a.M <= 16 && (small_groups || !uneven)) return launch_int4_tiles<1, 1>(a, dim3((unsigned)nblocks), stream);
     if (a.M > 16 && a.M <= 32) return launch_int4_tile<2>(a, stream);

@@ -244,3 +244,16 @@ def test_activations_of_large_magnitude(m, n, k, group):
     y = run(x, Q.pack(codes, 1), scale, Q.pack(zp, 0), None).cpu().double().numpy()
     want = 2.0 ** 112 * (codes - np.repeat(zp[:n], group, 1))[:, pos].T
     assert np.array_equal(y, want)
+
+
+@pytest.mark.parametrize("m,n,k,group", [(3, 66001, 4096, 128), (16, 70000, 4352, 256), (8, 80003, 5120, 5120),
+                                         (5, 66000, 3840, 128), (9, 70001, 5248, 128)])
+def test_few_rows_in_uneven_rounds(m, n, k, group):
+    """Up to 16 rows where the tile kernel's last round would be mostly empty: streamed for K of 16 to 20
+    chunks, tiles beside it.  (64 different rows, so that the host has little to make.)"""
+    x, packed, scales, _, _ = make(m, 64, k, group, False, m + n)
+    rows = np.arange(n) * 7 % 64
+    want, bound = Q.gemm(x.to(torch.float64).numpy(), packed, scales.to(torch.float64).numpy())
+    y = run(x, packed[rows], scales[torch.from_numpy(rows)], None, None).cpu().to(torch.float64).numpy()
+    err = np.abs(y - want[:, rows])
+    assert np.all(err <= bound[:, rows]), err.max()
