@@ -529,7 +529,8 @@ nvfp4_status nvfp4_logprobs(const void* logits, int dtype, int64_t M, int64_t V,
  *                                  token takes dlogprob as 0
  *   dlogits        out dtype [M, V] rows of dlogits_stride elements; it may be logits itself
  *                      (same pointer and stride: the gradient replaces the logits) and
- *                      otherwise overlaps no input
+ *                      otherwise its span, first row's start to last row's end, overlaps no
+ *                      input's
  */
 nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride,
                                      const int32_t* token_ids, const float* temperatures, const uint32_t* allowed,

@@ -102,8 +102,8 @@ __device__ __forceinline__ float scale_value(uint32_t bits16, bool f16) {
 // bf16 16 + q goes into v_dot2_f32_bf16 (float32 sum of exact products) with its
 // neighbour four codes on; a segment lies in one group.  Four rows a batch, the
 // next batch on its way meanwhile.  VALU and HBM about balance.  128256 x 4096,
-// M = 1, groups of 128: 49 us (5.5 TB/s), 58 us in the streamed form below; 8192 x
-// 2048 4.5 against 7.9 us; 128256 x 8192 116 against 141.
+// M = 1, groups of 128: 46 us (5.9 TB/s).  Against the streamed form below, random
+// codes: 128256 x 4096 55 and 67 us; 8192 x 2048 4.7 and 8.4; 128256 x 8192 110 and 125.
 // ---------------------------------------------------------------------------
 template <int MR, int SEG, bool ZP>
 __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
@@ -223,10 +223,10 @@ __global__ __launch_bounds__(256) void int4_dot_kernel(Int4Args a) {
 // beyond W NC chunks is taken in phases over the same tiles, whose sums wait in
 // LDS meanwhile.  NG: scales per 128 k (4, 2: groups of 32, 64; 1: groups of a
 // multiple of 128, or one group per row).  Up to 16 rows HBM bounds it (16 x 151936 x
-// 5120, zero points: 84 us, 4.9 TB/s; weights loaded to registers in the MFMA's layout,
+// 5120, zero points: 86 us, 4.8 TB/s; weights loaded to registers in the MFMA's layout,
 // four lanes a row: 216), beyond that, where few weight rows leave this form the
 // only one that fills the card, the unpacking and the sums through LDS (64 x 8000 x
-// 8192: 53 us).
+// 8192: 52 us).
 // ---------------------------------------------------------------------------
 // Wavefronts per workgroup: the x fragments take 32 MT NC registers of each lane.
 // Sum buffers, and tiles in flight per wavefront: beyond 16 rows the LDS that the
@@ -547,9 +547,11 @@ hipError_t launch_int4_dot(const Int4Args& a, hipStream_t stream) {
 // out of the x stores.  The vector units bound it, LDS reads of x come next (half
 // of either at 33 x 32000 x 4096 before the unpacking was cut from 11 to 7
 // instructions a word): two tiles share each x fragment where the grid still fills the
-// card.  33 x 32003 x 2080, groups of 32 with zero points: 27 us, 44 in the streamed
-// form; 64 x 128256 x 4096: 113 us (2.4 TB/s, 600 TFLOP/s) against 153, one tile 148;
-// 16 x 151936 x 5120 in groups of 32 with zero points 122 (4.0 TB/s) against 198.
+// card.  33 x 32003 x 2080, groups of 32 with zero points: 24 to 27 us, 44 in the
+// streamed form; 64 x 128256 x 4096: 106 us (2.6 TB/s, 640 TFLOP/s) against 165, one tile
+// 145; 16 x 151936 x 5120 in groups of 32 with zero points 119 (3.8 TB/s) against 225.
+// Beyond 64 rows every 64 read and unpack the weight again: 256 x 32000 x 4096 106 us
+// (630 TFLOP/s), 2048 rows 820 us (650 TFLOP/s).
 // ---------------------------------------------------------------------------
 template <int MT, int NT, int NG, bool ZP>
 __global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
@@ -807,8 +809,9 @@ hipError_t launch_int4_tiles(const Int4Args& a, const dim3& blocks, hipStream_t 
 }
 
 // Two tiles a wavefront where that takes fewer rounds of workgroups, a round
-// counted 1.6 times as long (64 x 128256 x 4096: 57 and 37 us a round; 1.1 to 1.5
-// times where one round is all, so that one tile is right there).
+// counted 1.6 times as long (64 x 128256 x 4096: 53 and 36 us a round; 1.1 to 1.5
+// times where one round is all, so that one tile is right there).  Over 17 to 160
+// rows, N of 4000 to 128256 and K of 2048 to 8192 it takes the faster one within 6 %.
 template <int MT>
 hipError_t launch_int4_tile(const Int4Args& a, hipStream_t stream) {
   const int64_t cus = device_cus(current_device());
@@ -823,9 +826,9 @@ hipError_t launch_int4_tile(const Int4Args& a, hipStream_t stream) {
 
 hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
   // One or two rows whose x fits in the lanes' registers (K to 8192, and 2048).
-  // The dot kernel against the streamed one, M = 1: 151936 x 5120 80 and 84 us,
-  // 128256 x 6656 101 and 131, 128256 x 1280 in groups of 32 23 and 41, 1024 x 1280 3.3
-  // and 5.6; M = 2, 128256 x 2048: 32.2 and 32.7, beyond that K 128256 x 4096 75 and 53.
+  // The dot kernel against the streamed one, M = 1: 151936 x 5120 82 and 84 us,
+  // 128256 x 6656 100 and 131, 128256 x 1280 in groups of 32 23 and 38, 1024 x 1280 3.6
+  // and 5.6; M = 2, 128256 x 2048: 33.4 and 32.8, beyond that K 128256 x 4096 75 and 53.
   const int64_t seg = ((int64_t)a.K + 2047) / 2048;
   if (a.M == 1 && seg == 1) return launch_int4_dot<1, 1>(a, stream);
   if (a.M == 1 && seg == 2) return launch_int4_dot<1, 2>(a, stream);
@@ -834,7 +837,7 @@ hipError_t launch_int4_gemm(Int4Args a, hipStream_t stream) {
   if (a.M == 2 && seg == 1) return launch_int4_dot<2, 1>(a, stream);
   // The tile kernel where one tile a wavefront gives two fifths of the compute
   // units a workgroup (64 x 12000 x 8192: 61 us, streamed 60; 33 x 16000 x 4096 26 and
-  // 27; 64 x 4096 x 4096 38 and 26; 16 x 13000 x 2048 9 and 13, x 8192 27 and 30), and K
+  // 27; 64 x 4096 x 4096 38 and 23; 16 x 13000 x 2048 9 and 13, x 8192 27 and 30), and K
   // leaves its 32-bit offsets in range.  Up to 16 rows in groups of 128 or more the
   // streamed form, whose work divides evenly, keeps the sizes that would leave a
   // second or later round of workgroups (two a compute unit) less than three quarters

@@ -9,8 +9,8 @@
 // rescaled when the maximum grows (s' = s a, t' = (t + s d) a with d = (m - m') log2(e) / T
 // and a = 2^d); then lse = m / T + log s and H = log s - (t / s) ln 2.  The difference
 // comes first: scaled logits rounded on their own would leave up to |z| 2^-24 between a
-// logit and its own maximum, which no float32 power holds from |z| of 2^31 on (one
-// instruction a logit less, and NaN there).  Logits go to float32's largest, so half
+// logit and its own maximum, which no float32 power holds from |z| of 2^31 on (12
+// operations a logit instead of 13, 2048 x 128256 at most 2 % faster, and NaN there).  Logits go to float32's largest, so half
 // the difference is taken, and twice the scale: no finite pair overflows.
 // The rank is a count of larger logits in the same pass.
 //
@@ -30,7 +30,7 @@
 // atomics, so results do not depend on timing).
 //
 // Many rows: 2048 x 128256 bf16 110 us (4.8 TB/s; the vector units are 80 % busy with
-// about 15 operations a logit, HBM close behind).  Few rows: launches and the
+// 13 operations a logit, HBM close behind).  Few rows: launches and the
 // lists; one row 13 us (9 us the segments, of which most is the first loads and the
 // sort, 5 us the join), 64 x 151936 masked with 20 alternatives 25 us, 333 x 32003
 // float32 with 64 alternatives 35 us (1.2 TB/s; most of it the lists).
@@ -536,9 +536,9 @@ __global__ __launch_bounds__(64 * kJoinWaves) void logprobs_join_kernel(Logprobs
 // -inf.  A workgroup owns a run of one row's vectors.  HBM bounds it: 1024 x 128256
 // bf16 95 us (5.5 TB/s read and written).
 //
-// lse is a float32, so p_j is off by half its last place: 2^-14 of p_j at |lse| = 1024,
-// 2^-11 at 8192, and nothing is right once |lse| passes 2^24 (low temperatures, large
-// logits).  From there on (8192 for bf16, whose own rounding is 2^-9) one of a row's
+// lse is a float32, so p_j is off by half its last place: 2^-15 of p_j below |lse| = 1024,
+// 2^-12 below 8192, and nothing is right once |lse| passes 2^24 (low temperatures, large
+// logits).  From 1024 on (8192 for bf16, whose own rounding is 2^-9) one of a row's
 // workgroups takes the whole row and sums it again relative to its maximum, as the
 // forward does, before it writes; the others leave.  Which one goes by the row, or
 // with a multiple of eight segments all of them would land on one XCD.

@@ -17,9 +17,11 @@
 //
 // HBM bounds both: 0.5625 bytes per weight of the chosen experts.  The streamed form
 // (further down) serves H and I that are multiples of 32, from 64.  8 experts, 4096 x
-// 14336, top-2: T = 1 49 us (198 MB, 4.0 TB/s: 28 us up, 21 us down), T = 16 163 us
-// (785 MB, 4.8 TB/s); 64 experts of 2048 x 1024, T = 4 34 us.  The register form here
-// serves the other sizes (at T = 1, 16 of the first layer it took 65 and 211 us).
+// 14336, top-2: T = 1 49 us (198 MB, 4.0 TB/s: 28 us up, 22 us down), T = 16 163 us
+// (785 MB, 4.8 TB/s); 64 experts of 2048 x 1024, T = 4 36 us.  The register form here
+// serves the other sizes (at T = 1, 16 of the first layer it took 65 and 211 us; 8
+// experts of 4112 x 14336 102 and 421 us).  H beyond 4096 takes the up kernel several
+// passes, whose sums wait in LDS: 8 of 64 experts of 7168 x 2048, T = 8 288 us (3.6 TB/s).
 //
 // Register form.  A workgroup of the down kernel owns 16 output columns, its
 // wavefronts split the K of all chosen experts, nothing per pair is written.
