@@ -575,7 +575,6 @@ __global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
   for (int t = 0; t < NT; ++t) tile[t] = min(((int)blockIdx.x * 8 + wave) * NT + t, tiles - 1);   // a repeat is not stored
 
   // one base per tile and 32-bit offsets beside it
-  const int piece = (lane & 7) ^ (lane >> 3);
   uint32_t roff[NT][2];
   const uint8_t* wbase[NT];
 #pragma unroll
@@ -584,14 +583,11 @@ __global__ __launch_bounds__(512) void int4_tile_kernel(Int4Args a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) roff[t][j] = (uint32_t)min(8 * j + (lane >> 3), N - 1 - 16 * tile[t]) * (uint32_t)pitch;
   }
-  auto copy = [&](int c, int slot) {                    // as st4_copy
-    const uint32_t off = (uint32_t)min(kSt4Chunk / 2 * c + 16 * piece, (int)pitch - 16);
+  auto copy = [&](int c, int slot) {
+    const uint32_t off = (uint32_t)st4_offset<int>(c, (int)pitch, lane);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        __builtin_amdgcn_global_load_lds((const void*)(wbase[t] + (roff[t][j] + off)),
-                                         (st4_lds_t)(ring + (slot * NT + t) * kSt4Bytes + 1024 * j), 16, 0, 2 /* nontemporal */);
+      st4_copy_rows(wbase[t] + (roff[t][0] + off), wbase[t] + (roff[t][1] + off), ring + (slot * NT + t) * kSt4Bytes);
   };
   // scale e = lane + 64 i of a step: row e / COLS of the NT tiles, column e % COLS
   uint32_t sv[2][SI], zv[2][SI];

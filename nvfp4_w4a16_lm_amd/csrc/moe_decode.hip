@@ -880,19 +880,13 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
     for (int i = 0; i < NC; ++i)
       scl[((u & 1) * 16 + srow[i]) * spitch + sword[i]] = scale_word(sv[slot][i], words * sslice[slot] + sword[i], nb);
   };
-  const int piece = (lane & 7) ^ (lane >> 3);
   const uint32_t roff = (uint32_t)(lane >> 3) * (uint32_t)pitch;
-  auto copy_tile = [&](const Pos& p, int slot) {           // as st4_copy
+  auto copy_tile = [&](const Pos& p, int slot) {
     const uint8_t* const base = a.w2_packed + p.row * pitch;
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
-      const int c = (p.slice * W + wave) * NC + q;
-      const uint32_t off = roff + (uint32_t)min(kSt4Chunk / 2 * c + 16 * piece, (int)pitch - 16);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        __builtin_amdgcn_global_load_lds((const void*)(base + 8 * j * pitch + off),
-                                         (st4_lds_t)(ring + (slot * NC + q) * kSt4Bytes + 1024 * j), 16, 0,
-                                         2 /* nontemporal */);
+      const uint32_t off = roff + (uint32_t)st4_offset<int>((p.slice * W + wave) * NC + q, (int)pitch, lane);
+      st4_copy_rows(base + off, base + 8 * pitch + off, ring + (slot * NC + q) * kSt4Bytes);
     }
   };
   Pos next = pos_of(u0), now = next;                       // fetched next; computed now
@@ -909,7 +903,7 @@ __global__ __launch_bounds__(1024) void moe_stream_down_kernel(MoeDecodeArgs a) 
 
   f16x8 xb[NC][8], xr[NC][8];
   float back = 0.0f;
-  int out_pair = -1;                           // out_pair: of this thread's token in the sums
+  int out_pair = -1;                                       // of this thread's token in the sums
   // the activations of (expert, slice) c: column r is token r's pair with the expert, or zeros
   auto load_act = [&](const Pos& at) {
     const int e = sh_list[at.combo / slices], c0 = (at.slice * W + wave) * NC;

@@ -23,19 +23,24 @@ typedef __attribute__((address_space(3))) void* st4_lds_t;
 constexpr int st4_vm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 constexpr int kSt4Lgkm0 = 0xC07F;
 
-// Copy the chunk's rows `rows` + 0..15 (row index clamped to last) into
-// region: lane l fetches piece (l % 8) ^ (l / 8) of row 8 j + l / 8.  Pieces past the
-// row's end (K % 256 != 0) repeat its last one; their activations are zero.
+// Byte of a row from which lane l copies chunk c: piece (l % 8) ^ (l / 8).  Pieces past
+// the row's end (K % 256 != 0) repeat its last one; their activations are zero.
+template <typename Int>
+__device__ __forceinline__ Int st4_offset(int c, Int pitch, int lane) {
+  return min((Int)(kSt4Chunk / 2) * c + 16 * ((lane & 7) ^ (lane >> 3)), pitch - 16);
+}
+
+// Copy a tile's chunk into region, lane l from row l / 8 (at) and row 8 + l / 8 (below).
+__device__ __forceinline__ void st4_copy_rows(const uint8_t* at, const uint8_t* below, uint8_t* region) {
+  __builtin_amdgcn_global_load_lds((const void*)at, (st4_lds_t)region, 16, 0, 2 /* nontemporal */);
+  __builtin_amdgcn_global_load_lds((const void*)below, (st4_lds_t)(region + 1024), 16, 0, 2 /* nontemporal */);
+}
+
+// The same for rows 0..15 of a tile (row index clamped to last).
 __device__ __forceinline__ void st4_copy(const uint8_t* tile, int64_t pitch, int last, int c, uint8_t* region,
                                          int lane) {
-  const int piece = (lane & 7) ^ (lane >> 3);
-  const int64_t off = min((int64_t)(kSt4Chunk / 2) * c + 16 * piece, pitch - 16);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int row = min(8 * j + (lane >> 3), last);
-    __builtin_amdgcn_global_load_lds((const void*)(tile + row * pitch + off), (st4_lds_t)(region + 1024 * j), 16, 0,
-                                     2 /* nontemporal */);
-  }
+  const uint8_t* const p = tile + st4_offset<int64_t>(c, pitch, lane);
+  st4_copy_rows(p + min(lane >> 3, last) * pitch, p + min(8 + (lane >> 3), last) * pitch, region);
 }
 
 // Piece p (0..7) of the chunk for lane row r.

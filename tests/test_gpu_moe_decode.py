@@ -245,3 +245,18 @@ def test_many_experts(T, E, topk, H, I):
     # worst cases aside, an output is the nearest bf16 value or, where the sums' errors (about 2^-20 of
     # the terms' norm) cross a border, its neighbour: a twentieth at most
     assert (out != want.to(torch.bfloat16)).double().mean() < 0.05
+
+
+@pytest.mark.parametrize("T,H,I", [(8, 512, 512), (3, 528, 272), (16, 1024, 256)])
+def test_agrees_with_the_layer_over_given_ids_within_both_bounds(T, H, I):
+    """nvfp4_moe_w4a16_forward on the routing reported here: apart by no more than the two bounds."""
+    E, topk = 8, 2
+    w13, w2 = experts(E, 2 * I, H, 5), experts(E, H, I, 6)
+    x = wl.random_activation_bits(T, H, seed=5)
+    router = torch.randn((T, E), generator=torch.Generator().manual_seed(T)).to(DEV)
+    out, ids, w = B.nvfp4_moe_w4a16_decode(dev_bf16(x), router, topk, upload(w13), upload(w2))
+    other = B.nvfp4_moe_w4a16_forward(dev_bf16(x), ids, w, upload(w13), upload(w2))
+    hids, hw = ids.cpu().numpy(), w.cpu().numpy()
+    _, bound = D.layer(x, hids, hw.astype(np.float64), w13, w2)
+    tol = MO.moe_tolerance(MO.moe_ref(x, hids, hw, w13, w2), hw, H)
+    assert np.all(np.abs(f64(out) - f64(other)) <= bound + tol)
