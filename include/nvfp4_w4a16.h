@@ -538,6 +538,100 @@ nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, i
                                      const float* dentropy, const float* dlse, void* dlogits,
                                      int64_t dlogits_stride, void* stream);
 
+/*
+ * int8 weights and activations, one scale per token and per channel.
+ * (vLLM API docs, compressed_tensors.schemes, class CompressedTensorsW8A8Int8,
+ * dynamic symmetric per-token activations and per-channel weights.)
+ *
+ * nvfp4_int8_quantize_rows -- row-wise int8 quantization of a bf16 [R, K] matrix:
+ *   scales[r] = max(fl32(amax_r / 127), 1e-12),  q = rne(127 a / amax_r) in [-127, 127]
+ * The codes are those of the exact ratio (nearest, ties to even); in a row whose scale is 1e-12 they
+ * are rne(fl32(a / scale)).  Non-finite values are outside the contract.  R == 0 enqueues nothing.
+ * K as below; a and q 16-byte aligned.
+ *
+ * nvfp4_int8_gemm
+ *   y[m, n] = bf16_rne( x_scales[m] * w_scales[n] * sum_k xq[m, k] * wq[n, k] + bias[n] )
+ * The sum is exact (any int8 codes, -128 among them), scaling and bias are float32.
+ *   xq       in  int8 [M, K], 16-byte aligned; 0 <= M <= 2^22 (M == 0 enqueues nothing)
+ *   wq       in  int8 [N, K], 16-byte aligned; K % 16 == 0, 16 <= K < 2^17
+ *   x_scales, w_scales  in  float [M], [N]
+ *   bias     in  bf16 [N] or NULL
+ *   y        out bf16 [M, N], 16-byte aligned
+ */
+nvfp4_status nvfp4_int8_quantize_rows(const void* a, int64_t R, int64_t K, int8_t* q, float* scales, void* stream);
+nvfp4_status nvfp4_int8_gemm(const int8_t* xq, const float* x_scales, int64_t M, int64_t K, const int8_t* wq,
+                             const float* w_scales, int64_t N, const void* bias, void* y, void* stream);
+
+/*
+ * Softmax cross entropy straight from hidden states and the bf16 lm_head weight (the
+ * weight that nvfp4_quantize takes; after a training step
+ * nvfp4_refresh_inplace re-derives the quantized copy), and its gradients.  The
+ * logits are never in memory.  With z[i, j] = sum_k x[i, k] weight[j, k] + bias[j]
+ * (float32 sums, not rounded):
+ *   stats[i] = (m, s),  m = max_j z[i, j],  s = sum_j exp(z[i, j] - m)
+ *   lse[i]   = m + log s
+ *   loss[i]  = (m - z[i, t]) + log s,  t = targets[i]
+ * A row whose target is outside [0, V) does not count: loss and lse 0, stats (0, 1),
+ * gradient 0, and neither its x nor its dloss is looked at.  The others are
+ * gathered first, so rows that do not count cost nothing.  A logit of -inf (a bias
+ * of -inf masks a token) has probability 0 and no gradient; a target there has
+ * loss +inf, and in a row with nothing else lse is -inf.  A NaN or +inf logit makes its
+ * row's loss and lse NaN.
+ *
+ * nvfp4_linear_ce_backward: with p = exp(z - m) / s, z computed again,
+ *   dz[i, j]    = bf16_rne( (dloss[i] + dlse[i]) * p[i, j] - dloss[i] * 1[j = t] )
+ *   dx[i, k]    = bf16_rne( sum_j dz[i, j] * weight[j, k] )
+ *   dweight[j, k] = bf16_rne( sum_i dz[i, j] * x[i, k] ),  dbias[j] = bf16_rne( sum_i dz[i, j] )
+ * float32 sums.  dz is rounded to bf16 because it is an operand of the two products.
+ *
+ *   x          in  bf16 [M, K], 16-byte aligned; 0 <= M <= 2^22 (M == 0 enqueues nothing: a
+ *                  caller's dweight and dbias stay as they are)
+ *   weight     in  bf16 [V, K], 16-byte aligned; K % 16 == 0, 16 <= K <= 2^20
+ *   bias       in  bf16 [V] or NULL
+ *   targets    in  int32 [M]
+ *   workspace  tmp nvfp4_linear_ce_workspace_bytes(M, V, K, backward) bytes, 16-byte aligned; its
+ *                  contents need no preparation, and the two calls may share one of the larger size
+ *   loss       out float [M];  lse out float [M] or NULL;  stats out float [M, 2], 8-byte aligned
+ *   dloss      in  float [M];  dlse in float [M] or NULL (0)
+ *   dx, dweight, dbias  out  bf16, each optional (NULL), dx and dweight 16-byte aligned
+ */
+int64_t nvfp4_linear_ce_workspace_bytes(int64_t M, int64_t V, int64_t K, int backward);
+nvfp4_status nvfp4_linear_ce(const void* x, int64_t M, int64_t K, const void* weight, int64_t V, const void* bias,
+                             const int32_t* targets, void* workspace, float* loss, float* lse, float* stats,
+                             void* stream);
+nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const void* weight, int64_t V,
+                                      const void* bias, const int32_t* targets, const float* stats,
+                                      const float* dloss, const float* dlse, void* workspace, void* dx,
+                                      void* dweight, void* dbias, void* stream);
+
+/*
+ * Gated feed-forward block on bf16 weights: the dense block beside the expert
+ * layer, with the experts' layout of w13 (rows [w1; w3]).
+ *   [g, u] = x w13^T,  a = silu(g) * u,  y = bf16_rne(a w2^T)
+ * float32 sums; a enters its product rounded to bf16.  h, where given, receives [g, u, a]
+ * rounded to bf16 for the backward pass:
+ *   da = dy w2,  dg = da * u * silu'(g),  du = da * silu(g)
+ *   dx = [dg, du] w13,  dw13 = [dg, du]^T x,  dw2 = dy^T a
+ * with g, u and a from h, and dg and du rounded to bf16 as operands of the products.
+ *
+ *   x          in  bf16 [T, H]; 0 <= T <= 2^22 (T == 0 enqueues nothing: dw13 and dw2 stay as they
+ *                  are)
+ *   w13, w2    in  bf16 [2 I, H], [H, I]; H and I multiples of 16, H <= 2^20, I <= 2^19, I * H <= 0x38000000
+ *   h          out (forward, or NULL) / in (backward)  bf16 [T, 3 I]
+ *   dy         in  bf16 [T, H]
+ *   workspace  tmp nvfp4_gated_ffn_workspace_bytes(T, H, I, backward) bytes; its contents need no
+ *                  preparation, and the two calls may share one of the larger size
+ *   y          out bf16 [T, H]
+ *   dx, dw13, dw2  out  bf16 as x, w13 and w2, each optional (NULL)
+ * Every pointer is 16-byte aligned.
+ */
+int64_t nvfp4_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, int backward);
+nvfp4_status nvfp4_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I,
+                             void* h, void* workspace, void* y, void* stream);
+nvfp4_status nvfp4_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
+                                      const void* w2, int64_t I, const void* dy, void* workspace, void* dx,
+                                      void* dw13, void* dw2, void* stream);
+
 /* Host-side helpers (no device work). */
 const char* nvfp4_status_string(int status);   /* static string for a status code        */
 const char* nvfp4_last_hip_error(void);        /* last HIP error text of this thread, or "" */

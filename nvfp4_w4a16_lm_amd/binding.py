@@ -55,6 +55,9 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_refresh_inplace", "nvfp4_w4a16_gemm",
             "nvfp4_moe_combine", "nvfp4_moe_workspace_bytes", "nvfp4_moe_w4a16_forward",
             "nvfp4_moe_decode_workspace_bytes", "nvfp4_moe_w4a16_decode", "nvfp4_int4_gemm",
             "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "nvfp4_logprobs_backward",
+            "nvfp4_int8_quantize_rows", "nvfp4_int8_gemm",
+            "nvfp4_linear_ce_workspace_bytes", "nvfp4_linear_ce", "nvfp4_linear_ce_backward",
+            "nvfp4_gated_ffn_workspace_bytes", "nvfp4_gated_ffn", "nvfp4_gated_ffn_backward",
             "nvfp4_status_string", "nvfp4_last_hip_error", "nvfp4_abi_version")
 
 
@@ -137,6 +140,22 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_logprobs_backward.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64,
                                             vp]
     lib.nvfp4_logprobs_backward.restype = ctypes.c_int
+    lib.nvfp4_int8_quantize_rows.argtypes = [vp, i64, i64, vp, vp, vp]
+    lib.nvfp4_int8_quantize_rows.restype = ctypes.c_int
+    lib.nvfp4_int8_gemm.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, vp, vp]
+    lib.nvfp4_int8_gemm.restype = ctypes.c_int
+    for name in ("nvfp4_linear_ce_workspace_bytes", "nvfp4_gated_ffn_workspace_bytes"):
+        fn = getattr(lib, name)
+        fn.argtypes = [i64, i64, i64, ctypes.c_int]
+        fn.restype = i64
+    lib.nvfp4_linear_ce.argtypes = [vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+    lib.nvfp4_linear_ce.restype = ctypes.c_int
+    lib.nvfp4_linear_ce_backward.argtypes = [vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.nvfp4_linear_ce_backward.restype = ctypes.c_int
+    lib.nvfp4_gated_ffn.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp]
+    lib.nvfp4_gated_ffn.restype = ctypes.c_int
+    lib.nvfp4_gated_ffn_backward.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    lib.nvfp4_gated_ffn_backward.restype = ctypes.c_int
     lib.nvfp4_status_string.argtypes = [ctypes.c_int]
     lib.nvfp4_status_string.restype = ctypes.c_char_p
     lib.nvfp4_last_hip_error.argtypes = []
@@ -848,3 +867,203 @@ def nvfp4_logprobs_backward(logits: torch.Tensor, token_ids: torch.Tensor | None
                                        _ptr(allowed), _ptr(lse), _ptr(entropy), _ptr(dlogprob), _ptr(dentropy),
                                        _ptr(dlse), _ptr(out), ostride, _stream_of(logits, stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# int8 weights and activations
+# ---------------------------------------------------------------------------
+
+@_on_its_stream
+def nvfp4_int8_quantize_rows(a: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                             stream=None):
+    """bf16 [R, K] -> (int8 [R, K], float32 [R]): one scale per row (per output
+    channel of a weight, per token of an activation)."""
+    a = _as_bf16_2d(a, "a")
+    r, k = a.shape
+    dev = a.device
+    if q is None:
+        q = torch.empty((r, k), dtype=torch.int8, device=dev)
+    else:
+        _check_out(q, (r, k), (torch.int8,), dev, "q")
+    if scales is None:
+        scales = torch.empty((r,), dtype=torch.float32, device=dev)
+    else:
+        _check_out(scales, (r,), (torch.float32,), dev, "scales")
+    lib = load_library()
+    _check("nvfp4_int8_quantize_rows",
+           lib.nvfp4_int8_quantize_rows(_ptr(a), r, k, _ptr(q), _ptr(scales), _stream_of(a, stream)))
+    return q, scales
+
+
+@_on_its_stream
+def nvfp4_int8_gemm(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor,
+                    bias: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bf16 [M, N] = x_scales[m] * w_scales[n] * (xq . wq^T) (+ bias), int8 xq [M, K] and wq [N, K]."""
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError(f"xq {tuple(xq.shape)} and wq {tuple(wq.shape)} must be [M, K] and [N, K]")
+    m, k = xq.shape
+    n = wq.shape[0]
+    dev = wq.device
+    if not wq.is_cuda:
+        raise ValueError("wq must be a device tensor")
+    _check_out(xq, (m, k), (torch.int8,), dev, "xq")
+    _check_out(wq, (n, k), (torch.int8,), dev, "wq")
+    _check_out(x_scales, (m,), (torch.float32,), dev, "x_scales")
+    _check_out(w_scales, (n,), (torch.float32,), dev, "w_scales")
+    if bias is not None:
+        _check_out(bias, (n,), (torch.bfloat16,), dev, "bias")
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_out(out, (m, n), (torch.bfloat16,), dev, "out")
+    lib = load_library()
+    _check("nvfp4_int8_gemm",
+           lib.nvfp4_int8_gemm(_ptr(xq), _ptr(x_scales), m, k, _ptr(wq), _ptr(w_scales), n, _ptr(bias), _ptr(out),
+                               _stream_of(wq, stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy from hidden states
+# ---------------------------------------------------------------------------
+
+class LinearCE(NamedTuple):
+    """Outputs of nvfp4_linear_ce."""
+    loss: torch.Tensor      # float32 [M]
+    lse: torch.Tensor       # float32 [M]
+    stats: torch.Tensor     # float32 [M, 2], for nvfp4_linear_ce_backward
+
+
+def _workspace(need: int, workspace, dev, fn: str, sizes: str) -> torch.Tensor:
+    if need == 0:
+        raise NVFP4ShapeError(fn, 2, sizes)
+    if workspace is None:
+        return torch.empty((need,), dtype=torch.uint8, device=dev)
+    if workspace.numel() * workspace.element_size() < need or workspace.device != dev or \
+            not workspace.is_contiguous():
+        raise ValueError(f"workspace needs {need} contiguous bytes on {dev}")
+    return workspace
+
+
+def linear_ce_workspace(m: int, v: int, k: int, device, backward: bool = True) -> torch.Tensor:
+    """Workspace of nvfp4_linear_ce, and with ``backward`` of nvfp4_linear_ce_backward too, to be kept."""
+    need = int(load_library().nvfp4_linear_ce_workspace_bytes(m, v, k, int(backward)))
+    return _workspace(need, None, device, "nvfp4_linear_ce", f"M={m}, V={v}, K={k}")
+
+
+def _check_linear_ce(x, weight, targets, bias):
+    x = _as_bf16_2d(x, "x")
+    weight = _as_bf16_2d(weight, "weight")
+    m, k = x.shape
+    v = weight.shape[0]
+    dev = x.device
+    if weight.shape[1] != k or weight.device != dev:
+        raise ValueError(f"weight {tuple(weight.shape)} on {weight.device} does not match x {tuple(x.shape)} on {dev}")
+    _check_vec(targets, m, torch.int32, dev, "targets")
+    _check_vec(bias, v, torch.bfloat16, dev, "bias")
+    return x, weight, m, v, k, dev
+
+
+@_on_its_stream
+def nvfp4_linear_ce(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, bias: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> LinearCE:
+    """Cross entropy of each row of softmax(x . weight^T (+ bias)) against its target, without the
+    logits in memory: bf16 x [M, K], weight [V, K], bias [V], int32 targets [M] (a row whose target
+    is outside [0, V) does not count)."""
+    x, weight, m, v, k, dev = _check_linear_ce(x, weight, targets, bias)
+    lib = load_library()
+    need = int(lib.nvfp4_linear_ce_workspace_bytes(m, v, k, 0))
+    workspace = _workspace(need, workspace, dev, "nvfp4_linear_ce", f"M={m}, V={v}, K={k}")
+    loss = torch.empty((m,), dtype=torch.float32, device=dev)
+    lse = torch.empty((m,), dtype=torch.float32, device=dev)
+    stats = torch.empty((m, 2), dtype=torch.float32, device=dev)
+    _check("nvfp4_linear_ce",
+           lib.nvfp4_linear_ce(_ptr(x), m, k, _ptr(weight), v, _ptr(bias), _ptr(targets), _ptr(workspace), _ptr(loss),
+                               _ptr(lse), _ptr(stats), _stream_of(x, stream)))
+    return LinearCE(loss, lse, stats)
+
+
+@_on_its_stream
+def nvfp4_linear_ce_backward(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor,
+                             dloss: torch.Tensor, bias: torch.Tensor | None = None, dlse: torch.Tensor | None = None,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of nvfp4_linear_ce: (dx [M, K], dweight [V, K], dbias [V] or None without a bias), all
+    bfloat16, from the gradients of its loss and lse (float32 [M], dlse or None) and its stats."""
+    x, weight, m, v, k, dev = _check_linear_ce(x, weight, targets, bias)
+    _check_out(stats, (m, 2), (torch.float32,), dev, "stats")
+    _check_vec(dloss, m, torch.float32, dev, "dloss")
+    _check_vec(dlse, m, torch.float32, dev, "dlse")
+    lib = load_library()
+    need = int(lib.nvfp4_linear_ce_workspace_bytes(m, v, k, 1))
+    workspace = _workspace(need, workspace, dev, "nvfp4_linear_ce_backward", f"M={m}, V={v}, K={k}")
+    make = torch.empty if m else torch.zeros           # no rows: the gradients are zero
+    dx = make((m, k), dtype=torch.bfloat16, device=dev)
+    dw = make((v, k), dtype=torch.bfloat16, device=dev)
+    db = make((v,), dtype=torch.bfloat16, device=dev) if bias is not None else None
+    _check("nvfp4_linear_ce_backward",
+           lib.nvfp4_linear_ce_backward(_ptr(x), m, k, _ptr(weight), v, _ptr(bias), _ptr(targets), _ptr(stats),
+                                        _ptr(dloss), _ptr(dlse), _ptr(workspace), _ptr(dx), _ptr(dw), _ptr(db),
+                                        _stream_of(x, stream)))
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------------------
+# Gated feed-forward block
+# ---------------------------------------------------------------------------
+
+def gated_ffn_workspace(t: int, h: int, i: int, device, backward: bool = True) -> torch.Tensor:
+    """Workspace of nvfp4_gated_ffn, and with ``backward`` of nvfp4_gated_ffn_backward too, to be kept."""
+    need = int(load_library().nvfp4_gated_ffn_workspace_bytes(t, h, i, int(backward)))
+    return _workspace(need, None, device, "nvfp4_gated_ffn", f"T={t}, H={h}, I={i}")
+
+
+def _check_gated_ffn(x, w13, w2):
+    x = _as_bf16_2d(x, "x")
+    w13 = _as_bf16_2d(w13, "w13")
+    w2 = _as_bf16_2d(w2, "w2")
+    t, h = x.shape
+    i = w2.shape[1]
+    dev = x.device
+    if tuple(w13.shape) != (2 * i, h) or w2.shape[0] != h or w13.device != dev or w2.device != dev:
+        raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} must be [2 I, H] and [H, I] on {dev}, H={h}")
+    return x, w13, w2, t, h, i, dev
+
+
+@_on_its_stream
+def nvfp4_gated_ffn(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, keep_h: bool = False,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """The gated block: bf16 x [T, H], w13 [2 I, H] (rows [w1; w3]), w2 [H, I] -> bf16 y [T, H] =
+    (silu(x w1^T) * (x w3^T)) w2^T; with ``keep_h`` (y, h), h = bf16 [T, 3 I] for the backward pass (gate, up, activation)."""
+    x, w13, w2, t, hdim, i, dev = _check_gated_ffn(x, w13, w2)
+    lib = load_library()
+    need = int(lib.nvfp4_gated_ffn_workspace_bytes(t, hdim, i, 0))
+    workspace = _workspace(need, workspace, dev, "nvfp4_gated_ffn", f"T={t}, H={hdim}, I={i}")
+    y = torch.empty((t, hdim), dtype=torch.bfloat16, device=dev)
+    h = torch.empty((t, 3 * i), dtype=torch.bfloat16, device=dev) if keep_h else None
+    _check("nvfp4_gated_ffn",
+           lib.nvfp4_gated_ffn(_ptr(x), t, hdim, _ptr(w13), _ptr(w2), i, _ptr(h), _ptr(workspace), _ptr(y),
+                               _stream_of(x, stream)))
+    return (y, h) if keep_h else y
+
+
+@_on_its_stream
+def nvfp4_gated_ffn_backward(x: torch.Tensor, h: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, dy: torch.Tensor,
+                             workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of nvfp4_gated_ffn: (dx [T, H], dw13 [2 I, H], dw2 [H, I]), all bfloat16, from dy
+    [T, H] and the h that the forward pass kept."""
+    x, w13, w2, t, hdim, i, dev = _check_gated_ffn(x, w13, w2)
+    dy = _as_bf16_2d(dy, "dy")
+    h = _as_bf16_2d(h, "h")
+    _check_out(dy, (t, hdim), (torch.bfloat16,), dev, "dy")
+    _check_out(h, (t, 3 * i), (torch.bfloat16,), dev, "h")
+    lib = load_library()
+    need = int(lib.nvfp4_gated_ffn_workspace_bytes(t, hdim, i, 1))
+    workspace = _workspace(need, workspace, dev, "nvfp4_gated_ffn_backward", f"T={t}, H={hdim}, I={i}")
+    make = torch.empty if t else torch.zeros           # no rows: the gradients are zero
+    dx = make((t, hdim), dtype=torch.bfloat16, device=dev)
+    dw13 = make((2 * i, hdim), dtype=torch.bfloat16, device=dev)
+    dw2 = make((hdim, i), dtype=torch.bfloat16, device=dev)
+    _check("nvfp4_gated_ffn_backward",
+           lib.nvfp4_gated_ffn_backward(_ptr(x), t, hdim, _ptr(h), _ptr(w13), _ptr(w2), i, _ptr(dy), _ptr(workspace),
+                                        _ptr(dx), _ptr(dw13), _ptr(dw2), _stream_of(x, stream)))
+    return dx, dw13, dw2

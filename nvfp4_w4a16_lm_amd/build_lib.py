@@ -22,6 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["nvfp4_quant.hip", "nvfp4_decode.hip", "nvfp4_prefill.hip", "nvfp4_import.hip", "fp8_lmhead.hip", "nvfp4_w4a4.hip", "nvfp4_moe.hip",
            "logprobs.hip", "int4_gemm.hip", "moe_decode.hip",
+           "int8_gemm.hip", "linear_ce.hip", "gated_ffn.hip",
            "nvfp4_api.cpp"]
 
 # Packed-fp32 VALU forms are disabled for all device code.

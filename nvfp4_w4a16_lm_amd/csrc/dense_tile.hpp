@@ -1,0 +1,527 @@
+// Dense matrix products on 128-byte slabs of the contraction (gfx950): the tile
+// kernel behind the int8 product, the cross entropy and the gated block.
+//
+//   acc[m][n] = sum_k Q[m][k] P[n][k],   the epilogue a template parameter.
+//
+// Each operand is stored either with k contiguous in a row ("straight": rows n or
+// m) or with k as the row ("transposed": bf16 only), so that the three products
+// of a linear layer, y = x W^T, dx = dy W and dW = dy^T x, read their tensors
+// as they lie.
+//
+// Four wavefronts, WN x WM of them over the tile, each IT x JT tiles of
+// v_mfma_f32_32x32x16_bf16 (or v_mfma_i32_32x32x32_i8: the same bytes).  The n side is
+// the instruction's row operand, so that a lane's accumulators are runs of four
+// n of one m.  A step is 128 bytes of k (64 bf16, 128 int8) in four sub-steps.
+//
+// Copies go straight to LDS (buffer loads with the LDS flag; what lies past an
+// operand's end reads as zero), into a ring of R steps; one barrier a step:
+//   * sub-steps 0..2: MFMAs, beside them the fragments of the next sub-step;
+//   * wait for the own copies of step s + 1, barrier: that step is visible, and
+//     nobody reads step s's buffer any more;
+//   * sub-step 3: MFMAs, the fragments of step s + 1's first sub-step, and the copies
+//     of step s + R into the buffer that has become free.
+// Straight rows take 128 bytes of LDS, their 16-byte pieces swizzled by the row;
+// half h of the wavefront supplies pieces 4 h + u in sub-step u.  A transposed
+// tile keeps its rows of k; ds_read_b64_tr_b16 hands each lane four k of one
+// column, twice for the eight k of a fragment, in the same order of k.
+#pragma once
+
+#include <type_traits>
+
+#include "nvfp4_device.hpp"
+#include "nvfp4_launch.hpp"
+
+namespace nvfp4 {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2t __attribute__((ext_vector_type(2)));
+
+enum TileEpilogue : int {
+  kTileBf16,        // out bf16 [m][n]
+  kTileF32,         // out float [split][m][n], added to what is there if accumulate
+  kTileInt8,        // out bf16 [m][n] = acc * sx[m] * sw[n] + bias[n]
+  kTileGated,       // P = [gate; up]: out a = silu(g) u, optionally h = [g, u, .]
+  kTileGatedBack,   // acc = da: dh = [da u silu'(g), da silu(g)], from h
+  kTileCeStats,     // per (m, tile of n): maximum and sum of exp, and the target's logit
+  kTileCeGrad       // out bf16 [m][n] = gradient of the logits
+};
+
+struct TileArgs {
+  const uint8_t* p;          // n side
+  const uint8_t* q;          // m side
+  int64_t p_pitch, q_pitch;  // bytes of a stored row
+  int64_t p_rows, q_rows;    // rows stored (straight: rows of the side; transposed: rows of k)
+  int32_t M, N, K;           // K in elements, a multiple of a 16-byte piece
+  const int32_t* m_count;    // device count in place of M, q_rows (NULL: none)
+  const int32_t* k_count;    // device count in place of K, p_rows and q_rows (transposed sides)
+  int32_t m_tiles, n_tiles, splits, k_split;   // k of a split, a multiple of a step
+  void* out;
+  int64_t out_pitch;         // elements
+  int32_t accumulate;
+  // epilogues
+  const float* sx;
+  const float* sw;
+  const uint16_t* bias;      // [n]
+  int32_t I;                 // gated: width of a half
+  uint16_t* h;               // gated: [m][3 I], its first 2 I written (forward, may be NULL) or read (backward)
+  uint16_t* dh;              // gated backward [m][2 I]
+  const int32_t* tok;        // [m] target of each row
+  float2* parts;             // [m][part_pitch]
+  int32_t part_pitch, n_first;   // n_first: n of column 0 (a piece of the vocabulary)
+  float* tlogit;             // [m]
+  const float2* stats;       // [m] (maximum, sum)
+  const float2* coef;        // [m] (dloss + dlse, dloss)
+};
+
+// s_waitcnt immediate: vmcnt(vm) lgkmcnt(0), expcnt left alone
+constexpr int tile_wait(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x0070; }
+constexpr int kTileThreads = 256;
+constexpr uint32_t kTileNowhere = 0xF0000000u;   // a buffer offset past every operand: reads as zero
+
+typedef __attribute__((address_space(3))) void* tile_lds_t;
+typedef __attribute__((address_space(3))) s16x4* tile_tr_t;
+
+// A transposing LDS read.  __restrict gives the read alias information: without any, the compiler waits before
+// it for every copy to LDS in flight, as it does not for ordinary LDS reads.
+__device__ __forceinline__ s16x4 tile_read_tr(tile_tr_t __restrict at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(at);
+}
+
+__device__ __forceinline__ void tile_copy16(__amdgpu_buffer_rsrc_t r, tile_lds_t dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {      // nearest even; NaN stays NaN
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2t));
+}
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+}
+__device__ __forceinline__ void unpack8(u32x4 w, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = bf16_lo(w[e]);
+    v[2 * e + 1] = bf16_hi(w[e]);
+  }
+}
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+__device__ __forceinline__ float sigmoid_fast(float g) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-g)); }
+
+template <int IT_, int JT_, int WN_, int WM_, bool PT_, bool QT_, int EPI_, int R_>
+struct TileCfg {
+  static constexpr int IT = IT_, JT = JT_, WN = WN_, WM = WM_, EPI = EPI_, R = R_;
+  static constexpr bool PT = PT_, QT = QT_, I8 = EPI_ == kTileInt8;
+  static constexpr int BN = 32 * IT * WN, BM = 32 * JT * WM;
+  static constexpr int KE = I8 ? 128 : 64;                      // elements of k per step
+  static constexpr int kPBytes = BN * 128, kQBytes = BM * 128;
+  static constexpr int kBuf = kPBytes + kQBytes;
+  static constexpr int kCopies = kBuf / 4096;                   // copies per wavefront per step
+  static constexpr int kStageRows = 32 * WM, kStagePitch = BN + 4;
+  static constexpr int kStage = kStageRows * kStagePitch * 4;
+  static constexpr int kLds = R * kBuf > kStage ? R * kBuf : kStage;
+  static_assert(WN * WM == 4 && kLds <= 160 * 1024, "tile");
+  static_assert(!I8 || (!PT && !QT), "int8 operands are straight");
+  static_assert((R - 1) * kCopies < 64, "copies in flight");
+};
+
+template <class C>
+__global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a) {
+  constexpr int IT = C::IT, JT = C::JT, R = C::R, BN = C::BN, BM = C::BM;
+  constexpr bool PT = C::PT, QT = C::QT;
+  constexpr int kPC = BN / 32;                                  // copies of the n side
+  constexpr int kMf = IT * JT;                                  // MFMAs per sub-step
+  constexpr int kReads = IT * (PT ? 2 : 1) + JT * (QT ? 2 : 1);
+  using Acc = std::conditional_t<C::I8, i32x16, f32x16>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % C::WN, wm = wave / C::WN;
+  const int r = lane & 31, h = lane >> 5;
+
+  // Workgroup b runs on XCD b % 8: each XCD takes one run of tiles, and in it
+  // patches of up to eight tiles of m under neighbouring tiles of n, so that
+  // what its compute units copy at a time meets in its own L2.
+  const int total = gridDim.x, xcd = blockIdx.x & 7;
+  const int t = xcd * (total >> 3) + min(xcd, total & 7) + (blockIdx.x >> 3);
+  const int tiles = a.m_tiles * a.n_tiles;
+  const int split = t / tiles, tile = t % tiles;
+  const int group = tile / (8 * a.n_tiles), in_group = tile % (8 * a.n_tiles);
+  const int gm = min(8, a.m_tiles - 8 * group);
+  const int m0 = (8 * group + in_group % gm) * BM, nt = in_group / gm;
+  const int n0 = nt * (C::EPI == kTileGated ? BN / 2 : BN);
+  const int M = a.m_count ? *a.m_count : a.M;
+  if (m0 >= M) return;
+  const int K = a.k_count ? *a.k_count : a.K;
+  const int k_begin = split * a.k_split, k_end = min(K, k_begin + a.k_split);
+  const int nsteps = k_end > k_begin ? (k_end - k_begin + C::KE - 1) / C::KE : 0;
+
+  // Straight copies: instruction c of wavefront w fills rows 8 (4 c + w) .. + 7, lane l slot l & 7 of row
+  // 8 (4 c + w) + (l >> 3), i.e. piece (l & 7) ^ (l >> 3) ^ (w & 1).  Transposed: with W columns a
+  // row has W / 8 pieces; lane l fills slot l % (W / 8) of row l / (W / 8) of the instruction's.
+  const int piece = (lane & 7) ^ (lane >> 3) ^ (wave & 1);
+  const uint8_t* p_base;
+  const uint8_t* q_base;
+  uint32_t p_range = 0, q_range = 0, p_off, q_off;
+  constexpr int kPPr = BN / 8, kQPr = BM / 8;                   // pieces of a transposed row
+  auto tr_swizzle = [](int row, int pieces) { return pieces >= 8 ? 2 * (row & 3) : 0; };
+  if (!PT) {
+    p_base = a.p + (int64_t)n0 * a.p_pitch;
+    p_range = (uint32_t)min((int64_t)0xE0000000u, (a.p_rows - n0) * a.p_pitch);
+    p_off = (uint32_t)((8 * wave + (lane >> 3)) * a.p_pitch + 16 * piece);
+  } else {
+    p_base = a.p + (int64_t)n0 * 2;
+    const int row = wave * (64 / kPPr) + lane / kPPr;
+    p_off = (uint32_t)(row * a.p_pitch + 16 * ((lane % kPPr) ^ tr_swizzle(row, kPPr)));
+  }
+  if (!QT) {
+    q_base = a.q + (int64_t)m0 * a.q_pitch;
+    q_range = (uint32_t)min((int64_t)0xE0000000u, ((a.m_count ? M : a.q_rows) - m0) * a.q_pitch);
+    q_off = (uint32_t)((8 * wave + (lane >> 3)) * a.q_pitch + 16 * piece);
+  } else {
+    q_base = a.q + (int64_t)m0 * 2;
+    const int row = wave * (64 / kQPr) + lane / kQPr;
+    q_off = (uint32_t)(row * a.q_pitch + 16 * ((lane % kQPr) ^ tr_swizzle(row, kQPr)));
+  }
+  const int piece_k = piece * (C::KE / 8);
+  // row of P's tile at which copy c starts, relative to n0 (gated: each wavefront column's rows are its
+  // gates, then its ups)
+  auto p_row = [&](int c) __attribute__((always_inline)) -> int64_t {
+    if constexpr (C::EPI == kTileGated) {
+      constexpr int half = 16 * IT;
+      const int row = 32 * c, g = row / (2 * half), in = row % (2 * half);
+      return in < half ? half * g + in : (int64_t)a.I + half * g + in - half;
+    } else {
+      return 32 * c;
+    }
+  };
+
+  // copy c of step st into ring buffer ph (steps past the last: nothing is read, zeros arrive)
+  auto copy_one = [&](int st, int ph, int c) __attribute__((always_inline)) {
+    uint8_t* const buf = lds + ph * C::kBuf;
+    const bool live = st < nsteps;
+    const int k0 = k_begin + st * C::KE;
+    if (c < kPC) {
+      uint8_t* const dst = buf + (4 * c + wave) * 1024;
+      if constexpr (!PT) {
+        const __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc((void*)p_base, (short)0, live ? (int)p_range : 0, 0x00020000);
+        const uint32_t off = p_off + (uint32_t)(p_row(c) * a.p_pitch);
+        tile_copy16(rs, (tile_lds_t)dst, k0 + piece_k < K ? off : kTileNowhere, live ? k0 * (128 / C::KE) : 0);
+      } else {
+        const int64_t left = live ? (int64_t)(K - k0) * a.p_pitch - 2 * (int64_t)n0 : 0;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(p_base + (int64_t)k0 * a.p_pitch), (short)0, (int)min(left, (int64_t)0x7FFFFFFF), 0x00020000);
+        tile_copy16(rs, (tile_lds_t)dst, p_off + (uint32_t)(c * 4 * (64 / kPPr) * a.p_pitch), 0);
+      }
+    } else {
+      const int d = c - kPC;
+      uint8_t* const dst = buf + C::kPBytes + (4 * d + wave) * 1024;
+      if constexpr (!QT) {
+        const __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc((void*)q_base, (short)0, live ? (int)q_range : 0, 0x00020000);
+        const uint32_t off = q_off + (uint32_t)(32 * d * a.q_pitch);
+        tile_copy16(rs, (tile_lds_t)dst, k0 + piece_k < K ? off : kTileNowhere, live ? k0 * (128 / C::KE) : 0);
+      } else {
+        const int64_t left = live ? (int64_t)(K - k0) * a.q_pitch - 2 * (int64_t)m0 : 0;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(q_base + (int64_t)k0 * a.q_pitch), (short)0, (int)min(left, (int64_t)0x7FFFFFFF), 0x00020000);
+        tile_copy16(rs, (tile_lds_t)dst, q_off + (uint32_t)(d * 4 * (64 / kQPr) * a.q_pitch), 0);
+      }
+    }
+  };
+
+  // Fragment reads.  Straight: row 32 i + r of the wavefront's, piece 4 h + u.  Transposed: lane l of a
+  // group of 16 names row k = l / 4 and columns 4 (l % 4) .. + 3 and receives column l's four k.
+  const int sw = (r & 7) ^ ((r >> 3) & 1);
+  const int l16 = lane & 15, grp = (lane >> 4) & 1;
+  const int tr_low = 2 * grp + ((l16 & 3) >> 1);
+  auto frag_straight = [&](const uint8_t* base, int row0, int u) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4*>(base + (row0 + r) * 128 + 16 * ((4 * h + u) ^ sw));
+  };
+  auto frag_tr = [&](const uint8_t* base, int pieces, int tile32, int u, int e) __attribute__((always_inline)) {
+    const int row = 32 * h + 8 * u + 4 * e + (l16 >> 2);
+    const int slot = (4 * tile32 + tr_low) ^ tr_swizzle(l16 >> 2, pieces);
+    const uint8_t* const at = base + row * pieces * 16 + 16 * slot + 8 * (l16 & 1);
+    return __builtin_bit_cast(uint2, tile_read_tr((tile_tr_t)at));
+  };
+  u32x4 pf[2][IT], qf[2][JT];
+  auto read_one = [&](int ph, int u, int x, u32x4 (&pn)[IT], u32x4 (&qn)[JT]) __attribute__((always_inline)) {
+    const uint8_t* const buf = lds + ph * C::kBuf;
+    constexpr int np = IT * (PT ? 2 : 1);
+    if (x < np) {
+      if constexpr (!PT) {
+        pn[x] = frag_straight(buf, 32 * IT * wn + 32 * x, u);
+      } else {
+        const uint2 v = frag_tr(buf, kPPr, IT * wn + x / 2, u, x % 2);
+        pn[x / 2][2 * (x % 2)] = v.x;
+        pn[x / 2][2 * (x % 2) + 1] = v.y;
+      }
+    } else {
+      const int y = x - np;
+      const uint8_t* const qb = buf + C::kPBytes;
+      if constexpr (!QT) {
+        qn[y] = frag_straight(qb, 32 * JT * wm + 32 * y, u);
+      } else {
+        const uint2 v = frag_tr(qb, kQPr, JT * wm + y / 2, u, y % 2);
+        qn[y / 2][2 * (y % 2)] = v.x;
+        qn[y / 2][2 * (y % 2) + 1] = v.y;
+      }
+    }
+  };
+
+  Acc acc[IT][JT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+
+  auto mfma = [&](u32x4 p, u32x4 q, Acc c) __attribute__((always_inline)) {
+    if constexpr (C::I8)
+      return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, p), __builtin_bit_cast(i32x4, q), c, 0, 0,
+                                                   0);
+    else
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c,
+                                                     0, 0, 0);
+  };
+
+  auto kstep = [&](int st, auto PH) __attribute__((always_inline)) {
+    constexpr int ph = decltype(PH)::value, ph1 = (ph + 1) % R;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (u == 3) {
+        __builtin_amdgcn_s_waitcnt(tile_wait((R - 2) * C::kCopies));
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      u32x4(&pc)[IT] = pf[u & 1];
+      u32x4(&qc)[JT] = qf[u & 1];
+#pragma unroll
+      for (int s = 0; s < kMf; ++s) {
+        acc[s / JT][s % JT] = mfma(pc[s / JT], qc[s % JT], acc[s / JT][s % JT]);
+#pragma unroll
+        for (int x = 0; x < kReads; ++x)
+          if (x * kMf / kReads == s) read_one(u < 3 ? ph : ph1, (u + 1) & 3, x, pf[(u + 1) & 1], qf[(u + 1) & 1]);
+        if (u == 3) {
+#pragma unroll
+          for (int c = 0; c < C::kCopies; ++c)
+            if (c * kMf / C::kCopies == s) copy_one(st + R, ph, c);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  };
+
+#pragma unroll
+  for (int x = 0; x < R * C::kCopies; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
+  __builtin_amdgcn_s_waitcnt(tile_wait((R - 1) * C::kCopies));
+  asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+  for (int x = 0; x < kReads; ++x) read_one(0, 0, x, pf[0], qf[0]);
+
+  int st = 0;
+  for (; st + R <= nsteps; st += R) {
+    kstep(st, std::integral_constant<int, 0>{});
+    kstep(st + 1, std::integral_constant<int, 1 % R>{});
+    if constexpr (R > 2) kstep(st + 2, std::integral_constant<int, 2 % R>{});
+    if constexpr (R > 3) kstep(st + 3, std::integral_constant<int, 3 % R>{});
+  }
+  static_assert(R >= 2 && R <= 4, "ring");
+  if (st < nsteps) kstep(st, std::integral_constant<int, 0>{});
+  if constexpr (R > 2)
+    if (st + 1 < nsteps) kstep(st + 1, std::integral_constant<int, 1 % R>{});
+  if constexpr (R > 3)
+    if (st + 2 < nsteps) kstep(st + 2, std::integral_constant<int, 2 % R>{});
+  __builtin_amdgcn_s_waitcnt(tile_wait(0));
+  __syncthreads();
+
+  if constexpr (C::EPI == kTileCeStats) {
+    // Each lane holds 16 IT logits of each of its JT rows; wavefronts of a row meet in LDS.
+    float2* const red = reinterpret_cast<float2*>(lds);          // [WN][BM]
+    const int nb = n0 + 32 * IT * wn + 4 * h;                    // accumulator 4 q + v of row tile i: n = nb + 32 i + 8 q + v
+    if (a.bias != nullptr || n0 + BN > a.N) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int n = nb + 32 * i + 8 * q + v;
+            const float b =
+                n >= a.N ? -INFINITY : a.bias != nullptr ? __uint_as_float((uint32_t)a.bias[n] << 16) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < JT; ++j)
+              acc[i][j][4 * q + v] = n >= a.N ? -INFINITY : acc[i][j][4 * q + v] + b;
+          }
+    }
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+      const int ml = 32 * (JT * wm + j) + r, m = m0 + ml;
+      const int tok = m < M ? a.tok[m] - a.n_first - nb : -1;
+      float mx = -INFINITY, s = 0.0f, zt = 0.0f;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          mx = fmaxf(mx, acc[i][j][v]);
+          zt = tok == 32 * i + 8 * (v >> 2) + (v & 3) ? acc[i][j][v] : zt;
+        }
+      if (tok >= 0 && tok < 32 * IT && (tok & 4) == 0) a.tlogit[m] = zt;
+      // halves of a row in two lanes: one maximum for both
+      const float mm = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const float ref = mm == -INFINITY ? 0.0f : mm;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s += exp_fast(acc[i][j][v] - ref);
+      s += __shfl_xor(s, 32, 64);
+      if (h == 0) red[wn * BM + ml] = make_float2(mm, s);
+    }
+    __syncthreads();
+    for (int ml = tid; ml < BM; ml += kTileThreads) {
+      if (m0 + ml >= M) continue;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) mm = fmaxf(mm, red[w * BM + ml].x);
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < C::WN; ++w) {
+        const float2 v = red[w * BM + ml];
+        s += v.x == -INFINITY ? v.y : v.y * exp_fast(v.x - mm);    // -inf: no logit, 0, or NaN
+      }
+      a.parts[(int64_t)(m0 + ml) * a.part_pitch + nt] = make_float2(mm, s);
+    }
+    return;
+  } else {
+    // 32 rows of each wavefront row at a time through LDS, so that memory is written in whole lines
+    float* const stage = reinterpret_cast<float*>(lds);
+    constexpr int kW = C::EPI == kTileGated ? BN / 2 : BN;       // columns written
+    constexpr int kChunks = kW / 8;
+#pragma unroll
+    for (int j = 0; j < JT; ++j) {
+      if (j > 0) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e];
+          *reinterpret_cast<f32x4*>(stage + (32 * wm + r) * C::kStagePitch + 32 * (IT * wn + i) + 8 * q + 4 * h) = v;
+        }
+      __syncthreads();
+      for (int x = tid; x < C::kStageRows * kChunks; x += kTileThreads) {
+        const int row = x / kChunks, c = x % kChunks;
+        const int m = m0 + 32 * (JT * (row >> 5) + j) + (row & 31);
+        const int n = n0 + 8 * c;
+        if (m >= M || n >= (C::EPI == kTileGated ? a.I : a.N)) continue;
+        const float* const src = stage + row * C::kStagePitch;
+        float v[8];
+        if constexpr (C::EPI == kTileGated) {
+          constexpr int half = 16 * IT;
+          const int at = 2 * half * (8 * c / half) + 8 * c % half;
+          float u[8], o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = src[at + e];
+            u[e] = src[at + half + e];
+            o[e] = v[e] * sigmoid_fast(v[e]) * u[e];
+          }
+          *reinterpret_cast<u32x4*>((uint16_t*)a.out + (int64_t)m * a.out_pitch + n) = pack8(o);
+          if (a.h != nullptr) {
+            *reinterpret_cast<u32x4*>(a.h + (int64_t)m * 3 * a.I + n) = pack8(v);
+            *reinterpret_cast<u32x4*>(a.h + (int64_t)m * 3 * a.I + a.I + n) = pack8(u);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = src[8 * c + e];
+          if constexpr (C::EPI == kTileBf16) {
+            *reinterpret_cast<u32x4*>((uint16_t*)a.out + (int64_t)m * a.out_pitch + n) = pack8(v);
+          } else if constexpr (C::EPI == kTileF32) {
+            float* const o = (float*)a.out + ((int64_t)split * a.M + m) * a.out_pitch + n;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              f32x4 w = {v[e], v[e + 1], v[e + 2], v[e + 3]};
+              if (a.accumulate) w += *reinterpret_cast<const f32x4*>(o + e);
+              *reinterpret_cast<f32x4*>(o + e) = w;
+            }
+          } else if constexpr (C::EPI == kTileInt8) {
+            const float sx = a.sx[m];
+            uint16_t* const o = (uint16_t*)a.out + (int64_t)m * a.out_pitch + n;
+            const bool whole = n + 8 <= a.N;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int ne = whole ? n + e : min(n + e, a.N - 1);
+              v[e] *= sx * a.sw[ne];
+              if (a.bias != nullptr) v[e] += __uint_as_float((uint32_t)a.bias[ne] << 16);
+            }
+            const u32x4 w = pack8(v);
+            if (whole && (a.N & 7) == 0) {
+              __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (n + e < a.N) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
+          } else if constexpr (C::EPI == kTileGatedBack) {
+            const uint16_t* const hp = a.h + (int64_t)m * 3 * a.I + n;
+            float g[8], u[8], dg[8], du[8];
+            unpack8(*reinterpret_cast<const u32x4*>(hp), g);
+            unpack8(*reinterpret_cast<const u32x4*>(hp + a.I), u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float s = sigmoid_fast(g[e]), gs = g[e] * s;
+              du[e] = v[e] * gs;
+              dg[e] = v[e] * u[e] * (s + gs * (1.0f - s));
+            }
+            *reinterpret_cast<u32x4*>(a.dh + (int64_t)m * 2 * a.I + n) = pack8(dg);
+            *reinterpret_cast<u32x4*>(a.dh + (int64_t)m * 2 * a.I + a.I + n) = pack8(du);
+          } else {                                                // kTileCeGrad
+            const float2 st2 = a.stats[m], cf = a.coef[m];
+            const float scale = cf.x / st2.y;
+            const int tok = a.tok[m] - a.n_first;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float z = v[e];
+              if (a.bias != nullptr && n + e < a.N) z += __uint_as_float((uint32_t)a.bias[n + e] << 16);
+              float d = exp_fast(z - st2.x) * scale;
+              if (n + e == tok) d -= cf.y;
+              v[e] = (n + e >= a.N || z == -INFINITY) ? 0.0f : d;
+            }
+            *reinterpret_cast<u32x4*>((uint16_t*)a.out + (int64_t)m * a.out_pitch + n) = pack8(v);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Launch with the tile that suits M: 256 x 256 over 2 x 2 wavefronts, or for few rows 256 (n) x 32, 64 or 128
+// over 4 x 1, whose smaller tiles leave room for more steps in flight.
+template <class C>
+inline hipError_t launch_tile_cfg(TileArgs a, hipStream_t stream) {
+  const int width = C::EPI == kTileGated ? C::BN / 2 : C::BN;
+  const int n = C::EPI == kTileGated ? a.I : a.N;
+  a.m_tiles = (a.M + C::BM - 1) / C::BM;
+  a.n_tiles = (n + width - 1) / width;
+  const int64_t grid = (int64_t)a.m_tiles * a.n_tiles * a.splits;
+  return launch_kernel((const void*)dense_tile_kernel<C>, dim3((unsigned)grid), dim3(kTileThreads), stream, a);
+}
+
+inline int tile_rows(int64_t M) { return M > 128 ? 256 : M > 64 ? 128 : M > 32 ? 64 : 32; }
+
+template <int EPI, bool PT, bool QT>
+inline hipError_t launch_tile(const TileArgs& a, hipStream_t stream) {
+  if constexpr (!QT) {
+    switch (tile_rows(a.M)) {
+      case 32: return launch_tile_cfg<TileCfg<2, 1, 4, 1, PT, QT, EPI, 4>>(a, stream);
+      case 64: return launch_tile_cfg<TileCfg<2, 2, 4, 1, PT, QT, EPI, 3>>(a, stream);
+      case 128: return launch_tile_cfg<TileCfg<2, 4, 4, 1, PT, QT, EPI, 3>>(a, stream);
+    }
+  }
+  return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 2>>(a, stream);
+}
+
+}  // namespace nvfp4

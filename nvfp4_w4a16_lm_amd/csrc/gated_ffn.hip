@@ -1,0 +1,175 @@
+// Gated feed-forward block on bf16 weights (gfx950), forward and backward.
+//
+//   [g, u] = x W13^T,  a = silu(g) u,  y = a W2^T
+//   da = dy W2,  du = da silu(g),  dg = da u silu'(g),  silu'(g) = s + g s (1 - s), s = 1 / (1 + e^-g)
+//   dx = [dg, du] W13,  dW13 = [dg, du]^T x,  dW2 = dy^T a
+//
+// Forward: both projections, the activation and the product are one kernel
+// whose tile holds matching rows of the gate and the up projection; the
+// activation enters the down projection rounded to bf16.  Kept for the
+// backward pass: h = [g, u, a] in bf16 (a is an operand of dW2; made again from
+// the rounded g and u it would be off by two roundings more).  Backward: the
+// kernel of da = dy W2 ends in [dg, du], in bf16; then three products.
+#include "dense_tile.hpp"
+
+namespace nvfp4 {
+
+// Sum of `splits` partial products: out bf16 [M][N] from float [splits][M][N].
+__global__ __launch_bounds__(256) void gated_join_kernel(const float* __restrict__ parts, int64_t count, int splits,
+                                                         uint16_t* __restrict__ out) {
+  for (int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < count; i += 8 * 256 * (int64_t)gridDim.x) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < splits; ++s) {
+      const f32x4* const p = reinterpret_cast<const f32x4*>(parts + s * count + i);
+      const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += lo[e];
+        v[4 + e] += hi[e];
+      }
+    }
+    *reinterpret_cast<u32x4*>(out + i) = pack8(v);
+  }
+}
+
+static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
+
+// Splits of K for an [M, N] product: enough workgroups for the compute units, at least 256 k each.
+static int gated_splits(int64_t M, int64_t N, int64_t K, int cus) {
+  const int bm = tile_rows(M);
+  const int64_t tiles = (M + bm - 1) / bm * ((N + 255) / 256);
+  int64_t s = cus / tiles;
+  s = s > 16 ? 16 : s;
+  const int64_t most = K / 256 > 1 ? K / 256 : 1;
+  return (int)(s < 1 ? 1 : s > most ? most : s);
+}
+
+struct GatedLayout {
+  int64_t parts, bytes;
+};
+static GatedLayout gated_layout(int64_t T, int64_t H, int64_t I, bool backward) {
+  GatedLayout l = {};
+  int64_t at = 0;
+  // the forward pass's a and the backward's [dg, du] share a place
+  at += up256((backward ? 4 : 2) * T * I);
+  l.parts = at;
+  const int cus = 256;
+  const int sd = gated_splits(T, H, I, cus), sx = gated_splits(T, H, 2 * I, cus);
+  const int s = backward && sx > sd ? sx : sd;
+  if (s > 1) at += up256(4 * s * T * H);
+  l.bytes = at;
+  return l;
+}
+
+int64_t gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, bool backward) {
+  const int64_t b = T == 0 ? 16 : gated_layout(T, H, I, backward).bytes;
+  return b < 16 ? 16 : b;
+}
+
+// out bf16 [M, N] = q [M, K] p^T or q p (PT), K split where the tiles are few
+template <bool PT>
+static hipError_t gated_product(const void* q, int64_t q_pitch, const void* p, int64_t M, int64_t N, int64_t K, void* out,
+                                float* parts, hipStream_t stream) {
+  TileArgs a = {};
+  a.p = (const uint8_t*)p;
+  a.q = (const uint8_t*)q;
+  a.p_pitch = 2 * (PT ? N : K);
+  a.q_pitch = 2 * q_pitch;
+  a.p_rows = PT ? K : N;
+  a.q_rows = M;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.out_pitch = N;
+  const int s = gated_splits(M, N, K, 256);
+  a.k_split = (int)(((K + s - 1) / s + 63) / 64 * 64);
+  a.splits = (int)((K + a.k_split - 1) / a.k_split);
+  if (a.splits == 1) {
+    a.out = out;
+    return launch_tile<kTileBf16, PT, false>(a, stream);
+  }
+  a.out = parts;
+  const hipError_t e = launch_tile<kTileF32, PT, false>(a, stream);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (M * N / 8 + 255) / 256;
+  return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256),
+                       stream, (const float*)parts, (int64_t)(M * N), (int)a.splits, (uint16_t*)out);
+}
+
+// out bf16 [M, N] = q^T p, q [K, M], p [K, N]
+static hipError_t gated_weight_grad(const void* q, int64_t M, const void* p, int64_t p_pitch, int64_t N, int64_t K,
+                                    void* out, hipStream_t stream) {
+  TileArgs a = {};
+  a.p = (const uint8_t*)p;
+  a.q = (const uint8_t*)q;
+  a.p_pitch = 2 * p_pitch;
+  a.q_pitch = 2 * M;
+  a.p_rows = a.q_rows = K;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.splits = 1;
+  a.k_split = (int)((K + 63) / 64 * 64);
+  a.out = out;
+  a.out_pitch = N;
+  return launch_tile<kTileBf16, true, true>(a, stream);
+}
+
+hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I, void* h,
+                            void* workspace, void* y, hipStream_t stream) {
+  const GatedLayout l = gated_layout(T, H, I, false);
+  uint8_t* const ws = (uint8_t*)workspace;
+  TileArgs a = {};
+  a.p = (const uint8_t*)w13;
+  a.q = (const uint8_t*)x;
+  a.p_pitch = a.q_pitch = 2 * H;
+  a.p_rows = 2 * I;
+  a.q_rows = T;
+  a.M = (int)T;
+  a.N = (int)I;
+  a.I = (int)I;
+  a.K = (int)H;
+  a.splits = 1;
+  a.k_split = (int)((H + 63) / 64 * 64);
+  a.out = h == nullptr ? (void*)ws : (void*)((uint16_t*)h + 2 * I);
+  a.out_pitch = h == nullptr ? I : 3 * I;
+  a.h = (uint16_t*)h;
+  const hipError_t e = launch_tile<kTileGated, false, false>(a, stream);
+  if (e != hipSuccess) return e;
+  return gated_product<false>(a.out, a.out_pitch, w2, T, H, I, y, (float*)(ws + l.parts), stream);
+}
+
+hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
+                                     const void* w2, int64_t I, const void* dy, void* workspace, void* dx, void* dw13,
+                                     void* dw2, hipStream_t stream) {
+  const GatedLayout l = gated_layout(T, H, I, true);
+  uint8_t* const ws = (uint8_t*)workspace;
+  TileArgs a = {};
+  a.p = (const uint8_t*)w2;
+  a.q = (const uint8_t*)dy;
+  a.p_pitch = 2 * I;
+  a.q_pitch = 2 * H;
+  a.p_rows = H;
+  a.q_rows = T;
+  a.M = (int)T;
+  a.N = (int)I;
+  a.I = (int)I;
+  a.K = (int)H;
+  a.splits = 1;
+  a.k_split = (int)((H + 63) / 64 * 64);
+  a.h = (uint16_t*)const_cast<void*>(h);
+  a.dh = (uint16_t*)ws;
+  hipError_t e = launch_tile<kTileGatedBack, true, false>(a, stream);
+  if (e != hipSuccess) return e;
+  if (dw2 != nullptr) {
+    e = gated_weight_grad(dy, H, (const uint16_t*)h + 2 * I, 3 * I, I, T, dw2, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (dx != nullptr) {
+    e = gated_product<true>(ws, 2 * I, w13, T, H, 2 * I, dx, (float*)(ws + l.parts), stream);
+    if (e != hipSuccess) return e;
+  }
+  return dw13 == nullptr ? hipSuccess : gated_weight_grad(ws, 2 * I, x, H, H, T, dw13, stream);
+}
+
+}  // namespace nvfp4

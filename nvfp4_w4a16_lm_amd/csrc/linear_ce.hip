@@ -1,0 +1,358 @@
+// Softmax cross entropy from hidden states and the lm_head weight (gfx950), without
+// the logits ever in memory, and its gradients.
+//
+//   z = x W^T + b,  m = max_j z_j,  s = sum_j exp(z_j - m),  lse = m + log s,  loss = (m - z_t) + log s
+//   dz_j = (dloss + dlse) exp(z_j - m) / s - dloss 1[j = t]
+//   dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+//
+// Rows whose target is outside the vocabulary have no loss and no gradient: the
+// rows that count are gathered first, and only they enter the products.
+//
+// Forward: tiles of logits end as one maximum and one sum per row and tile,
+// which a second kernel joins.  Backward, for each piece of the vocabulary: the
+// logits again, ending in dz (bf16, the operand type of what follows); dx gains dz W
+// in float32; the piece of dW is dz^T x.
+#include "dense_tile.hpp"
+
+namespace nvfp4 {
+
+static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
+
+constexpr int kCeRows = 16;          // rows a workgroup gathers
+
+struct CeGather {
+  const uint16_t* x;
+  const int32_t* tok;
+  int32_t M, V, K;
+  uint16_t* xc;                      // rows that count, in order
+  int32_t* ctok;
+  int32_t* index;                    // their rows
+  int32_t* count;
+  // forward: what the other rows get
+  float* loss;
+  float* lse;
+  float2* stats;
+  // backward
+  const float2* stats_in;
+  const float* dloss;
+  const float* dlse;
+  float2* cstats;
+  float2* coef;
+  uint16_t* dx;                      // zero in the other rows
+};
+
+// Workgroup b: rows 16 b .. + 15.  Its first place is the number of earlier rows that count.
+__global__ __launch_bounds__(256) void ce_gather_kernel(CeGather a) {
+  __shared__ int part[4];
+  const int tid = threadIdx.x, row0 = blockIdx.x * kCeRows;
+  int before = 0;
+  for (int i = tid; i < row0; i += 256) before += (uint32_t)a.tok[i] < (uint32_t)a.V;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d, 64);
+  if ((tid & 63) == 0) part[tid >> 6] = before;
+  __syncthreads();
+  int place = part[0] + part[1] + part[2] + part[3];
+  const int pieces = a.K / 8;
+  for (int row = row0; row < min(row0 + kCeRows, a.M); ++row) {
+    const int tok = a.tok[row];
+    const bool counts = (uint32_t)tok < (uint32_t)a.V;
+    if (counts) {
+      const u32x4* const src = reinterpret_cast<const u32x4*>(a.x + (int64_t)row * a.K);
+      u32x4* const dst = reinterpret_cast<u32x4*>(a.xc + (int64_t)place * a.K);
+      for (int p = tid; p < pieces; p += 256) dst[p] = src[p];
+      if (tid == 0) {
+        a.ctok[place] = tok;
+        a.index[place] = row;
+        if (a.coef != nullptr) {
+          const float d = a.dloss[row];
+          a.cstats[place] = a.stats_in[row];
+          a.coef[place] = make_float2(d + (a.dlse != nullptr ? a.dlse[row] : 0.0f), d);
+        }
+      }
+      ++place;
+    } else {
+      if (a.dx != nullptr) {
+        u32x4* const dst = reinterpret_cast<u32x4*>(a.dx + (int64_t)row * a.K);
+        for (int p = tid; p < pieces; p += 256) dst[p] = u32x4{0, 0, 0, 0};
+      }
+      if (tid == 0 && a.loss != nullptr) {
+        a.loss[row] = 0.0f;
+        if (a.lse != nullptr) a.lse[row] = 0.0f;
+        a.stats[row] = make_float2(0.0f, 1.0f);
+      }
+    }
+  }
+  if (row0 + kCeRows >= a.M && tid == 0) *a.count = place;
+}
+
+// A wavefront per row joins its tiles' maxima and sums.
+__global__ __launch_bounds__(256) void ce_join_kernel(const float2* __restrict__ parts, int tiles,
+                                                      const float* __restrict__ tlogit,
+                                                      const int32_t* __restrict__ index,
+                                                      const int32_t* __restrict__ count, float* __restrict__ loss,
+                                                      float* __restrict__ lse, float2* __restrict__ stats) {
+  const int lane = threadIdx.x & 63, row = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= *count) return;
+  const float2* const p = parts + (int64_t)row * tiles;
+  float m = -INFINITY, s = 0.0f;
+  for (int i = lane; i < tiles; i += 64) {
+    const float2 v = p[i];
+    if (v.x > m) {
+      if (m != -INFINITY) s *= exp_fast(m - v.x);
+      m = v.x;
+    }
+    s += v.x == -INFINITY ? v.y : v.y * exp_fast(v.x - m);       // -inf: no logit, 0, or NaN
+  }
+  float mm = m;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d, 64));
+  if (m != mm && m != -INFINITY) s *= exp_fast(m - mm);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
+  if (lane == 0) {
+    const int at = index[row];
+    const float ls = logf(s);
+    loss[at] = tlogit[row] == -INFINITY ? (s == s ? INFINITY : s) : (mm - tlogit[row]) + ls;
+    if (lse != nullptr) lse[at] = mm == -INFINITY && s == 0.0f ? -INFINITY : mm + ls;
+    stats[at] = make_float2(mm, s);
+  }
+}
+
+// dx: the splits' sums, rounded once, back in their rows
+__global__ __launch_bounds__(256) void ce_dx_kernel(const float* __restrict__ parts, int M, int K, int splits,
+                                                    const int32_t* __restrict__ index,
+                                                    const int32_t* __restrict__ count, uint16_t* __restrict__ dx) {
+  const int row = blockIdx.x;
+  if (row >= *count) return;
+  const int64_t at = index[row];
+  for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < splits; ++s) {
+      const f32x4* const p = reinterpret_cast<const f32x4*>(parts + ((int64_t)s * M + row) * K + k);
+      const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += lo[e];
+        v[4 + e] += hi[e];
+      }
+    }
+    *reinterpret_cast<u32x4*>(dx + at * K + k) = pack8(v);
+  }
+}
+
+// db of a piece: column sums of dz, 64 columns a workgroup
+__global__ __launch_bounds__(256) void ce_bias_kernel(const uint16_t* __restrict__ d, int64_t pitch, int width,
+                                                      const int32_t* __restrict__ count, uint16_t* __restrict__ db) {
+  __shared__ float sum[32][65];
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3, rows = *count;
+  const int n = blockIdx.x * 64 + 8 * c;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n < width)
+    for (int row = g; row < rows; row += 32) {
+      float w[8];
+      unpack8(*reinterpret_cast<const u32x4*>(d + row * pitch + n), w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += w[e];
+    }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[g][8 * c + e] = v[e];
+  __syncthreads();
+  if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < width) {
+    float s = 0.0f;
+    for (int i = 0; i < 32; ++i) s += sum[i][threadIdx.x];
+    db[blockIdx.x * 64 + threadIdx.x] = (uint16_t)(pack_bf16(s, 0.0f) & 0xFFFFu);
+  }
+}
+
+constexpr int64_t kCePieceBytes = (int64_t)128 << 20;   // dz of a piece: stays in the last-level cache
+constexpr int64_t kCePieceMost = 1 << 18;               // its columns: 32-bit offsets
+
+struct CeLayout {
+  int64_t xc, ctok, index, count, parts, tlogit, cstats, coef, d, acc, bytes;
+  int64_t piece, tiles;
+  int splits;
+};
+
+static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
+  CeLayout l = {};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  l.xc = take(2 * M * K);
+  l.ctok = take(4 * M);
+  l.index = take(4 * M);
+  l.count = take(4);
+  l.tiles = (V + 255) / 256;
+  // the forward pass's part and the backward's overlap
+  const int64_t common = at;
+  l.parts = take(8 * M * l.tiles);
+  l.tlogit = take(4 * M);
+  if (backward) {
+    const int64_t forward_end = at;
+    at = common;
+    l.cstats = take(8 * M);
+    l.coef = take(8 * M);
+    int64_t most = kCePieceBytes / (2 * M) / 256 * 256;
+    most = most < 1024 ? 1024 : most > kCePieceMost ? kCePieceMost : most;
+    const int64_t pieces = (V + most - 1) / most;
+    l.piece = up256((V + pieces - 1) / pieces);
+    l.d = take(2 * M * l.piece);
+    const int bm = tile_rows(M);
+    const int64_t tiles = (M + bm - 1) / bm * ((K + 255) / 256);
+    int64_t s = 256 / tiles;
+    const int64_t deep = l.piece / 512 > 1 ? l.piece / 512 : 1;
+    s = s < 1 ? 1 : s > 64 ? 64 : s;
+    l.splits = (int)(s > deep ? deep : s);
+    l.acc = take(4 * l.splits * M * K);
+    if (at < forward_end) at = forward_end;
+  }
+  l.bytes = at;
+  return l;
+}
+
+int64_t linear_ce_workspace_bytes(int64_t M, int64_t V, int64_t K, bool backward) {
+  const int64_t b = M == 0 ? 16 : ce_layout(M, V, K, backward).bytes;
+  return b < 16 ? 16 : b;
+}
+
+static TileArgs ce_logits(const void* w, int64_t V, int64_t K, const void* bias, uint8_t* ws, const CeLayout& l,
+                          int64_t M) {
+  TileArgs a = {};
+  a.p = (const uint8_t*)w;
+  a.q = ws + l.xc;
+  a.p_pitch = a.q_pitch = 2 * K;
+  a.p_rows = V;
+  a.q_rows = M;
+  a.M = (int)M;
+  a.N = (int)V;
+  a.K = (int)K;
+  a.m_count = (const int32_t*)(ws + l.count);
+  a.splits = 1;
+  a.k_split = (int)((K + 63) / 64 * 64);
+  a.bias = (const uint16_t*)bias;
+  a.tok = (const int32_t*)(ws + l.ctok);
+  return a;
+}
+
+hipError_t launch_linear_ce(const void* x, int64_t M, int64_t K, const void* w, int64_t V, const void* bias,
+                            const int32_t* tok, void* workspace, float* loss, float* lse, float* stats,
+                            hipStream_t stream) {
+  const CeLayout l = ce_layout(M, V, K, false);
+  uint8_t* const ws = (uint8_t*)workspace;
+  CeGather g = {};
+  g.x = (const uint16_t*)x;
+  g.tok = tok;
+  g.M = (int)M;
+  g.V = (int)V;
+  g.K = (int)K;
+  g.xc = (uint16_t*)(ws + l.xc);
+  g.ctok = (int32_t*)(ws + l.ctok);
+  g.index = (int32_t*)(ws + l.index);
+  g.count = (int32_t*)(ws + l.count);
+  g.loss = loss;
+  g.lse = lse;
+  g.stats = (float2*)stats;
+  hipError_t e = launch_kernel((const void*)ce_gather_kernel, dim3((unsigned)((M + kCeRows - 1) / kCeRows)), dim3(256),
+                               stream, g);
+  if (e != hipSuccess) return e;
+  TileArgs a = ce_logits(w, V, K, bias, ws, l, M);
+  a.parts = (float2*)(ws + l.parts);
+  a.part_pitch = (int)l.tiles;
+  a.tlogit = (float*)(ws + l.tlogit);
+  e = launch_tile<kTileCeStats, false, false>(a, stream);
+  if (e != hipSuccess) return e;
+  return launch_kernel((const void*)ce_join_kernel, dim3((unsigned)((M + 3) / 4)), dim3(256), stream,
+                       (const float2*)(ws + l.parts), (int)l.tiles, (const float*)(ws + l.tlogit),
+                       (const int32_t*)g.index, (const int32_t*)g.count, loss, lse, (float2*)stats);
+}
+
+hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const void* w, int64_t V, const void* bias,
+                                     const int32_t* tok, const float* stats, const float* dloss, const float* dlse,
+                                     void* workspace, void* dx, void* dw, void* db, hipStream_t stream) {
+  const CeLayout l = ce_layout(M, V, K, true);
+  uint8_t* const ws = (uint8_t*)workspace;
+  CeGather g = {};
+  g.x = (const uint16_t*)x;
+  g.tok = tok;
+  g.M = (int)M;
+  g.V = (int)V;
+  g.K = (int)K;
+  g.xc = (uint16_t*)(ws + l.xc);
+  g.ctok = (int32_t*)(ws + l.ctok);
+  g.index = (int32_t*)(ws + l.index);
+  g.count = (int32_t*)(ws + l.count);
+  g.stats_in = (const float2*)stats;
+  g.dloss = dloss;
+  g.dlse = dlse;
+  g.cstats = (float2*)(ws + l.cstats);
+  g.coef = (float2*)(ws + l.coef);
+  g.dx = (uint16_t*)dx;
+  hipError_t e = launch_kernel((const void*)ce_gather_kernel, dim3((unsigned)((M + kCeRows - 1) / kCeRows)), dim3(256),
+                               stream, g);
+  if (e != hipSuccess) return e;
+  for (int64_t v0 = 0; v0 < V; v0 += l.piece) {
+    const int64_t width = V - v0 < l.piece ? V - v0 : l.piece;
+    const uint8_t* const wp = (const uint8_t*)w + v0 * K * 2;
+    TileArgs a = ce_logits(wp, width, K, bias == nullptr ? nullptr : (const uint16_t*)bias + v0, ws, l, M);
+    a.n_first = (int)v0;
+    a.stats = g.cstats;
+    a.coef = g.coef;
+    a.out = ws + l.d;
+    a.out_pitch = l.piece;
+    e = launch_tile<kTileCeGrad, false, false>(a, stream);
+    if (e != hipSuccess) return e;
+    if (dx != nullptr) {
+      TileArgs b = {};
+      b.p = wp;
+      b.q = ws + l.d;
+      b.p_pitch = 2 * K;
+      b.q_pitch = 2 * l.piece;
+      b.p_rows = width;
+      b.q_rows = M;
+      b.M = (int)M;
+      b.N = (int)K;
+      b.K = (int)width;
+      b.m_count = g.count;
+      b.splits = l.splits;
+      b.k_split = (int)(((width + l.splits - 1) / l.splits + 63) / 64 * 64);
+      b.out = ws + l.acc;
+      b.out_pitch = K;
+      b.accumulate = v0 > 0;
+      e = launch_tile<kTileF32, true, false>(b, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (dw != nullptr) {
+      TileArgs b = {};
+      b.p = ws + l.xc;
+      b.q = ws + l.d;
+      b.p_pitch = 2 * K;
+      b.q_pitch = 2 * l.piece;
+      b.p_rows = b.q_rows = M;
+      b.M = (int)width;
+      b.N = (int)K;
+      b.K = (int)M;
+      b.k_count = g.count;
+      b.splits = 1;
+      b.k_split = (int)((M + 63) / 64 * 64);
+      b.out = (uint16_t*)dw + v0 * K;
+      b.out_pitch = K;
+      e = launch_tile<kTileBf16, true, true>(b, stream);
+      if (e != hipSuccess) return e;
+    }
+    if (db != nullptr) {
+      e = launch_kernel((const void*)ce_bias_kernel, dim3((unsigned)((width + 63) / 64)), dim3(256), stream,
+                        (const uint16_t*)(ws + l.d), l.piece, (int)width, (const int32_t*)g.count,
+                        (uint16_t*)db + v0);
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (dx == nullptr) return hipSuccess;
+  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M), dim3(256), stream, (const float*)(ws + l.acc),
+                       (int)M, (int)K, (int)l.splits, (const int32_t*)g.index, (const int32_t*)g.count,
+                       (uint16_t*)dx);
+}
+
+}  // namespace nvfp4

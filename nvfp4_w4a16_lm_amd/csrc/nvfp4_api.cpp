@@ -647,6 +647,168 @@ nvfp4_status nvfp4_int4_gemm(const void* x, int64_t M, int64_t K, const int32_t*
   return finish(nvfp4::launch_int4_gemm(a, (hipStream_t)stream));
 }
 
+// ---------------------------------------------------------------------------
+// int8 weights and activations
+// ---------------------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxDenseM = (int64_t)1 << 22;     // rows of the dense calls
+constexpr int64_t kMaxDenseK = (int64_t)1 << 20;     // bf16 row length: 32-bit offsets inside a tile
+constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 16;  // 128 * 128 * K < 2^31
+constexpr int64_t kMaxGated = 0x38000000;            // I * H: 32-bit offsets between gate and up rows
+
+bool dense_width(int64_t k, int64_t most) { return k >= NVFP4_GROUP && k % NVFP4_GROUP == 0 && k <= most; }
+
+nvfp4_status check_linear_ce(int64_t M, int64_t V, int64_t K) {
+  if (M < 0 || M > kMaxDenseM || V < 1 || V > kMaxDim || !dense_width(K, kMaxDenseK) || V * K > kMaxElems ||
+      M * K > kMaxElems || M * V > kMaxElems)
+    return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+nvfp4_status check_gated_ffn(int64_t T, int64_t H, int64_t I) {
+  if (T < 0 || T > kMaxDenseM || !dense_width(H, kMaxDenseK) || !dense_width(I, kMaxDenseK / 2) || H * I > kMaxGated)
+    return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_int8_quantize_rows(const void* a, int64_t R, int64_t K, int8_t* q, float* scales, void* stream) {
+  if (R != 0 && (!a || !q || !scales)) return NVFP4_ERR_NULL;
+  if (R < 0 || R > kMaxDim || !dense_width(K, kMaxInt8K) || R * K > kMaxElems) return NVFP4_ERR_SHAPE;
+  if (R == 0) return NVFP4_OK;
+  if (!aligned(a, 16) || !aligned(q, 16) || !aligned(scales, 4)) return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(q, R * K), span(scales, R * 4)};
+  const Range ins[] = {span(a, R * K * 2)};
+  if (any_overlap(outs, 2, ins, 1)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  return finish(nvfp4::launch_int8_quant_rows(a, R, K, q, scales, (hipStream_t)stream));
+}
+
+nvfp4_status nvfp4_int8_gemm(const int8_t* xq, const float* x_scales, int64_t M, int64_t K, const int8_t* wq,
+                             const float* w_scales, int64_t N, const void* bias, void* y, void* stream) {
+  if (!wq || !w_scales || (M != 0 && (!xq || !x_scales || !y))) return NVFP4_ERR_NULL;
+  if (M < 0 || M > kMaxDenseM || N < 1 || N > kMaxDim || !dense_width(K, kMaxInt8K) || N * K > kMaxElems ||
+      M * N > kMaxElems)
+    return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 2) ||
+      !aligned(y, 16))
+    return NVFP4_ERR_ALIGN;
+  const Range out = span(y, M * N * 2);
+  const Range ins[] = {span(xq, M * K), span(x_scales, M * 4), span(wq, N * K), span(w_scales, N * 4),
+                       optional_span(bias, N * 2)};
+  if (any_overlap(&out, 1, ins, 5)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  return finish(nvfp4::launch_int8_gemm(xq, x_scales, M, K, wq, w_scales, N, bias, y, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// Cross entropy from hidden states
+// ---------------------------------------------------------------------------
+
+int64_t nvfp4_linear_ce_workspace_bytes(int64_t M, int64_t V, int64_t K, int backward) {
+  if ((backward != 0 && backward != 1) || check_linear_ce(M, V, K) != NVFP4_OK) return 0;
+  return nvfp4::linear_ce_workspace_bytes(M, V, K, backward != 0);
+}
+
+nvfp4_status nvfp4_linear_ce(const void* x, int64_t M, int64_t K, const void* weight, int64_t V, const void* bias,
+                             const int32_t* targets, void* workspace, float* loss, float* lse, float* stats,
+                             void* stream) {
+  if (!weight || (M != 0 && (!x || !targets || !workspace || !loss || !stats))) return NVFP4_ERR_NULL;
+  const nvfp4_status s = check_linear_ce(M, V, K);
+  if (s != NVFP4_OK) return s;
+  if (M == 0) return NVFP4_OK;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 2) || !aligned(targets, 4) ||
+      !aligned(workspace, 16) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(stats, 8))
+    return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(workspace, nvfp4::linear_ce_workspace_bytes(M, V, K, false)), span(loss, M * 4),
+                        optional_span(lse, M * 4), span(stats, M * 8)};
+  const Range ins[] = {span(x, M * K * 2), span(weight, V * K * 2), optional_span(bias, V * 2), span(targets, M * 4)};
+  if (any_overlap(outs, 4, ins, 4)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  return finish(nvfp4::launch_linear_ce(x, M, K, weight, V, bias, targets, workspace, loss, lse, stats,
+                                        (hipStream_t)stream));
+}
+
+nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const void* weight, int64_t V,
+                                      const void* bias, const int32_t* targets, const float* stats,
+                                      const float* dloss, const float* dlse, void* workspace, void* dx,
+                                      void* dweight, void* dbias, void* stream) {
+  if (M != 0 && (!x || !weight || !targets || !stats || !dloss || !workspace)) return NVFP4_ERR_NULL;
+  const nvfp4_status s = check_linear_ce(M, V, K);
+  if (s != NVFP4_OK) return s;
+  if (M == 0) return NVFP4_OK;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 2) || !aligned(targets, 4) || !aligned(stats, 8) ||
+      !aligned(dloss, 4) || !aligned(dlse, 4) || !aligned(workspace, 16) || !aligned(dx, 16) ||
+      !aligned(dweight, 16) || !aligned(dbias, 2))
+    return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(workspace, nvfp4::linear_ce_workspace_bytes(M, V, K, true)),
+                        optional_span(dx, M * K * 2), optional_span(dweight, V * K * 2),
+                        optional_span(dbias, V * 2)};
+  const Range ins[] = {span(x, M * K * 2),   span(weight, V * K * 2), optional_span(bias, V * 2),
+                       span(targets, M * 4), span(stats, M * 8),      span(dloss, M * 4),
+                       optional_span(dlse, M * 4)};
+  if (any_overlap(outs, 4, ins, 7)) return NVFP4_ERR_ALIAS;
+  if (!dx && !dweight && !dbias) return NVFP4_OK;
+  g_last_hip_error[0] = '\0';
+  return finish(nvfp4::launch_linear_ce_backward(x, M, K, weight, V, bias, targets, stats, dloss, dlse, workspace, dx,
+                                                 dweight, dbias, (hipStream_t)stream));
+}
+
+// ---------------------------------------------------------------------------
+// Gated feed-forward block
+// ---------------------------------------------------------------------------
+
+int64_t nvfp4_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, int backward) {
+  if ((backward != 0 && backward != 1) || check_gated_ffn(T, H, I) != NVFP4_OK) return 0;
+  return nvfp4::gated_ffn_workspace_bytes(T, H, I, backward != 0);
+}
+
+nvfp4_status nvfp4_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I,
+                             void* h, void* workspace, void* y, void* stream) {
+  if (!w13 || !w2 || (T != 0 && (!x || !workspace || !y))) return NVFP4_ERR_NULL;
+  const nvfp4_status s = check_gated_ffn(T, H, I);
+  if (s != NVFP4_OK) return s;
+  if (T == 0) return NVFP4_OK;
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(h, 16) || !aligned(workspace, 16) ||
+      !aligned(y, 16))
+    return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(workspace, nvfp4::gated_ffn_workspace_bytes(T, H, I, false)),
+                        optional_span(h, T * I * 6), span(y, T * H * 2)};
+  const Range ins[] = {span(x, T * H * 2), span(w13, I * H * 4), span(w2, I * H * 2)};
+  if (any_overlap(outs, 3, ins, 3)) return NVFP4_ERR_ALIAS;
+  g_last_hip_error[0] = '\0';
+  return finish(nvfp4::launch_gated_ffn(x, T, H, w13, w2, I, h, workspace, y, (hipStream_t)stream));
+}
+
+nvfp4_status nvfp4_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
+                                      const void* w2, int64_t I, const void* dy, void* workspace, void* dx,
+                                      void* dw13, void* dw2, void* stream) {
+  if (T != 0 && (!x || !h || !w13 || !w2 || !dy || !workspace)) return NVFP4_ERR_NULL;
+  const nvfp4_status s = check_gated_ffn(T, H, I);
+  if (s != NVFP4_OK) return s;
+  if (T == 0) return NVFP4_OK;
+  if (!aligned(x, 16) || !aligned(h, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(dy, 16) ||
+      !aligned(workspace, 16) || !aligned(dx, 16) || !aligned(dw13, 16) || !aligned(dw2, 16))
+    return NVFP4_ERR_ALIGN;
+  const Range outs[] = {span(workspace, nvfp4::gated_ffn_workspace_bytes(T, H, I, true)),
+                        optional_span(dx, T * H * 2), optional_span(dw13, I * H * 4), optional_span(dw2, I * H * 2)};
+  const Range ins[] = {span(x, T * H * 2), span(h, T * I * 6), span(w13, I * H * 4), span(w2, I * H * 2),
+                       span(dy, T * H * 2)};
+  if (any_overlap(outs, 4, ins, 5)) return NVFP4_ERR_ALIAS;
+  if (!dx && !dw13 && !dw2) return NVFP4_OK;
+  g_last_hip_error[0] = '\0';
+  return finish(nvfp4::launch_gated_ffn_backward(x, T, H, h, w13, w2, I, dy, workspace, dx, dw13, dw2,
+                                                 (hipStream_t)stream));
+}
+
 const char* nvfp4_status_string(int status) {
   switch (status) {
     case NVFP4_OK: return "ok";

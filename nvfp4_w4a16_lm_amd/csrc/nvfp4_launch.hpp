@@ -266,4 +266,26 @@ struct MoeDecodeArgs {
 int64_t moe_decode_workspace_bytes(int64_t T, int64_t topk, int64_t H, int64_t I);
 hipError_t launch_moe_decode(MoeDecodeArgs a, void* workspace, hipStream_t stream);
 
+// int8 weights and activations (int8_gemm.hip).
+hipError_t launch_int8_quant_rows(const void* a, int64_t R, int64_t K, int8_t* q, float* scales, hipStream_t stream);
+hipError_t launch_int8_gemm(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int8_t* wq,
+                            const float* sw, int64_t N, const void* bias, void* y, hipStream_t stream);
+
+// Cross entropy from hidden states and the lm_head weight (linear_ce.hip).
+int64_t linear_ce_workspace_bytes(int64_t M, int64_t V, int64_t K, bool backward);
+hipError_t launch_linear_ce(const void* x, int64_t M, int64_t K, const void* w, int64_t V, const void* bias,
+                            const int32_t* tok, void* workspace, float* loss, float* lse, float* stats,
+                            hipStream_t stream);
+hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const void* w, int64_t V, const void* bias,
+                                     const int32_t* tok, const float* stats, const float* dloss, const float* dlse,
+                                     void* workspace, void* dx, void* dw, void* db, hipStream_t stream);
+
+// Gated feed-forward block on bf16 weights (gated_ffn.hip).
+int64_t gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, bool backward);
+hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I, void* h,
+                            void* workspace, void* y, hipStream_t stream);
+hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
+                                     const void* w2, int64_t I, const void* dy, void* workspace, void* dx, void* dw13,
+                                     void* dw2, hipStream_t stream);
+
 }  // namespace nvfp4

@@ -1,0 +1,185 @@
+"""GPU parity of the gated feed-forward block and its gradients with the float64
+oracle: sizes around every tile width, single tokens, saturated gates,
+differences, outputs written exactly, graph replays and given streams."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.dense_oracle as D
+from nvfp4_w4a16_lm_amd import binding as B
+
+from gpu_util import DEV
+from test_gpu_graphs import capture
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def bf16(rng, *shape, sigma=1.0):
+    return torch.from_numpy(sigma * rng.standard_normal(shape)).to(BF16)
+
+
+def make(t, h, i, seed, gate=1.3):
+    rng = np.random.default_rng(seed)
+    return [bf16(rng, t, h), bf16(rng, 2 * i, h, sigma=gate / np.sqrt(h)), bf16(rng, h, i, sigma=1 / np.sqrt(i)),
+            bf16(rng, t, h, sigma=0.1)]
+
+
+def f64(t):
+    return t.cpu().double().numpy()
+
+
+def within(got, want, bound, what):
+    err = np.abs(f64(got) - want)
+    assert np.all(err <= bound), (what, err.max(), (err / bound).max())
+
+
+def check(t, h, i, seed, gate=1.3):
+    a = make(t, h, i, seed, gate)
+    x, w13, w2, dy = (v.to(DEV) for v in a)
+    y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    (wy, wh), (by, bh) = D.gated_ffn(*map(f64, a[:3]))
+    within(y, wy, by, "y")
+    within(kept, wh, bh, "h")
+    assert torch.equal(y, B.nvfp4_gated_ffn(x, w13, w2))
+    grads = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy)
+    want, bounds = D.gated_ffn_backward(f64(x), f64(kept), f64(w13), f64(w2), f64(dy))
+    for g, v, b, what in zip(grads, want, bounds, ("dx", "dw13", "dw2")):
+        within(g, v, b, what)
+    return (x, w13, w2, dy), kept, grads
+
+
+@pytest.mark.parametrize("t,h,i", [
+    (1, 16, 16), (1, 528, 1040), (2, 64, 48), (3, 256, 128), (7, 272, 528), (15, 1040, 144), (16, 512, 256), (17, 144, 272),
+    (31, 80, 400), (32, 256, 256), (33, 528, 112), (64, 336, 640), (65, 272, 528), (128, 144, 144), (129, 528, 272),
+    (200, 528, 1040), (257, 144, 528), (333, 2080, 560), (600, 272, 272)])
+def test_sizes(t, h, i):
+    check(t, h, i, seed=t + h + i)
+
+
+@pytest.mark.parametrize("t", [1, 16, 100])
+def test_saturated_gates(t):
+    """Gates of hundreds: the logistic function at 0 and 1, its exponential at infinity."""
+    check(t, 64, 128, seed=t, gate=150.0)
+
+
+def test_long_rows():
+    check(1, 4096, 2048, seed=1)
+    check(12, 1024, 8192, seed=2)
+
+
+def test_gradient_against_differences():
+    a = make(20, 64, 96, seed=3)
+    n = [f64(v) for v in a]
+    (x, w13, w2, dy), kept, grads = check(20, 64, 96, seed=3)
+    # h is rounded between the passes: each of dg, du and a moves by its slope times that
+    i = 96
+    g, u = (n[0] @ n[1].T)[:, :i], (n[0] @ n[1].T)[:, i:]
+    da = np.abs(n[3] @ n[2])
+    r = 2.0 ** -8 * 1.01
+    s = D.sigmoid(g)
+    slope = np.abs(s * (1 + g * (1 - s)))
+    e = np.concatenate((da * (np.abs(u) * 0.55 * np.abs(g) + np.abs(u) * slope) * r * 1.2, da * 1.2 * np.abs(g) * r), 1)
+    extra = (e @ np.abs(n[1]), e.T @ np.abs(n[0]), np.abs(n[3]).T @ (np.abs(g * s * u) * r))
+    _, bounds = D.gated_ffn_backward(n[0], f64(kept), n[1], n[2], n[3])
+    rng = np.random.default_rng(1)
+    f = lambda *p: (D.gated_ffn(*p)[0][0] * n[3]).sum()
+    for which, grad in enumerate(grads):
+        d = rng.standard_normal(n[which].shape)
+        up, down = n[:3], n[:3]
+        up[which], down[which] = n[which] + 1e-5 * d, n[which] - 1e-5 * d
+        diff = (f(*up) - f(*down)) / 2e-5
+        assert abs(diff - (f64(grad) * d).sum()) <= ((bounds[which] + extra[which]) * np.abs(d)).sum() + 1e-5
+
+
+def test_infinite_and_nan_rows_stay_alone():
+    x, w13, w2, dy = (v.to(DEV) for v in make(40, 64, 96, seed=5))
+    x[3, 5], x[7, 9] = float("nan"), float("inf")
+    y, h = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    bad = torch.zeros(40, dtype=torch.bool, device=DEV)
+    bad[[3, 7]] = True
+    assert torch.isfinite(y[~bad]).all() and not torch.isfinite(y[3]).any()
+    dx, _, _ = B.nvfp4_gated_ffn_backward(x, h, w13, w2, dy)
+    assert torch.isfinite(dx[~bad]).all()
+
+
+@pytest.mark.parametrize("t", [1, 20, 150])
+def test_buffers_are_written_exactly(t):
+    lib = B.load_library()
+    h, i = 80, 112
+    x, w13, w2, dy = (v.to(DEV) for v in make(t, h, i, seed=6))
+    y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    want = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy)
+    size = int(lib.nvfp4_gated_ffn_workspace_bytes(t, h, i, 1))
+    ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device=DEV)
+    outs = [torch.full((n + 32,), 3.0, dtype=BF16, device=DEV) for n in (t * h, 3 * t * i, t * h, 2 * i * h, h * i)]
+    p = [o.data_ptr() for o in outs]
+    s = torch.cuda.current_stream().cuda_stream
+    xp, w13p, w2p, dyp = (v.data_ptr() for v in (x, w13, w2, dy))
+    assert lib.nvfp4_gated_ffn(xp, t, h, w13p, w2p, i, p[1], ws.data_ptr(), p[0], s) == 0
+    assert lib.nvfp4_gated_ffn_backward(xp, t, h, p[1], w13p, w2p, i, dyp, ws.data_ptr(), p[2], p[3], p[4], s) == 0
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, (y, kept, *want)):
+        assert torch.equal(got[:ref.numel()], ref.flatten()) and torch.all(got[ref.numel():] == 3.0)
+    assert torch.all(ws[size:] == 0xFF)
+    for keep in range(3):                                # each gradient alone
+        alone = [torch.full_like(o, 3.0) for o in outs[2:]]
+        a = [o.data_ptr() if j == keep else None for j, o in enumerate(alone)]
+        assert lib.nvfp4_gated_ffn_backward(xp, t, h, p[1], w13p, w2p, i, dyp, ws.data_ptr(), *a, s) == 0
+        torch.cuda.synchronize()
+        for j, o in enumerate(alone):
+            assert torch.equal(o, outs[2 + j]) if j == keep else torch.all(o == 3.0)
+
+
+@pytest.mark.parametrize("t", [1, 16, 100, 300])
+def test_graph_replays(t):
+    h, i = 272, 528
+    x, w13, w2, dy = (v.to(DEV) for v in make(t, h, i, seed=7))
+    ws = B.gated_ffn_workspace(t, h, i, DEV)
+    held = []
+
+    def call():
+        y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True, workspace=ws)
+        return (y, kept, *B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy, workspace=ws))
+    graph = capture(lambda: held.append(call()))
+    rng = np.random.default_rng(t)
+    for _ in range(3):
+        x.copy_(bf16(rng, t, h))
+        dy.copy_(bf16(rng, t, h))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in held[-1]]
+        for a, b in zip(got, call()):
+            assert torch.equal(a, b)
+
+
+def test_given_stream_with_wide_input():
+    x, w13, w2, dy = (v.to(DEV) for v in make(20, 144, 272, seed=8))
+    y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    want = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy)
+    wide = lambda v: torch.stack([v, v], -1)[..., 0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y2, h2 = B.nvfp4_gated_ffn(wide(x), wide(w13), wide(w2), keep_h=True, stream=side)
+    g2 = B.nvfp4_gated_ffn_backward(wide(x), h2, wide(w13), wide(w2), wide(dy), stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((y, kept, *want), (y2, h2, *g2)))
+
+
+def test_empty_batch_and_refusals():
+    x, w13, w2, dy = (v.to(DEV) for v in make(4, 32, 48, seed=9))
+    y, kept = B.nvfp4_gated_ffn(x[:0], w13, w2, keep_h=True)
+    assert y.shape == (0, 32) and kept.shape == (0, 144)
+    dx, d13, d2 = B.nvfp4_gated_ffn_backward(x[:0], kept, w13, w2, dy[:0])
+    assert dx.shape == (0, 32) and not d13.any() and not d2.any()
+    y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    for bad in ((x, w13[:95], w2), (x, w13, w2[:31]), (x[:, :16].contiguous(), w13, w2)):
+        with pytest.raises(ValueError):
+            B.nvfp4_gated_ffn(*bad)
+    with pytest.raises(ValueError):
+        B.nvfp4_gated_ffn_backward(x, kept[:, :96].contiguous(), w13, w2, dy)
+    with pytest.raises(ValueError):
+        B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy[:3])
+    with pytest.raises(ValueError):
+        B.nvfp4_gated_ffn(x, w13, w2, workspace=torch.empty((16,), dtype=torch.uint8, device=DEV))
