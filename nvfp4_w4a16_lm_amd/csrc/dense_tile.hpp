@@ -80,6 +80,17 @@ constexpr int tile_wait(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x0070;
 constexpr int kTileThreads = 256;
 constexpr uint32_t kTileNowhere = 0xF0000000u;   // a buffer offset past every operand: reads as zero
 
+// Unit ring: the MFMA slot, counted from the barrier, after which copy c of a period is issued
+#ifndef TILE_SLOTS
+#define TILE_SLOTS {1, 5, 9, 13, 17, 21, 25, 29, 33, 37, 41, 45, 49, 53, 57, 61}
+#endif
+constexpr int kTileUnitSlot[16] = TILE_SLOTS;
+constexpr int tile_unit_early(int slots) {
+  int n = 0;
+  for (int at : kTileUnitSlot) n += at < slots;
+  return n;
+}
+
 typedef __attribute__((address_space(3))) void* tile_lds_t;
 typedef __attribute__((address_space(3))) s16x4* tile_tr_t;
 
@@ -116,14 +127,24 @@ struct TileCfg {
   static constexpr int BN = 32 * IT * WN, BM = 32 * JT * WM;
   static constexpr int KE = I8 ? 128 : 64;                      // elements of k per step
   static constexpr int kPBytes = BN * 128, kQBytes = BM * 128;
+  // R = 0: five units of half a step (P, Q, P, Q, P ...); else R whole steps
+  static constexpr bool kUnits = R == 0;
   static constexpr int kBuf = kPBytes + kQBytes;
+  static constexpr int kRing = kUnits ? 5 : R;                  // steps until a buffer returns to its place
   static constexpr int kCopies = kBuf / 4096;                   // copies per wavefront per step
+  static constexpr int kRingBytes = kUnits ? 5 * kPBytes : R * kBuf;
+  static constexpr int p_at(int ph) { return kUnits ? 2 * ph % 5 * kPBytes : ph * kBuf; }
+  static constexpr int q_at(int ph) { return kUnits ? (2 * ph + 1) % 5 * kPBytes : ph * kBuf + kPBytes; }
+  // epilogue: rows in float32, 32 of each wavefront at a time, or bf16 outputs, all of them (gated: h beside them, half)
+  static constexpr bool kStageF32 = EPI == kTileF32 || EPI == kTileGatedBack;
   static constexpr int kStageRows = 32 * WM, kStagePitch = BN + 4;
-  static constexpr int kStage = kStageRows * kStagePitch * 4;
-  static constexpr int kLds = R * kBuf > kStage ? R * kBuf : kStage;
+  static constexpr int kStageJ = EPI == kTileGated && JT > 1 ? JT / 2 : JT;
+  static constexpr int kOutPitch = (EPI == kTileGated ? BN / 2 * 3 : BN) + 8;
+  static constexpr int kStage = kStageF32 ? kStageRows * kStagePitch * 4 : 32 * kStageJ * WM * kOutPitch * 2;
+  static constexpr int kLds = kRingBytes > kStage ? kRingBytes : kStage;
   static_assert(WN * WM == 4 && kLds <= 160 * 1024, "tile");
   static_assert(!I8 || (!PT && !QT), "int8 operands are straight");
-  static_assert((R - 1) * kCopies < 64, "copies in flight");
+  static_assert(kUnits ? BN == BM : R >= 2 && R <= 4 && (R - 1) * kCopies < 64, "ring");
 };
 
 template <class C>
@@ -198,11 +219,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
 
   // copy c of step st into ring buffer ph (steps past the last: nothing is read, zeros arrive)
   auto copy_one = [&](int st, int ph, int c) __attribute__((always_inline)) {
-    uint8_t* const buf = lds + ph * C::kBuf;
     const bool live = st < nsteps;
     const int k0 = k_begin + st * C::KE;
     if (c < kPC) {
-      uint8_t* const dst = buf + (4 * c + wave) * 1024;
+      uint8_t* const dst = lds + C::p_at(ph) + (4 * c + wave) * 1024;
       if constexpr (!PT) {
         const __amdgpu_buffer_rsrc_t rs =
             __builtin_amdgcn_make_buffer_rsrc((void*)p_base, (short)0, live ? (int)p_range : 0, 0x00020000);
@@ -216,7 +236,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
       }
     } else {
       const int d = c - kPC;
-      uint8_t* const dst = buf + C::kPBytes + (4 * d + wave) * 1024;
+      uint8_t* const dst = lds + C::q_at(ph) + (4 * d + wave) * 1024;
       if constexpr (!QT) {
         const __amdgpu_buffer_rsrc_t rs =
             __builtin_amdgcn_make_buffer_rsrc((void*)q_base, (short)0, live ? (int)q_range : 0, 0x00020000);
@@ -247,19 +267,19 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
   };
   u32x4 pf[2][IT], qf[2][JT];
   auto read_one = [&](int ph, int u, int x, u32x4 (&pn)[IT], u32x4 (&qn)[JT]) __attribute__((always_inline)) {
-    const uint8_t* const buf = lds + ph * C::kBuf;
+    const uint8_t* const pb = lds + C::p_at(ph);
     constexpr int np = IT * (PT ? 2 : 1);
     if (x < np) {
       if constexpr (!PT) {
-        pn[x] = frag_straight(buf, 32 * IT * wn + 32 * x, u);
+        pn[x] = frag_straight(pb, 32 * IT * wn + 32 * x, u);
       } else {
-        const uint2 v = frag_tr(buf, kPPr, IT * wn + x / 2, u, x % 2);
+        const uint2 v = frag_tr(pb, kPPr, IT * wn + x / 2, u, x % 2);
         pn[x / 2][2 * (x % 2)] = v.x;
         pn[x / 2][2 * (x % 2) + 1] = v.y;
       }
     } else {
       const int y = x - np;
-      const uint8_t* const qb = buf + C::kPBytes;
+      const uint8_t* const qb = lds + C::q_at(ph);
       if constexpr (!QT) {
         qn[y] = frag_straight(qb, 32 * JT * wm + 32 * y, u);
       } else {
@@ -287,12 +307,34 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
                                                      0, 0, 0);
   };
 
+  // Copies of sub-step u of step st (ring place ph), the s-th of kMf slots.  Whole steps: all of step st + R in
+  // sub-step 3.  Units: between two barriers Q of the step after next, then P of the step behind it.
+  auto copy_slot = [&](int st, auto PH, int u, int s) __attribute__((always_inline)) {
+    constexpr int ph = decltype(PH)::value;
+    if constexpr (!C::kUnits) {
+      if (u == 3) {
+#pragma unroll
+        for (int c = 0; c < C::kCopies; ++c)
+          if (c * kMf / C::kCopies == s) copy_one(st + R, ph, c);
+      }
+    } else {
+      constexpr int half = C::kCopies / 2;                      // copies of a unit
+#pragma unroll
+      for (int c = 0; c < C::kCopies; ++c) {
+        const int at = kTileUnitSlot[c];                        // slot of the 4 kMf from sub-step 3 on
+        if (((u + 1) & 3) * kMf + s != at) continue;
+        const int ahead = u == 3 ? 1 : 0;                       // the period belongs to the step of its barrier
+        if (c < half) copy_one(st + ahead + 1, (ph + ahead + 1) % 5, half + c);
+        else copy_one(st + ahead + 2, (ph + ahead + 2) % 5, c - half);
+      }
+    }
+  };
   auto kstep = [&](int st, auto PH) __attribute__((always_inline)) {
-    constexpr int ph = decltype(PH)::value, ph1 = (ph + 1) % R;
+    constexpr int ph = decltype(PH)::value, ph1 = (ph + 1) % C::kRing;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (u == 3) {
-        __builtin_amdgcn_s_waitcnt(tile_wait((R - 2) * C::kCopies));
+        __builtin_amdgcn_s_waitcnt(tile_wait(C::kUnits ? C::kCopies / 2 : (R - 2) * C::kCopies));
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -304,36 +346,45 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
 #pragma unroll
         for (int x = 0; x < kReads; ++x)
           if (x * kMf / kReads == s) read_one(u < 3 ? ph : ph1, (u + 1) & 3, x, pf[(u + 1) & 1], qf[(u + 1) & 1]);
-        if (u == 3) {
-#pragma unroll
-          for (int c = 0; c < C::kCopies; ++c)
-            if (c * kMf / C::kCopies == s) copy_one(st + R, ph, c);
-        }
+        copy_slot(st, PH, u, s);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
 
+  if constexpr (!C::kUnits) {
 #pragma unroll
-  for (int x = 0; x < R * C::kCopies; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
-  __builtin_amdgcn_s_waitcnt(tile_wait((R - 1) * C::kCopies));
+    for (int x = 0; x < R * C::kCopies; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
+    __builtin_amdgcn_s_waitcnt(tile_wait((R - 1) * C::kCopies));
+  } else {
+    constexpr int half = C::kCopies / 2;
+#pragma unroll
+    for (int x = 0; x < 3 * half; ++x) copy_one(x / (2 * half), x / (2 * half), x % (2 * half));
+    constexpr int early = tile_unit_early(kMf);                 // Q of step 1: what sub-step 3 would have copied
+#pragma unroll
+    for (int x = 0; x < early; ++x) copy_one(1, 1, half + x);
+    __builtin_amdgcn_s_waitcnt(tile_wait(half + early));
+  }
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int x = 0; x < kReads; ++x) read_one(0, 0, x, pf[0], qf[0]);
 
   int st = 0;
-  for (; st + R <= nsteps; st += R) {
-    kstep(st, std::integral_constant<int, 0>{});
-    kstep(st + 1, std::integral_constant<int, 1 % R>{});
-    if constexpr (R > 2) kstep(st + 2, std::integral_constant<int, 2 % R>{});
-    if constexpr (R > 3) kstep(st + 3, std::integral_constant<int, 3 % R>{});
+  using std::integral_constant;
+  for (; st + C::kRing <= nsteps; st += C::kRing) {
+    kstep(st, integral_constant<int, 0>{});
+    kstep(st + 1, integral_constant<int, 1>{});
+    if constexpr (C::kRing > 2) kstep(st + 2, integral_constant<int, 2>{});
+    if constexpr (C::kRing > 3) kstep(st + 3, integral_constant<int, 3>{});
+    if constexpr (C::kRing > 4) kstep(st + 4, integral_constant<int, 4>{});
   }
-  static_assert(R >= 2 && R <= 4, "ring");
-  if (st < nsteps) kstep(st, std::integral_constant<int, 0>{});
-  if constexpr (R > 2)
-    if (st + 1 < nsteps) kstep(st + 1, std::integral_constant<int, 1 % R>{});
-  if constexpr (R > 3)
-    if (st + 2 < nsteps) kstep(st + 2, std::integral_constant<int, 2 % R>{});
+  if (st < nsteps) kstep(st, integral_constant<int, 0>{});
+  if constexpr (C::kRing > 2)
+    if (st + 1 < nsteps) kstep(st + 1, integral_constant<int, 1>{});
+  if constexpr (C::kRing > 3)
+    if (st + 2 < nsteps) kstep(st + 2, integral_constant<int, 2>{});
+  if constexpr (C::kRing > 4)
+    if (st + 3 < nsteps) kstep(st + 3, integral_constant<int, 3>{});
   __builtin_amdgcn_s_waitcnt(tile_wait(0));
   __syncthreads();
 
@@ -394,13 +445,36 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
       a.parts[(int64_t)(m0 + ml) * a.part_pitch + nt] = make_float2(mm, s);
     }
     return;
-  } else {
-    // 32 rows of each wavefront row at a time through LDS, so that memory is written in whole lines
+  } else if constexpr (C::kStageF32) {
+    // 32 rows of each wavefront row at a time through LDS in float32, so that memory is read and written in
+    // whole lines; a pass's reads are under way before its rows are in place.
     float* const stage = reinterpret_cast<float*>(lds);
-    constexpr int kW = C::EPI == kTileGated ? BN / 2 : BN;       // columns written
-    constexpr int kChunks = kW / 8;
+    constexpr int kChunks = BN / 8, kIters = C::kStageRows * kChunks / kTileThreads;
+    const int c = tid % kChunks, n = n0 + 8 * c;
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
+      u32x4 in[kIters][2];
+      int64_t at[kIters];
+      bool on[kIters];
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int row = tid / kChunks + it * (kTileThreads / kChunks);
+        const int m = m0 + 32 * (JT * (row >> 5) + j) + (row & 31);
+        on[it] = m < M && n < a.N;
+        if constexpr (C::EPI == kTileF32) {
+          at[it] = ((int64_t)split * a.M + m) * a.out_pitch + n;
+          if (on[it] && a.accumulate) {
+            in[it][0] = *reinterpret_cast<const u32x4*>((const float*)a.out + at[it]);
+            in[it][1] = *reinterpret_cast<const u32x4*>((const float*)a.out + at[it] + 4);
+          }
+        } else {
+          at[it] = m;
+          if (on[it]) {
+            in[it][0] = *reinterpret_cast<const u32x4*>(a.h + (int64_t)m * 3 * a.I + n);
+            in[it][1] = *reinterpret_cast<const u32x4*>(a.h + (int64_t)m * 3 * a.I + a.I + n);
+          }
+        }
+      }
       if (j > 0) __syncthreads();
 #pragma unroll
       for (int i = 0; i < IT; ++i)
@@ -408,89 +482,156 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
         for (int q = 0; q < 4; ++q) {
           f32x4 v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][4 * q + e];
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
           *reinterpret_cast<f32x4*>(stage + (32 * wm + r) * C::kStagePitch + 32 * (IT * wn + i) + 8 * q + 4 * h) = v;
         }
       __syncthreads();
-      for (int x = tid; x < C::kStageRows * kChunks; x += kTileThreads) {
-        const int row = x / kChunks, c = x % kChunks;
-        const int m = m0 + 32 * (JT * (row >> 5) + j) + (row & 31);
-        const int n = n0 + 8 * c;
-        if (m >= M || n >= (C::EPI == kTileGated ? a.I : a.N)) continue;
-        const float* const src = stage + row * C::kStagePitch;
-        float v[8];
-        if constexpr (C::EPI == kTileGated) {
-          constexpr int half = 16 * IT;
-          const int at = 2 * half * (8 * c / half) + 8 * c % half;
-          float u[8], o[8];
+#pragma unroll
+      for (int it = 0; it < kIters; ++it) {
+        const int row = tid / kChunks + it * (kTileThreads / kChunks);
+        const f32x4* const src = reinterpret_cast<const f32x4*>(stage + row * C::kStagePitch + 8 * c);
+        f32x4 lo = src[0], hi = src[1];
+        if (!on[it]) continue;
+        if constexpr (C::EPI == kTileF32) {
+          if (a.accumulate) {
+            lo += __builtin_bit_cast(f32x4, in[it][0]);
+            hi += __builtin_bit_cast(f32x4, in[it][1]);
+          }
+          *reinterpret_cast<f32x4*>((float*)a.out + at[it]) = lo;
+          *reinterpret_cast<f32x4*>((float*)a.out + at[it] + 4) = hi;
+        } else {
+          float g[8], u[8], dg[8], du[8];
+          unpack8(in[it][0], g);
+          unpack8(in[it][1], u);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            v[e] = src[at + e];
-            u[e] = src[at + half + e];
-            o[e] = v[e] * sigmoid_fast(v[e]) * u[e];
+            const float v = e < 4 ? lo[e & 3] : hi[e & 3];
+            const float s = sigmoid_fast(g[e]), gs = g[e] * s;
+            du[e] = v * gs;
+            dg[e] = v * u[e] * (s + gs * (1.0f - s));
           }
-          *reinterpret_cast<u32x4*>((uint16_t*)a.out + (int64_t)m * a.out_pitch + n) = pack8(o);
-          if (a.h != nullptr) {
-            *reinterpret_cast<u32x4*>(a.h + (int64_t)m * 3 * a.I + n) = pack8(v);
-            *reinterpret_cast<u32x4*>(a.h + (int64_t)m * 3 * a.I + a.I + n) = pack8(u);
+          *reinterpret_cast<u32x4*>(a.dh + at[it] * 2 * a.I + n) = pack8(dg);
+          *reinterpret_cast<u32x4*>(a.dh + at[it] * 2 * a.I + a.I + n) = pack8(du);
+        }
+      }
+    }
+  } else {
+    // Outputs are made in registers, rounded, and gathered in LDS so that memory is written in whole lines.
+    constexpr int kW = C::EPI == kTileGated ? BN / 2 : BN;       // columns written
+    constexpr int kJP = C::kStageJ;                              // column tiles of a wavefront per pass
+    uint16_t* const stage = reinterpret_cast<uint16_t*>(lds);
+    float cs[C::I8 ? IT : 1][4][4], cb[C::I8 || C::EPI == kTileCeGrad ? IT : 1][4][4];
+    const bool has_bias = (C::I8 || C::EPI == kTileCeGrad) && a.bias != nullptr;
+    if constexpr (C::I8 || C::EPI == kTileCeGrad) {
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + 32 * (IT * wn + i) + 8 * q + 4 * h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int ne = min(n + e, a.N - 1);
+            if constexpr (C::I8) cs[i][q][e] = a.sw[ne];
+            cb[i][q][e] = has_bias ? __uint_as_float((uint32_t)a.bias[ne] << 16) : 0.0f;
           }
+        }
+    }
+#pragma unroll
+    for (int j0 = 0; j0 < JT; j0 += kJP) {
+      if (j0 > 0) __syncthreads();
+#pragma unroll
+      for (int jj = 0; jj < kJP; ++jj) {
+        const int j = j0 + jj, m = m0 + 32 * (JT * wm + j) + r;
+        uint16_t* const to = stage + (32 * (kJP * wm + jj) + r) * C::kOutPitch;
+        if constexpr (C::EPI == kTileGated) {
+#pragma unroll
+          for (int i = 0; i < IT / 2; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int at = 32 * (IT / 2 * wn + i) + 8 * q + 4 * h;
+              float g[4], u[4], o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                g[e] = acc[i][j][4 * q + e];
+                u[e] = acc[i + IT / 2][j][4 * q + e];
+                o[e] = g[e] * sigmoid_fast(g[e]) * u[e];
+              }
+              *reinterpret_cast<uint2*>(to + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+              if (a.h != nullptr) {
+                *reinterpret_cast<uint2*>(to + kW + at) = make_uint2(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]));
+                *reinterpret_cast<uint2*>(to + 2 * kW + at) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+              }
+            }
+        } else {
+          float sx = 1.0f, top = 0.0f, scale = 0.0f, minus = 0.0f;
+          int tok = -1;
+          if constexpr (C::I8) sx = a.sx[min(m, M - 1)];
+          if constexpr (C::EPI == kTileCeGrad) {
+            const int mc = min(m, M - 1);
+            const float2 st2 = a.stats[mc], cf = a.coef[mc];
+            top = st2.x;
+            scale = cf.x / st2.y;
+            minus = cf.y;
+            tok = a.tok[mc] - a.n_first - n0 - 32 * IT * wn - 4 * h;
+          }
+#pragma unroll
+          for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                v[e] = (float)acc[i][j][4 * q + e];
+                if constexpr (C::I8) {
+                  v[e] *= sx * cs[i][q][e];
+                  if (has_bias) v[e] += cb[i][q][e];
+                }
+                if constexpr (C::EPI == kTileCeGrad) {
+                  if (has_bias) v[e] += cb[i][q][e];
+                  // a logit of -inf: exp gives 0 for the others' maximum, and no 1[j = t] either
+                  const float p = v[e] == -INFINITY ? 0.0f : exp_fast(v[e] - top) * scale;
+                  const bool target = tok == 32 * i + 8 * q + e && v[e] != -INFINITY;
+                  v[e] = p - (target ? minus : 0.0f);
+                }
+              }
+              *reinterpret_cast<uint2*>(to + 32 * (IT * wn + i) + 8 * q + 4 * h) =
+                  make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            }
+        }
+      }
+      __syncthreads();
+      constexpr int kChunks = kW / 8, kRows = 32 * kJP * C::WM, kIters = kRows * kChunks / kTileThreads;
+      const int c = tid % kChunks, n = n0 + 8 * c, width = C::EPI == kTileGated ? a.I : a.N;
+      if (n >= width) continue;
+      const bool whole = !C::I8 || ((a.N & 7) == 0 && n + 8 <= a.N);
+#pragma unroll 8
+      for (int it = 0; it < kIters; ++it) {
+        const int row = tid / kChunks + it * (kTileThreads / kChunks);
+        const int m = m0 + 32 * (JT * (row / (32 * kJP)) + j0) + row % (32 * kJP);
+        if (m >= M) continue;
+        const u32x4* const src = reinterpret_cast<const u32x4*>(stage + row * C::kOutPitch + 8 * c);
+        uint16_t* const o = (uint16_t*)a.out + (int64_t)m * a.out_pitch + n;
+        u32x4 w = src[0];
+        if constexpr (C::EPI == kTileCeGrad) {                   // columns past the vocabulary: zero operands
+          if (n + 8 > a.N) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = n + 2 * e + 1 < a.N ? w[e] : n + 2 * e < a.N ? w[e] & 0xFFFFu : 0u;
+          }
+        }
+        if (whole) {
+          if constexpr (C::I8) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));
+          else *reinterpret_cast<u32x4*>(o) = w;
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = src[8 * c + e];
-          if constexpr (C::EPI == kTileBf16) {
-            *reinterpret_cast<u32x4*>((uint16_t*)a.out + (int64_t)m * a.out_pitch + n) = pack8(v);
-          } else if constexpr (C::EPI == kTileF32) {
-            float* const o = (float*)a.out + ((int64_t)split * a.M + m) * a.out_pitch + n;
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              f32x4 w = {v[e], v[e + 1], v[e + 2], v[e + 3]};
-              if (a.accumulate) w += *reinterpret_cast<const f32x4*>(o + e);
-              *reinterpret_cast<f32x4*>(o + e) = w;
-            }
-          } else if constexpr (C::EPI == kTileInt8) {
-            const float sx = a.sx[m];
-            uint16_t* const o = (uint16_t*)a.out + (int64_t)m * a.out_pitch + n;
-            const bool whole = n + 8 <= a.N;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int ne = whole ? n + e : min(n + e, a.N - 1);
-              v[e] *= sx * a.sw[ne];
-              if (a.bias != nullptr) v[e] += __uint_as_float((uint32_t)a.bias[ne] << 16);
-            }
-            const u32x4 w = pack8(v);
-            if (whole && (a.N & 7) == 0) {
-              __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < a.N) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-            }
-          } else if constexpr (C::EPI == kTileGatedBack) {
-            const uint16_t* const hp = a.h + (int64_t)m * 3 * a.I + n;
-            float g[8], u[8], dg[8], du[8];
-            unpack8(*reinterpret_cast<const u32x4*>(hp), g);
-            unpack8(*reinterpret_cast<const u32x4*>(hp + a.I), u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float s = sigmoid_fast(g[e]), gs = g[e] * s;
-              du[e] = v[e] * gs;
-              dg[e] = v[e] * u[e] * (s + gs * (1.0f - s));
-            }
-            *reinterpret_cast<u32x4*>(a.dh + (int64_t)m * 2 * a.I + n) = pack8(dg);
-            *reinterpret_cast<u32x4*>(a.dh + (int64_t)m * 2 * a.I + a.I + n) = pack8(du);
-          } else {                                                // kTileCeGrad
-            const float2 st2 = a.stats[m], cf = a.coef[m];
-            const float scale = cf.x / st2.y;
-            const int tok = a.tok[m] - a.n_first;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float z = v[e];
-              if (a.bias != nullptr && n + e < a.N) z += __uint_as_float((uint32_t)a.bias[n + e] << 16);
-              float d = exp_fast(z - st2.x) * scale;
-              if (n + e == tok) d -= cf.y;
-              v[e] = (n + e >= a.N || z == -INFINITY) ? 0.0f : d;
-            }
-            *reinterpret_cast<u32x4*>((uint16_t*)a.out + (int64_t)m * a.out_pitch + n) = pack8(v);
+          for (int e = 0; e < 8; ++e)
+            if (n + e < a.N) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+        if constexpr (C::EPI == kTileGated) {
+          if (a.h != nullptr) {
+            uint16_t* const hp = a.h + (int64_t)m * 3 * a.I + n;
+            *reinterpret_cast<u32x4*>(hp) = src[kChunks];
+            *reinterpret_cast<u32x4*>(hp + a.I) = src[2 * kChunks];
           }
         }
       }
@@ -521,7 +662,7 @@ inline hipError_t launch_tile(const TileArgs& a, hipStream_t stream) {
       case 128: return launch_tile_cfg<TileCfg<2, 4, 4, 1, PT, QT, EPI, 3>>(a, stream);
     }
   }
-  return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 2>>(a, stream);
+  return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 0>>(a, stream);
 }
 
 }  // namespace nvfp4
