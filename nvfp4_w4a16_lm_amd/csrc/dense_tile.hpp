@@ -60,6 +60,7 @@ struct TileArgs {
   void* out;
   int64_t out_pitch;         // elements
   int32_t accumulate;
+  int32_t turn_by_tile;      // the launcher's: where a workgroup starts in K
   // epilogues
   const float* sx;
   const float* sw;
@@ -79,17 +80,6 @@ struct TileArgs {
 constexpr int tile_wait(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x0070; }
 constexpr int kTileThreads = 256;
 constexpr uint32_t kTileNowhere = 0xF0000000u;   // a buffer offset past every operand: reads as zero
-
-// Unit ring: the MFMA slot, counted from the barrier, after which copy c of a period is issued
-#ifndef TILE_SLOTS
-#define TILE_SLOTS {1, 5, 9, 13, 17, 21, 25, 29, 33, 37, 41, 45, 49, 53, 57, 61}
-#endif
-constexpr int kTileUnitSlot[16] = TILE_SLOTS;
-constexpr int tile_unit_early(int slots) {
-  int n = 0;
-  for (int at : kTileUnitSlot) n += at < slots;
-  return n;
-}
 
 typedef __attribute__((address_space(3))) void* tile_lds_t;
 typedef __attribute__((address_space(3))) s16x4* tile_tr_t;
@@ -132,6 +122,7 @@ struct TileCfg {
   static constexpr int kBuf = kPBytes + kQBytes;
   static constexpr int kRing = kUnits ? 5 : R;                  // steps until a buffer returns to its place
   static constexpr int kCopies = kBuf / 4096;                   // copies per wavefront per step
+  static constexpr int copy_slot(int c) { return (8 * c + 1) * 2 * IT * JT / (4 * kCopies); }   // even spacing
   static constexpr int kRingBytes = kUnits ? 5 * kPBytes : R * kBuf;
   static constexpr int p_at(int ph) { return kUnits ? 2 * ph % 5 * kPBytes : ph * kBuf; }
   static constexpr int q_at(int ph) { return kUnits ? (2 * ph + 1) % 5 * kPBytes : ph * kBuf + kPBytes; }
@@ -142,13 +133,14 @@ struct TileCfg {
   static constexpr int kOutPitch = (EPI == kTileGated ? BN / 2 * 3 : BN) + 8;
   static constexpr int kStage = kStageF32 ? kStageRows * kStagePitch * 4 : 32 * kStageJ * WM * kOutPitch * 2;
   static constexpr int kLds = kRingBytes > kStage ? kRingBytes : kStage;
+  static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;      // workgroups meant to share a compute unit
   static_assert(WN * WM == 4 && kLds <= 160 * 1024, "tile");
   static_assert(!I8 || (!PT && !QT), "int8 operands are straight");
-  static_assert(kUnits ? BN == BM : R >= 2 && R <= 4 && (R - 1) * kCopies < 64, "ring");
+  static_assert(kUnits ? BN == BM : R >= 2 && R <= 4 && R * kCopies < 64, "ring");
 };
 
 template <class C>
-__global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a) {
+__global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(TileArgs a) {
   constexpr int IT = C::IT, JT = C::JT, R = C::R, BN = C::BN, BM = C::BM;
   constexpr bool PT = C::PT, QT = C::QT;
   constexpr int kPC = BN / 32;                                  // copies of the n side
@@ -177,6 +169,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
   const int k_begin = split * a.k_split, k_end = min(K, k_begin + a.k_split);
   const int nsteps = k_end > k_begin ? (k_end - k_begin + C::KE - 1) / C::KE : 0;
 
+  // Straight rows a power of two apart put one step of every row on few memory channels, and workgroups that start
+  // together would all be at that step: they start at different ones (one token, 128256 x 4096 int8: 110 -> 94 us).
+  // Rows of k are read whole by neighbouring tiles, which should stay together (dx of 4096 x 28672 x 4096: 700 -> 820 us).
+  const int turn = PT || nsteps == 0 ? 0 : a.turn_by_tile ? nt % nsteps : (xcd * nsteps) >> 3;
+
   // Straight copies: instruction c of wavefront w fills rows 8 (4 c + w) .. + 7, lane l slot l & 7 of row
   // 8 (4 c + w) + (l >> 3), i.e. piece (l & 7) ^ (l >> 3) ^ (w & 1).  Transposed: with W columns a
   // row has W / 8 pieces; lane l fills slot l % (W / 8) of row l / (W / 8) of the instruction's.
@@ -185,7 +182,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
   const uint8_t* q_base;
   uint32_t p_range = 0, q_range = 0, p_off, q_off;
   constexpr int kPPr = BN / 8, kQPr = BM / 8;                   // pieces of a transposed row
-  auto tr_swizzle = [](int row, int pieces) { return pieces >= 8 ? 2 * (row & 3) : 0; };
+  auto tr_swizzle = [](int row, int pieces) { return pieces >= 16 ? 4 * (row & 3) : 0; };
   if (!PT) {
     p_base = a.p + (int64_t)n0 * a.p_pitch;
     p_range = (uint32_t)min((int64_t)0xE0000000u, (a.p_rows - n0) * a.p_pitch);
@@ -220,52 +217,44 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
   // copy c of step st into ring buffer ph (steps past the last: nothing is read, zeros arrive)
   auto copy_one = [&](int st, int ph, int c) __attribute__((always_inline)) {
     const bool live = st < nsteps;
-    const int k0 = k_begin + st * C::KE;
-    if (c < kPC) {
-      uint8_t* const dst = lds + C::p_at(ph) + (4 * c + wave) * 1024;
-      if constexpr (!PT) {
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc((void*)p_base, (short)0, live ? (int)p_range : 0, 0x00020000);
-        const uint32_t off = p_off + (uint32_t)(p_row(c) * a.p_pitch);
-        tile_copy16(rs, (tile_lds_t)dst, k0 + piece_k < K ? off : kTileNowhere, live ? k0 * (128 / C::KE) : 0);
-      } else {
-        const int64_t left = live ? (int64_t)(K - k0) * a.p_pitch - 2 * (int64_t)n0 : 0;
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(p_base + (int64_t)k0 * a.p_pitch), (short)0, (int)min(left, (int64_t)0x7FFFFFFF), 0x00020000);
-        tile_copy16(rs, (tile_lds_t)dst, p_off + (uint32_t)(c * 4 * (64 / kPPr) * a.p_pitch), 0);
-      }
+    const int turned = st + turn;
+    const int k0 = k_begin + (turned < nsteps ? turned : turned - nsteps) * C::KE;
+    const bool left = c < kPC;
+    const int i = left ? c : c - kPC;
+    uint8_t* const dst = lds + (left ? C::p_at(ph) : C::q_at(ph)) + (4 * i + wave) * 1024;
+    const int64_t pitch = left ? a.p_pitch : a.q_pitch;
+    if (left ? !PT : !QT) {
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(left ? p_base : q_base), (short)0, live ? (int)(left ? p_range : q_range) : 0, 0x00020000);
+      const uint32_t off = (left ? p_off : q_off) + (uint32_t)((left ? p_row(i) : 32 * i) * pitch);
+      tile_copy16(rs, (tile_lds_t)dst, k0 + piece_k < K ? off : kTileNowhere, live ? k0 * (128 / C::KE) : 0);
     } else {
-      const int d = c - kPC;
-      uint8_t* const dst = lds + C::q_at(ph) + (4 * d + wave) * 1024;
-      if constexpr (!QT) {
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc((void*)q_base, (short)0, live ? (int)q_range : 0, 0x00020000);
-        const uint32_t off = q_off + (uint32_t)(32 * d * a.q_pitch);
-        tile_copy16(rs, (tile_lds_t)dst, k0 + piece_k < K ? off : kTileNowhere, live ? k0 * (128 / C::KE) : 0);
-      } else {
-        const int64_t left = live ? (int64_t)(K - k0) * a.q_pitch - 2 * (int64_t)m0 : 0;
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(q_base + (int64_t)k0 * a.q_pitch), (short)0, (int)min(left, (int64_t)0x7FFFFFFF), 0x00020000);
-        tile_copy16(rs, (tile_lds_t)dst, q_off + (uint32_t)(d * 4 * (64 / kQPr) * a.q_pitch), 0);
-      }
+      const int rows = live ? min(K - k0, 64) : 0;               // no branch: the loop stays one block
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc((void*)((left ? p_base : q_base) + k0 * pitch), (short)0,
+                                            max(rows * (int)pitch - 2 * (left ? n0 : m0), 0), 0x00020000);
+      tile_copy16(rs, (tile_lds_t)dst, (left ? p_off : q_off) + (uint32_t)(i * (256 / (left ? kPPr : kQPr)) * pitch), 0);
     }
   };
 
   // Fragment reads.  Straight: row 32 i + r of the wavefront's, piece 4 h + u.  Transposed: lane l of a
   // group of 16 names row k = l / 4 and columns 4 (l % 4) .. + 3 and receives column l's four k.
   const int sw = (r & 7) ^ ((r >> 3) & 1);
-  const int l16 = lane & 15, grp = (lane >> 4) & 1;
-  const int tr_low = 2 * grp + ((l16 & 3) >> 1);
+  const int l16 = lane & 15, k4 = l16 >> 2;
+  auto tr_lane = [&](int pieces, int tile0) __attribute__((always_inline)) {   // XORed with 64 i for 32-column tile i
+    return (uint32_t)((32 * h + k4) * pieces * 16 + 64 * (tile0 ^ (pieces >= 16 ? k4 : 0)) + 32 * ((lane >> 4) & 1) +
+                      8 * (l16 & 3));
+  };
+  uint32_t tr_p = PT ? tr_lane(kPPr, IT * wn) : 0, tr_q = QT ? tr_lane(kQPr, JT * wm) : 0;
   auto frag_straight = [&](const uint8_t* base, int row0, int u) __attribute__((always_inline)) {
     return *reinterpret_cast<const u32x4*>(base + (row0 + r) * 128 + 16 * ((4 * h + u) ^ sw));
   };
-  auto frag_tr = [&](const uint8_t* base, int pieces, int tile32, int u, int e) __attribute__((always_inline)) {
-    const int row = 32 * h + 8 * u + 4 * e + (l16 >> 2);
-    const int slot = (4 * tile32 + tr_low) ^ tr_swizzle(l16 >> 2, pieces);
-    const uint8_t* const at = base + row * pieces * 16 + 16 * slot + 8 * (l16 & 1);
-    return __builtin_bit_cast(uint2, tile_read_tr((tile_tr_t)at));
+  auto frag_tr = [&](const uint8_t* base, uint32_t at, int pieces, int i, int u, int e) __attribute__((always_inline)) {
+    return __builtin_bit_cast(uint2, tile_read_tr((tile_tr_t)(base + (at ^ (64 * i)) + (8 * u + 4 * e) * pieces * 16)));
   };
-  u32x4 pf[2][IT], qf[2][JT];
+  // fragments: two sub-steps' (units), or two steps'
+  constexpr int kSets = C::kUnits ? 2 : 8;
+  u32x4 pf[kSets][IT], qf[kSets][JT];
   auto read_one = [&](int ph, int u, int x, u32x4 (&pn)[IT], u32x4 (&qn)[JT]) __attribute__((always_inline)) {
     const uint8_t* const pb = lds + C::p_at(ph);
     constexpr int np = IT * (PT ? 2 : 1);
@@ -273,7 +262,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
       if constexpr (!PT) {
         pn[x] = frag_straight(pb, 32 * IT * wn + 32 * x, u);
       } else {
-        const uint2 v = frag_tr(pb, kPPr, IT * wn + x / 2, u, x % 2);
+        const uint2 v = frag_tr(pb, tr_p, kPPr, x / 2, u, x % 2);
         pn[x / 2][2 * (x % 2)] = v.x;
         pn[x / 2][2 * (x % 2) + 1] = v.y;
       }
@@ -283,7 +272,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
       if constexpr (!QT) {
         qn[y] = frag_straight(qb, 32 * JT * wm + 32 * y, u);
       } else {
-        const uint2 v = frag_tr(qb, kQPr, JT * wm + y / 2, u, y % 2);
+        const uint2 v = frag_tr(qb, tr_q, kQPr, y / 2, u, y % 2);
         qn[y / 2][2 * (y % 2)] = v.x;
         qn[y / 2][2 * (y % 2) + 1] = v.y;
       }
@@ -307,84 +296,106 @@ __global__ __launch_bounds__(kTileThreads, 1) void dense_tile_kernel(TileArgs a)
                                                      0, 0, 0);
   };
 
-  // Copies of sub-step u of step st (ring place ph), the s-th of kMf slots.  Whole steps: all of step st + R in
-  // sub-step 3.  Units: between two barriers Q of the step after next, then P of the step behind it.
+  // Units: copies after MFMA s of sub-step u of step st (ring place ph), spread evenly between two barriers: Q of
+  // the step after next, then P of the step behind it.
   auto copy_slot = [&](int st, auto PH, int u, int s) __attribute__((always_inline)) {
     constexpr int ph = decltype(PH)::value;
-    if constexpr (!C::kUnits) {
-      if (u == 3) {
+    const int ahead = u == 3 ? 1 : 0;                           // the period belongs to the step of its barrier
 #pragma unroll
-        for (int c = 0; c < C::kCopies; ++c)
-          if (c * kMf / C::kCopies == s) copy_one(st + R, ph, c);
-      }
-    } else {
+    for (int c = 0; c < C::kCopies; ++c) {
+      if (((u + 1) & 3) * kMf + s != C::copy_slot(c)) continue;  // slots counted from the barrier on
       constexpr int half = C::kCopies / 2;                      // copies of a unit
-#pragma unroll
-      for (int c = 0; c < C::kCopies; ++c) {
-        const int at = kTileUnitSlot[c];                        // slot of the 4 kMf from sub-step 3 on
-        if (((u + 1) & 3) * kMf + s != at) continue;
-        const int ahead = u == 3 ? 1 : 0;                       // the period belongs to the step of its barrier
-        if (c < half) copy_one(st + ahead + 1, (ph + ahead + 1) % 5, half + c);
-        else copy_one(st + ahead + 2, (ph + ahead + 2) % 5, c - half);
-      }
+      if (c < half) copy_one(st + ahead + 1, (ph + ahead + 1) % 5, half + c);
+      else copy_one(st + ahead + 2, (ph + ahead + 2) % 5, c - half);
     }
   };
-  auto kstep = [&](int st, auto PH) __attribute__((always_inline)) {
+  auto kstep = [&](int st, auto PH, auto ODD) __attribute__((always_inline)) {
     constexpr int ph = decltype(PH)::value, ph1 = (ph + 1) % C::kRing;
+    if constexpr (C::kUnits) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (u == 3) {
-        __builtin_amdgcn_s_waitcnt(tile_wait(C::kUnits ? C::kCopies / 2 : (R - 2) * C::kCopies));
-        asm volatile("s_barrier" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
+      for (int u = 0; u < 4; ++u) {
+        if (u == 3) {
+          __builtin_amdgcn_s_waitcnt(tile_wait(C::kCopies / 2));
+          asm volatile("s_barrier" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        u32x4(&pc)[IT] = pf[u & 1];
+        u32x4(&qc)[JT] = qf[u & 1];
+#pragma unroll
+        for (int s = 0; s < kMf; ++s) {
+          acc[s / JT][s % JT] = mfma(pc[s / JT], qc[s % JT], acc[s / JT][s % JT]);
+#pragma unroll
+          for (int x = 0; x < kReads; ++x)
+            if (x * kMf / kReads == s) read_one(u < 3 ? ph : ph1, (u + 1) & 3, x, pf[(u + 1) & 1], qf[(u + 1) & 1]);
+          copy_slot(st, PH, u, s);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
-      u32x4(&pc)[IT] = pf[u & 1];
-      u32x4(&qc)[JT] = qf[u & 1];
+    } else {
+      constexpr int now = 4 * decltype(ODD)::value, next = 4 - now;
+      __builtin_amdgcn_s_waitcnt(tile_wait((R - 2) * C::kCopies));   // step st + 1 has landed, this wavefront has read step st
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int s = 0; s < kMf; ++s) {
-        acc[s / JT][s % JT] = mfma(pc[s / JT], qc[s % JT], acc[s / JT][s % JT]);
+      for (int t = 0; t < 4 * kMf; ++t) {
+        const int u = t / kMf, s = t % kMf;
+        acc[s / JT][s % JT] = mfma(pf[now + u][s / JT], qf[now + u][s % JT], acc[s / JT][s % JT]);
 #pragma unroll
-        for (int x = 0; x < kReads; ++x)
-          if (x * kMf / kReads == s) read_one(u < 3 ? ph : ph1, (u + 1) & 3, x, pf[(u + 1) & 1], qf[(u + 1) & 1]);
-        copy_slot(st, PH, u, s);
+        for (int x = 0; x < 4 * kReads; ++x)
+          if (x * kMf / kReads == t) read_one(ph1, x / kReads, x % kReads, pf[next + x / kReads], qf[next + x / kReads]);
+#pragma unroll
+        for (int c = 0; c < C::kCopies; ++c)
+          if (c * 4 * kMf / C::kCopies == t) copy_one(st + R, ph, c);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
 
-  if constexpr (!C::kUnits) {
-#pragma unroll
-    for (int x = 0; x < R * C::kCopies; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
-    __builtin_amdgcn_s_waitcnt(tile_wait((R - 1) * C::kCopies));
-  } else {
-    constexpr int half = C::kCopies / 2;
+  if constexpr (C::kUnits) {
+    constexpr int half = C::kCopies / 2, early = (C::kCopies + 3) / 4;   // early: what sub-step 3 before the first would copy
+    static_assert(C::copy_slot(early - 1) < kMf && C::copy_slot(early) >= kMf, "copies before sub-step 0");
 #pragma unroll
     for (int x = 0; x < 3 * half; ++x) copy_one(x / (2 * half), x / (2 * half), x % (2 * half));
-    constexpr int early = tile_unit_early(kMf);                 // Q of step 1: what sub-step 3 would have copied
 #pragma unroll
     for (int x = 0; x < early; ++x) copy_one(1, 1, half + x);
     __builtin_amdgcn_s_waitcnt(tile_wait(half + early));
+  } else {
+#pragma unroll
+    for (int x = 0; x < R * C::kCopies; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
+    __builtin_amdgcn_s_waitcnt(tile_wait((R - 1) * C::kCopies));
   }
   asm volatile("s_barrier" ::: "memory");
 #pragma unroll
-  for (int x = 0; x < kReads; ++x) read_one(0, 0, x, pf[0], qf[0]);
+  for (int x = 0; x < (C::kUnits ? 1 : 4) * kReads; ++x)
+    read_one(0, x / kReads, x % kReads, pf[x / kReads], qf[x / kReads]);
 
   int st = 0;
   using std::integral_constant;
-  for (; st + C::kRing <= nsteps; st += C::kRing) {
-    kstep(st, integral_constant<int, 0>{});
-    kstep(st + 1, integral_constant<int, 1>{});
-    if constexpr (C::kRing > 2) kstep(st + 2, integral_constant<int, 2>{});
-    if constexpr (C::kRing > 3) kstep(st + 3, integral_constant<int, 3>{});
-    if constexpr (C::kRing > 4) kstep(st + 4, integral_constant<int, 4>{});
+  // a loop's length: places of the ring, and for whole steps both halves of the fragment registers
+  constexpr int kLoop = !C::kUnits && C::kRing % 2 ? 2 * C::kRing : C::kRing;
+  auto step = [&](auto X) __attribute__((always_inline)) {
+    constexpr int x = decltype(X)::value;
+    kstep(st + x, integral_constant<int, x % C::kRing>{}, integral_constant<int, x % 2>{});
+  };
+  auto rest = [&](auto X) __attribute__((always_inline)) {
+    constexpr int x = decltype(X)::value;
+    if constexpr (x < kLoop - 1)
+      if (st + x < nsteps) step(X);
+  };
+  for (; st + kLoop <= nsteps; st += kLoop) {
+    step(integral_constant<int, 0>{});
+    step(integral_constant<int, 1>{});
+    if constexpr (kLoop > 2) step(integral_constant<int, 2>{});
+    if constexpr (kLoop > 3) step(integral_constant<int, 3>{});
+    if constexpr (kLoop > 4) step(integral_constant<int, 4>{});
+    if constexpr (kLoop > 5) step(integral_constant<int, 5>{});
   }
-  if (st < nsteps) kstep(st, integral_constant<int, 0>{});
-  if constexpr (C::kRing > 2)
-    if (st + 1 < nsteps) kstep(st + 1, integral_constant<int, 1>{});
-  if constexpr (C::kRing > 3)
-    if (st + 2 < nsteps) kstep(st + 2, integral_constant<int, 2>{});
-  if constexpr (C::kRing > 4)
-    if (st + 3 < nsteps) kstep(st + 3, integral_constant<int, 3>{});
+  static_assert(kLoop <= 6, "steps of the loop");
+  rest(integral_constant<int, 0>{});
+  rest(integral_constant<int, 1>{});
+  rest(integral_constant<int, 2>{});
+  rest(integral_constant<int, 3>{});
+  rest(integral_constant<int, 4>{});
   __builtin_amdgcn_s_waitcnt(tile_wait(0));
   __syncthreads();
 
@@ -647,6 +658,9 @@ inline hipError_t launch_tile_cfg(TileArgs a, hipStream_t stream) {
   const int n = C::EPI == kTileGated ? a.I : a.N;
   a.m_tiles = (a.M + C::BM - 1) / C::BM;
   a.n_tiles = (n + width - 1) / width;
+  // While the m side fits an XCD's L2, tiles of n may be anywhere in K; a larger one is shared
+  // through the L2 by workgroups of one XCD that are at the same step.
+  a.turn_by_tile = (int64_t)a.M * a.K * (C::I8 ? 1 : 2) <= ((int64_t)2 << 20);
   const int64_t grid = (int64_t)a.m_tiles * a.n_tiles * a.splits;
   return launch_kernel((const void*)dense_tile_kernel<C>, dim3((unsigned)grid), dim3(kTileThreads), stream, a);
 }
@@ -662,6 +676,9 @@ inline hipError_t launch_tile(const TileArgs& a, hipStream_t stream) {
       case 128: return launch_tile_cfg<TileCfg<2, 4, 4, 1, PT, QT, EPI, 3>>(a, stream);
     }
   }
+#ifdef FORCE_B
+  return launch_tile_cfg<TileCfg<2, 2, 2, 2, PT, QT, EPI, FORCE_B>>(a, stream);
+#endif
   return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 0>>(a, stream);
 }
 
