@@ -650,8 +650,62 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
   }
 }
 
-// Launch with the tile that suits M: 256 x 256 over 2 x 2 wavefronts, or for few rows 256 (n) x 32, 64 or 128
-// over 4 x 1, whose smaller tiles leave room for more steps in flight.
+// Tiles, as rows of m by columns of n (gated: half the columns of output) and workgroups a compute unit takes.
+enum TileSize : int { kTile32, kTile64, kTile128, kTile256 };
+struct TileShape {
+  int bm, bn, per_cu;
+};
+constexpr TileShape tile_shape(TileSize t) {
+  return t == kTile32 ? TileShape{32, 128, 2} : t == kTile64 ? TileShape{64, 128, 2}
+       : t == kTile128 ? TileShape{128, 128, 2} : TileShape{256, 256, 1};
+}
+inline int64_t tile_count(TileSize t, int64_t M, int64_t N) {
+  const TileShape s = tile_shape(t);
+  return (M + s.bm - 1) / s.bm * ((N + s.bn - 1) / s.bn);
+}
+
+constexpr int kTileCus = 256;      // fixed, so that a workspace's size does not depend on the device that is current
+
+// The tile for an [M, N] product over `steps` steps, K split `splits` times.  Few rows: the least tile that holds
+// them (bound by memory; two workgroups a compute unit keep more of it in flight).  Else by the time measured for a
+// round of workgroups: 1.3 us a step and 8 us besides for 256 x 256, 1.0 and 6 for two of 128 x 128, 0.65 a
+// step where those have a compute unit each (4096 x 28672 over 64 steps: 740 and 890 us; 333 x 11232
+// over 33: 47 and 33 us).
+inline TileSize tile_size(int64_t M, int64_t N, int64_t steps, int64_t splits) {
+  if (M <= 32) return kTile32;
+  if (M <= 64) return kTile64;
+  const int64_t t256 = tile_count(kTile256, M, N) * splits, t128 = tile_count(kTile128, M, N) * splits;
+  const double big = (double)((t256 + kTileCus - 1) / kTileCus) * (1.3 * (double)steps + 8.0);
+  const double small = t128 <= kTileCus ? 0.65 * (double)steps + 6.0
+                                        : (double)((t128 + 2 * kTileCus - 1) / (2 * kTileCus)) * (1.0 * (double)steps + 6.0);
+  return small < big ? kTile128 : kTile256;
+}
+
+// Splits of K (in steps of 64) for an [M, N] product whose tiles do not fill the compute units: at least `least`
+// steps each, the tile chosen with them.
+struct TileSplit {
+  TileSize size;
+  int splits, k_split;
+};
+inline TileSplit tile_split(int64_t M, int64_t N, int64_t K, int64_t least, int64_t most) {
+  const int64_t steps = (K + 63) / 64;
+  TileSplit best = {tile_size(M, N, steps, 1), 1, 0};
+  const TileShape shape = tile_shape(M > 64 ? kTile128 : best.size);
+  const int64_t tiles = (M + shape.bm - 1) / shape.bm * ((N + shape.bn - 1) / shape.bn);
+  int64_t s = kTileCus * shape.per_cu / tiles;
+  s = s > most ? most : s;
+  s = s > steps / least ? steps / least : s;
+  if (s > 1) {
+    const int64_t per = (steps + s - 1) / s;
+    best.splits = (int)((steps + per - 1) / per);
+    best.k_split = (int)per * 64;
+    best.size = tile_size(M, N, per, best.splits);
+  } else {
+    best.k_split = (int)steps * 64;
+  }
+  return best;
+}
+
 template <class C>
 inline hipError_t launch_tile_cfg(TileArgs a, hipStream_t stream) {
   const int width = C::EPI == kTileGated ? C::BN / 2 : C::BN;
@@ -665,20 +719,17 @@ inline hipError_t launch_tile_cfg(TileArgs a, hipStream_t stream) {
   return launch_kernel((const void*)dense_tile_kernel<C>, dim3((unsigned)grid), dim3(kTileThreads), stream, a);
 }
 
-inline int tile_rows(int64_t M) { return M > 128 ? 256 : M > 64 ? 128 : M > 32 ? 64 : 32; }
-
 template <int EPI, bool PT, bool QT>
-inline hipError_t launch_tile(const TileArgs& a, hipStream_t stream) {
+inline hipError_t launch_tile(const TileArgs& a, TileSize size, hipStream_t stream) {
   if constexpr (!QT) {
-    switch (tile_rows(a.M)) {
-      case 32: return launch_tile_cfg<TileCfg<2, 1, 4, 1, PT, QT, EPI, 4>>(a, stream);
-      case 64: return launch_tile_cfg<TileCfg<2, 2, 4, 1, PT, QT, EPI, 3>>(a, stream);
-      case 128: return launch_tile_cfg<TileCfg<2, 4, 4, 1, PT, QT, EPI, 3>>(a, stream);
+    if (size == kTile32) {
+      // a wavefront of the gated kernel needs a tile of gates and one of ups
+      if constexpr (EPI == kTileGated) return launch_tile_cfg<TileCfg<2, 1, 2, 2, PT, QT, EPI, 3>>(a, stream);
+      else return launch_tile_cfg<TileCfg<1, 1, 4, 1, PT, QT, EPI, 4>>(a, stream);
     }
+    if (size == kTile64) return launch_tile_cfg<TileCfg<2, 1, 2, 2, PT, QT, EPI, 3>>(a, stream);
   }
-#ifdef FORCE_B
-  return launch_tile_cfg<TileCfg<2, 2, 2, 2, PT, QT, EPI, FORCE_B>>(a, stream);
-#endif
+  if (size != kTile256) return launch_tile_cfg<TileCfg<2, 2, 2, 2, PT, QT, EPI, 0>>(a, stream);
   return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 0>>(a, stream);
 }
 

@@ -14,35 +14,29 @@
 
 namespace nvfp4 {
 
-// Sum of `splits` partial products: out bf16 [M][N] from float [splits][M][N].
-__global__ __launch_bounds__(256) void gated_join_kernel(const float* __restrict__ parts, int64_t count, int splits,
-                                                         uint16_t* __restrict__ out) {
-  for (int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < count; i += 8 * 256 * (int64_t)gridDim.x) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < splits; ++s) {
-      const f32x4* const p = reinterpret_cast<const f32x4*>(parts + s * count + i);
-      const f32x4 lo = p[0], hi = p[1];
+// Sum of `splits` partial products: out bf16 [M][N] from float [splits][M][N]; a thread eight columns.
+__global__ __launch_bounds__(64) void gated_join_kernel(const float* __restrict__ parts, int64_t count, int splits,
+                                                        uint16_t* __restrict__ out) {
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 64 + threadIdx.x);
+  if (i >= count) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const f32x4* const p = reinterpret_cast<const f32x4*>(parts + s * count + i);
+    const f32x4 lo = p[0], hi = p[1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += lo[e];
-        v[4 + e] += hi[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      v[e] += lo[e];
+      v[4 + e] += hi[e];
     }
-    *reinterpret_cast<u32x4*>(out + i) = pack8(v);
   }
+  *reinterpret_cast<u32x4*>(out + i) = pack8(v);
 }
 
 static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
 
-// Splits of K for an [M, N] product: enough workgroups for the compute units, at least 256 k each.
-static int gated_splits(int64_t M, int64_t N, int64_t K, int cus) {
-  const int bm = tile_rows(M);
-  const int64_t tiles = (M + bm - 1) / bm * ((N + 255) / 256);
-  int64_t s = cus / tiles;
-  s = s > 16 ? 16 : s;
-  const int64_t most = K / 256 > 1 ? K / 256 : 1;
-  return (int)(s < 1 ? 1 : s > most ? most : s);
-}
+// The down projection and dx: K split where the tiles are few, at least 8 steps a part.
+static TileSplit gated_split(int64_t M, int64_t N, int64_t K) { return tile_split(M, N, K, 8, 16); }
 
 struct GatedLayout {
   int64_t parts, bytes;
@@ -53,8 +47,7 @@ static GatedLayout gated_layout(int64_t T, int64_t H, int64_t I, bool backward) 
   // the forward pass's a and the backward's [dg, du] share a place
   at += up256((backward ? 4 : 2) * T * I);
   l.parts = at;
-  const int cus = 256;
-  const int sd = gated_splits(T, H, I, cus), sx = gated_splits(T, H, 2 * I, cus);
+  const int sd = gated_split(T, H, I).splits, sx = gated_split(T, H, 2 * I).splits;
   const int s = backward && sx > sd ? sx : sd;
   if (s > 1) at += up256(4 * s * T * H);
   l.bytes = at;
@@ -81,19 +74,18 @@ static hipError_t gated_product(const void* q, int64_t q_pitch, const void* p, i
   a.N = (int)N;
   a.K = (int)K;
   a.out_pitch = N;
-  const int s = gated_splits(M, N, K, 256);
-  a.k_split = (int)(((K + s - 1) / s + 63) / 64 * 64);
-  a.splits = (int)((K + a.k_split - 1) / a.k_split);
+  const TileSplit s = gated_split(M, N, K);
+  a.k_split = s.k_split;
+  a.splits = s.splits;
   if (a.splits == 1) {
     a.out = out;
-    return launch_tile<kTileBf16, PT, false>(a, stream);
+    return launch_tile<kTileBf16, PT, false>(a, s.size, stream);
   }
   a.out = parts;
-  const hipError_t e = launch_tile<kTileF32, PT, false>(a, stream);
+  const hipError_t e = launch_tile<kTileF32, PT, false>(a, s.size, stream);
   if (e != hipSuccess) return e;
-  const int64_t blocks = (M * N / 8 + 255) / 256;
-  return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256),
-                       stream, (const float*)parts, (int64_t)(M * N), (int)a.splits, (uint16_t*)out);
+  return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)((M * N / 8 + 63) / 64)), dim3(64), stream,
+                       (const float*)parts, (int64_t)(M * N), (int)a.splits, (uint16_t*)out);
 }
 
 // out bf16 [M, N] = q^T p, q [K, M], p [K, N]
@@ -112,7 +104,7 @@ static hipError_t gated_weight_grad(const void* q, int64_t M, const void* p, int
   a.k_split = (int)((K + 63) / 64 * 64);
   a.out = out;
   a.out_pitch = N;
-  return launch_tile<kTileBf16, true, true>(a, stream);
+  return launch_tile<kTileBf16, true, true>(a, tile_size(M, N, (K + 63) / 64, 1), stream);
 }
 
 hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I, void* h,
@@ -134,7 +126,7 @@ hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13
   a.out = h == nullptr ? (void*)ws : (void*)((uint16_t*)h + 2 * I);
   a.out_pitch = h == nullptr ? I : 3 * I;
   a.h = (uint16_t*)h;
-  const hipError_t e = launch_tile<kTileGated, false, false>(a, stream);
+  const hipError_t e = launch_tile<kTileGated, false, false>(a, tile_size(T, 2 * I, (H + 63) / 64, 1), stream);
   if (e != hipSuccess) return e;
   return gated_product<false>(a.out, a.out_pitch, w2, T, H, I, y, (float*)(ws + l.parts), stream);
 }
@@ -159,7 +151,7 @@ hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const 
   a.k_split = (int)((H + 63) / 64 * 64);
   a.h = (uint16_t*)const_cast<void*>(h);
   a.dh = (uint16_t*)ws;
-  hipError_t e = launch_tile<kTileGatedBack, true, false>(a, stream);
+  hipError_t e = launch_tile<kTileGatedBack, true, false>(a, tile_size(T, I, (H + 63) / 64, 1), stream);
   if (e != hipSuccess) return e;
   if (dw2 != nullptr) {
     e = gated_weight_grad(dy, H, (const uint16_t*)h + 2 * I, 3 * I, I, T, dw2, stream);

@@ -97,7 +97,7 @@ hipError_t launch_int8_gemm(const int8_t* xq, const float* sx, int64_t M, int64_
   a.sx = sx;
   a.sw = sw;
   a.bias = (const uint16_t*)bias;
-  return launch_tile<kTileInt8, false, false>(a, stream);
+  return launch_tile<kTileInt8, false, false>(a, tile_size(M, N, (K + 127) / 128, 1), stream);
 }
 
 }  // namespace nvfp4

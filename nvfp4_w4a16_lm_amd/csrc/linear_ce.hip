@@ -18,12 +18,11 @@ namespace nvfp4 {
 
 static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
 
-constexpr int kCeRows = 16;          // rows a workgroup gathers
-
 struct CeGather {
   const uint16_t* x;
   const int32_t* tok;
   int32_t M, V, K;
+  int32_t rows;                      // rows a workgroup gathers: four, more beyond 4096 rows, as each counts all before it
   uint16_t* xc;                      // rows that count, in order
   int32_t* ctok;
   int32_t* index;                    // their rows
@@ -41,27 +40,34 @@ struct CeGather {
   uint16_t* dx;                      // zero in the other rows
 };
 
-// Workgroup b: rows 16 b .. + 15.  Its first place is the number of earlier rows that count.
+// Workgroup b: rows a.rows b and on, a wavefront each, four at a time.  A row's place is the number of earlier rows
+// that count.
 __global__ __launch_bounds__(256) void ce_gather_kernel(CeGather a) {
   __shared__ int part[4];
-  const int tid = threadIdx.x, row0 = blockIdx.x * kCeRows;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row0 = blockIdx.x * a.rows, row1 = min(row0 + a.rows, a.M);
   int before = 0;
+#pragma unroll 8
   for (int i = tid; i < row0; i += 256) before += (uint32_t)a.tok[i] < (uint32_t)a.V;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) before += __shfl_xor(before, d, 64);
-  if ((tid & 63) == 0) part[tid >> 6] = before;
+  if (lane == 0) part[wave] = before;
   __syncthreads();
-  int place = part[0] + part[1] + part[2] + part[3];
+  int first = part[0] + part[1] + part[2] + part[3];
   const int pieces = a.K / 8;
-  for (int row = row0; row < min(row0 + kCeRows, a.M); ++row) {
-    const int tok = a.tok[row];
-    const bool counts = (uint32_t)tok < (uint32_t)a.V;
-    if (counts) {
+  for (int base = row0; base < row1; base += 4) {
+    const bool mine = lane < 4 && base + lane < row1 && (uint32_t)a.tok[base + lane] < (uint32_t)a.V;
+    const uint32_t rows = (uint32_t)__ballot(mine);
+    const int row = base + wave, place = first + __popc(rows & ((1u << wave) - 1));
+    first += __popc(rows);
+    if (row >= row1) continue;
+    if (rows >> wave & 1) {
       const u32x4* const src = reinterpret_cast<const u32x4*>(a.x + (int64_t)row * a.K);
       u32x4* const dst = reinterpret_cast<u32x4*>(a.xc + (int64_t)place * a.K);
-      for (int p = tid; p < pieces; p += 256) dst[p] = src[p];
-      if (tid == 0) {
-        a.ctok[place] = tok;
+#pragma unroll 8
+      for (int p = lane; p < pieces; p += 64) dst[p] = src[p];
+      if (lane == 0) {
+        a.ctok[place] = a.tok[row];
         a.index[place] = row;
         if (a.coef != nullptr) {
           const float d = a.dloss[row];
@@ -69,20 +75,19 @@ __global__ __launch_bounds__(256) void ce_gather_kernel(CeGather a) {
           a.coef[place] = make_float2(d + (a.dlse != nullptr ? a.dlse[row] : 0.0f), d);
         }
       }
-      ++place;
     } else {
       if (a.dx != nullptr) {
         u32x4* const dst = reinterpret_cast<u32x4*>(a.dx + (int64_t)row * a.K);
-        for (int p = tid; p < pieces; p += 256) dst[p] = u32x4{0, 0, 0, 0};
+        for (int p = lane; p < pieces; p += 64) dst[p] = u32x4{0, 0, 0, 0};
       }
-      if (tid == 0 && a.loss != nullptr) {
+      if (lane == 0 && a.loss != nullptr) {
         a.loss[row] = 0.0f;
         if (a.lse != nullptr) a.lse[row] = 0.0f;
         a.stats[row] = make_float2(0.0f, 1.0f);
       }
     }
   }
-  if (row0 + kCeRows >= a.M && tid == 0) *a.count = place;
+  if (row1 == a.M && tid == 0) *a.count = first;
 }
 
 // A wavefront per row joins its tiles' maxima and sums.
@@ -118,26 +123,24 @@ __global__ __launch_bounds__(256) void ce_join_kernel(const float2* __restrict__
   }
 }
 
-// dx: the splits' sums, rounded once, back in their rows
-__global__ __launch_bounds__(256) void ce_dx_kernel(const float* __restrict__ parts, int M, int K, int splits,
-                                                    const int32_t* __restrict__ index,
-                                                    const int32_t* __restrict__ count, uint16_t* __restrict__ dx) {
-  const int row = blockIdx.x;
-  if (row >= *count) return;
-  const int64_t at = index[row];
-  for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < splits; ++s) {
-      const f32x4* const p = reinterpret_cast<const f32x4*>(parts + ((int64_t)s * M + row) * K + k);
-      const f32x4 lo = p[0], hi = p[1];
+// dx: the splits' sums, rounded once, back in their rows; a thread eight columns of a row
+__global__ __launch_bounds__(64) void ce_dx_kernel(const float* __restrict__ parts, int M, int K, int splits,
+                                                   const int32_t* __restrict__ index,
+                                                   const int32_t* __restrict__ count, uint16_t* __restrict__ dx) {
+  const int row = blockIdx.x, k = 8 * (blockIdx.y * 64 + threadIdx.x);
+  if (row >= *count || k >= K) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const f32x4* const p = reinterpret_cast<const f32x4*>(parts + ((int64_t)s * M + row) * K + k);
+    const f32x4 lo = p[0], hi = p[1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] += lo[e];
-        v[4 + e] += hi[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      v[e] += lo[e];
+      v[4 + e] += hi[e];
     }
-    *reinterpret_cast<u32x4*>(dx + at * K + k) = pack8(v);
   }
+  *reinterpret_cast<u32x4*>(dx + (int64_t)index[row] * K + k) = pack8(v);
 }
 
 // db of a piece: column sums of dz, 64 columns a workgroup
@@ -170,7 +173,8 @@ constexpr int64_t kCePieceMost = 1 << 18;               // its columns: 32-bit o
 struct CeLayout {
   int64_t xc, ctok, index, count, parts, tlogit, cstats, coef, d, acc, bytes;
   int64_t piece, tiles;
-  int splits;
+  TileSize logits, grad;           // tiles of the two passes over the logits
+  TileSplit dx;
 };
 
 static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
@@ -185,7 +189,8 @@ static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
   l.ctok = take(4 * M);
   l.index = take(4 * M);
   l.count = take(4);
-  l.tiles = (V + 255) / 256;
+  l.logits = tile_size(M, V, (K + 63) / 64, 1);
+  l.tiles = (V + tile_shape(l.logits).bn - 1) / tile_shape(l.logits).bn;
   // the forward pass's part and the backward's overlap
   const int64_t common = at;
   l.parts = take(8 * M * l.tiles);
@@ -200,13 +205,9 @@ static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
     const int64_t pieces = (V + most - 1) / most;
     l.piece = up256((V + pieces - 1) / pieces);
     l.d = take(2 * M * l.piece);
-    const int bm = tile_rows(M);
-    const int64_t tiles = (M + bm - 1) / bm * ((K + 255) / 256);
-    int64_t s = 256 / tiles;
-    const int64_t deep = l.piece / 512 > 1 ? l.piece / 512 : 1;
-    s = s < 1 ? 1 : s > 64 ? 64 : s;
-    l.splits = (int)(s > deep ? deep : s);
-    l.acc = take(4 * l.splits * M * K);
+    l.grad = tile_size(M, l.piece, (K + 63) / 64, 1);
+    l.dx = tile_split(M, K, l.piece, 8, 64);
+    l.acc = take(4 * l.dx.splits * M * K);
     if (at < forward_end) at = forward_end;
   }
   l.bytes = at;
@@ -237,6 +238,12 @@ static TileArgs ce_logits(const void* w, int64_t V, int64_t K, const void* bias,
   return a;
 }
 
+static hipError_t launch_ce_gather(CeGather g, hipStream_t stream) {
+  g.rows = 4 * ((g.M + 4095) / 4096);
+  return launch_kernel((const void*)ce_gather_kernel, dim3((unsigned)((g.M + g.rows - 1) / g.rows)), dim3(256), stream,
+                       g);
+}
+
 hipError_t launch_linear_ce(const void* x, int64_t M, int64_t K, const void* w, int64_t V, const void* bias,
                             const int32_t* tok, void* workspace, float* loss, float* lse, float* stats,
                             hipStream_t stream) {
@@ -255,14 +262,13 @@ hipError_t launch_linear_ce(const void* x, int64_t M, int64_t K, const void* w, 
   g.loss = loss;
   g.lse = lse;
   g.stats = (float2*)stats;
-  hipError_t e = launch_kernel((const void*)ce_gather_kernel, dim3((unsigned)((M + kCeRows - 1) / kCeRows)), dim3(256),
-                               stream, g);
+  hipError_t e = launch_ce_gather(g, stream);
   if (e != hipSuccess) return e;
   TileArgs a = ce_logits(w, V, K, bias, ws, l, M);
   a.parts = (float2*)(ws + l.parts);
   a.part_pitch = (int)l.tiles;
   a.tlogit = (float*)(ws + l.tlogit);
-  e = launch_tile<kTileCeStats, false, false>(a, stream);
+  e = launch_tile<kTileCeStats, false, false>(a, l.logits, stream);
   if (e != hipSuccess) return e;
   return launch_kernel((const void*)ce_join_kernel, dim3((unsigned)((M + 3) / 4)), dim3(256), stream,
                        (const float2*)(ws + l.parts), (int)l.tiles, (const float*)(ws + l.tlogit),
@@ -290,8 +296,7 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
   g.cstats = (float2*)(ws + l.cstats);
   g.coef = (float2*)(ws + l.coef);
   g.dx = (uint16_t*)dx;
-  hipError_t e = launch_kernel((const void*)ce_gather_kernel, dim3((unsigned)((M + kCeRows - 1) / kCeRows)), dim3(256),
-                               stream, g);
+  hipError_t e = launch_ce_gather(g, stream);
   if (e != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < V; v0 += l.piece) {
     const int64_t width = V - v0 < l.piece ? V - v0 : l.piece;
@@ -302,7 +307,7 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
     a.coef = g.coef;
     a.out = ws + l.d;
     a.out_pitch = l.piece;
-    e = launch_tile<kTileCeGrad, false, false>(a, stream);
+    e = launch_tile<kTileCeGrad, false, false>(a, l.grad, stream);
     if (e != hipSuccess) return e;
     if (dx != nullptr) {
       TileArgs b = {};
@@ -316,12 +321,12 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
       b.N = (int)K;
       b.K = (int)width;
       b.m_count = g.count;
-      b.splits = l.splits;
-      b.k_split = (int)(((width + l.splits - 1) / l.splits + 63) / 64 * 64);
+      b.splits = l.dx.splits;
+      b.k_split = l.dx.k_split;                                   // a narrower last piece leaves the last parts empty
       b.out = ws + l.acc;
       b.out_pitch = K;
       b.accumulate = v0 > 0;
-      e = launch_tile<kTileF32, true, false>(b, stream);
+      e = launch_tile<kTileF32, true, false>(b, l.dx.size, stream);
       if (e != hipSuccess) return e;
     }
     if (dw != nullptr) {
@@ -339,7 +344,7 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
       b.k_split = (int)((M + 63) / 64 * 64);
       b.out = (uint16_t*)dw + v0 * K;
       b.out_pitch = K;
-      e = launch_tile<kTileBf16, true, true>(b, stream);
+      e = launch_tile<kTileBf16, true, true>(b, tile_size(width, K, (M + 63) / 64, 1), stream);
       if (e != hipSuccess) return e;
     }
     if (db != nullptr) {
@@ -350,8 +355,8 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
     }
   }
   if (dx == nullptr) return hipSuccess;
-  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M), dim3(256), stream, (const float*)(ws + l.acc),
-                       (int)M, (int)K, (int)l.splits, (const int32_t*)g.index, (const int32_t*)g.count,
+  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M, (unsigned)((K + 511) / 512)), dim3(64), stream, (const float*)(ws + l.acc),
+                       (int)M, (int)K, l.dx.splits, (const int32_t*)g.index, (const int32_t*)g.count,
                        (uint16_t*)dx);
 }
 
