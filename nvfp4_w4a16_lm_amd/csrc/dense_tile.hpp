@@ -136,14 +136,14 @@ struct TileCfg {
   static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;      // workgroups meant to share a compute unit
   static_assert(WN * WM == 4 && kLds <= 160 * 1024, "tile");
   static_assert(!I8 || (!PT && !QT), "int8 operands are straight");
-  static_assert(kUnits ? BN == BM : R >= 2 && R <= 4 && R * kCopies < 64, "ring");
+  static_assert(kUnits ? BN >= BM : R >= 2 && R <= 4 && R * kCopies < 64, "ring");
 };
 
 template <class C>
 __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(TileArgs a) {
   constexpr int IT = C::IT, JT = C::JT, R = C::R, BN = C::BN, BM = C::BM;
   constexpr bool PT = C::PT, QT = C::QT;
-  constexpr int kPC = BN / 32;                                  // copies of the n side
+  constexpr int kPC = BN / 32, kQC = BM / 32;                    // copies of each side
   constexpr int kMf = IT * JT;                                  // MFMAs per sub-step
   constexpr int kReads = IT * (PT ? 2 : 1) + JT * (QT ? 2 : 1);
   using Acc = std::conditional_t<C::I8, i32x16, f32x16>;
@@ -304,9 +304,8 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
 #pragma unroll
     for (int c = 0; c < C::kCopies; ++c) {
       if (((u + 1) & 3) * kMf + s != C::copy_slot(c)) continue;  // slots counted from the barrier on
-      constexpr int half = C::kCopies / 2;                      // copies of a unit
-      if (c < half) copy_one(st + ahead + 1, (ph + ahead + 1) % 5, half + c);
-      else copy_one(st + ahead + 2, (ph + ahead + 2) % 5, c - half);
+      if (c < kQC) copy_one(st + ahead + 1, (ph + ahead + 1) % 5, kPC + c);
+      else copy_one(st + ahead + 2, (ph + ahead + 2) % 5, c - kQC);
     }
   };
   auto kstep = [&](int st, auto PH, auto ODD) __attribute__((always_inline)) {
@@ -315,7 +314,7 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (u == 3) {
-          __builtin_amdgcn_s_waitcnt(tile_wait(C::kCopies / 2));
+          __builtin_amdgcn_s_waitcnt(tile_wait(kPC));
           asm volatile("s_barrier" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -352,13 +351,13 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
   };
 
   if constexpr (C::kUnits) {
-    constexpr int half = C::kCopies / 2, early = (C::kCopies + 3) / 4;   // early: what sub-step 3 before the first would copy
-    static_assert(C::copy_slot(early - 1) < kMf && C::copy_slot(early) >= kMf, "copies before sub-step 0");
+    constexpr int early = (C::kCopies + 3) / 4;                 // what sub-step 3 before the first would have copied
+    static_assert(C::copy_slot(early - 1) < kMf && C::copy_slot(early) >= kMf && early <= kQC, "copies before sub-step 0");
 #pragma unroll
-    for (int x = 0; x < 3 * half; ++x) copy_one(x / (2 * half), x / (2 * half), x % (2 * half));
+    for (int x = 0; x < C::kCopies + kPC; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
 #pragma unroll
-    for (int x = 0; x < early; ++x) copy_one(1, 1, half + x);
-    __builtin_amdgcn_s_waitcnt(tile_wait(half + early));
+    for (int x = 0; x < early; ++x) copy_one(1, 1, kPC + x);
+    __builtin_amdgcn_s_waitcnt(tile_wait(kPC + early));
   } else {
 #pragma unroll
     for (int x = 0; x < R * C::kCopies; ++x) copy_one(x / C::kCopies, x / C::kCopies, x % C::kCopies);
@@ -651,13 +650,13 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
 }
 
 // Tiles, as rows of m by columns of n (gated: half the columns of output) and workgroups a compute unit takes.
-enum TileSize : int { kTile32, kTile64, kTile128, kTile256 };
+enum TileSize : int { kTile32, kTile64, kTile128, kTile192, kTile256 };
 struct TileShape {
   int bm, bn, per_cu;
 };
 constexpr TileShape tile_shape(TileSize t) {
   return t == kTile32 ? TileShape{32, 128, 2} : t == kTile64 ? TileShape{64, 128, 2}
-       : t == kTile128 ? TileShape{128, 128, 2} : TileShape{256, 256, 1};
+       : t == kTile128 ? TileShape{128, 128, 2} : t == kTile192 ? TileShape{192, 256, 1} : TileShape{256, 256, 1};
 }
 inline int64_t tile_count(TileSize t, int64_t M, int64_t N) {
   const TileShape s = tile_shape(t);
@@ -667,17 +666,21 @@ inline int64_t tile_count(TileSize t, int64_t M, int64_t N) {
 constexpr int kTileCus = 256;      // fixed, so that a workspace's size does not depend on the device that is current
 
 // The tile for an [M, N] product over `steps` steps, K split `splits` times.  Few rows: the least tile that holds
-// them (bound by memory; two workgroups a compute unit keep more of it in flight).  Else by the time measured for a
-// round of workgroups: 1.3 us a step and 8 us besides for 256 x 256, 1.0 and 6 for two of 128 x 128, 0.65 a
-// step where those have a compute unit each (4096 x 28672 over 64 steps: 740 and 890 us; 333 x 11232
-// over 33: 47 and 33 us).
+// them (bound by memory; two workgroups a compute unit keep more of it in flight).  Else by the time of a round of
+// workgroups, as measured: 1.3 us a step and 8 us besides for 256 x 256, 1.0 and 7 for 192 x 256, 1.0 and 2.5
+// for two of 128 x 128 (one's epilogue under the other's steps), or 0.65 and 6 where those have a compute
+// unit each.  4096 x 28672 over 64 steps: 740 us in 256 x 256, 890 in 128 x 128; 333 x 32003 over 33: 59, 52 (192 x 256),
+// 67; 333 x 11232 over 33: 46, 37, 32; 32003 x 2080 over 6: 76, 72, 67.
 inline TileSize tile_size(int64_t M, int64_t N, int64_t steps, int64_t splits) {
   if (M <= 32) return kTile32;
   if (M <= 64) return kTile64;
   const int64_t t256 = tile_count(kTile256, M, N) * splits, t128 = tile_count(kTile128, M, N) * splits;
   const double big = (double)((t256 + kTileCus - 1) / kTileCus) * (1.3 * (double)steps + 8.0);
   const double small = t128 <= kTileCus ? 0.65 * (double)steps + 6.0
-                                        : (double)((t128 + 2 * kTileCus - 1) / (2 * kTileCus)) * (1.0 * (double)steps + 6.0);
+                                        : (double)((t128 + 2 * kTileCus - 1) / (2 * kTileCus)) * (1.0 * (double)steps + 2.5);
+  const int64_t t192 = tile_count(kTile192, M, N) * splits;
+  const double mid = (double)((t192 + kTileCus - 1) / kTileCus) * (1.0 * (double)steps + 7.0);
+  if (mid < big && mid < small) return kTile192;
   return small < big ? kTile128 : kTile256;
 }
 
@@ -706,6 +709,40 @@ inline TileSplit tile_split(int64_t M, int64_t N, int64_t K, int64_t least, int6
   return best;
 }
 
+// Eight columns from `at` of the sum of `splits` partial products `stride` floats apart, by 256 threads: thread
+// t's wavefront adds every fourth part, the first wavefront the four sums.  Only lanes with `on` read; the sum
+// is the first wavefront's.
+__device__ __forceinline__ void tile_join(const float* __restrict__ parts, int64_t at, int64_t stride, int splits,
+                                          bool on, float (&v)[8]) {
+  __shared__ float sums[3][64][9];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  if (on) {
+#pragma unroll 4
+    for (int s = wave; s < splits; s += 4) {
+      const f32x4* const p = reinterpret_cast<const f32x4*>(parts + s * stride + at);
+      const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] += lo[e];
+        v[4 + e] += hi[e];
+      }
+    }
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[wave - 1][lane][e] = v[e];
+  }
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 0; w < 3; ++w)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += sums[w][lane][e];
+  }
+}
+
 template <class C>
 inline hipError_t launch_tile_cfg(TileArgs a, hipStream_t stream) {
   const int width = C::EPI == kTileGated ? C::BN / 2 : C::BN;
@@ -729,7 +766,8 @@ inline hipError_t launch_tile(const TileArgs& a, TileSize size, hipStream_t stre
     }
     if (size == kTile64) return launch_tile_cfg<TileCfg<2, 1, 2, 2, PT, QT, EPI, 3>>(a, stream);
   }
-  if (size != kTile256) return launch_tile_cfg<TileCfg<2, 2, 2, 2, PT, QT, EPI, 0>>(a, stream);
+  if (size <= kTile128) return launch_tile_cfg<TileCfg<2, 2, 2, 2, PT, QT, EPI, 0>>(a, stream);
+  if (size == kTile192) return launch_tile_cfg<TileCfg<4, 3, 2, 2, PT, QT, EPI, 0>>(a, stream);
   return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 0>>(a, stream);
 }
 

@@ -14,23 +14,13 @@
 
 namespace nvfp4 {
 
-// Sum of `splits` partial products: out bf16 [M][N] from float [splits][M][N]; a thread eight columns.
-__global__ __launch_bounds__(64) void gated_join_kernel(const float* __restrict__ parts, int64_t count, int splits,
-                                                        uint16_t* __restrict__ out) {
-  const int64_t i = 8 * ((int64_t)blockIdx.x * 64 + threadIdx.x);
-  if (i >= count) return;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const f32x4* const p = reinterpret_cast<const f32x4*>(parts + s * count + i);
-    const f32x4 lo = p[0], hi = p[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] += lo[e];
-      v[4 + e] += hi[e];
-    }
-  }
-  *reinterpret_cast<u32x4*>(out + i) = pack8(v);
+// Sum of `splits` partial products: out bf16 [M][N] from float [splits][M][N].
+__global__ __launch_bounds__(256) void gated_join_kernel(const float* __restrict__ parts, int64_t count, int splits,
+                                                         uint16_t* __restrict__ out) {
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63));
+  float v[8];
+  tile_join(parts, i, count, splits, i < count, v);
+  if (threadIdx.x < 64 && i < count) *reinterpret_cast<u32x4*>(out + i) = pack8(v);
 }
 
 static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -84,7 +74,7 @@ static hipError_t gated_product(const void* q, int64_t q_pitch, const void* p, i
   a.out = parts;
   const hipError_t e = launch_tile<kTileF32, PT, false>(a, s.size, stream);
   if (e != hipSuccess) return e;
-  return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)((M * N / 8 + 63) / 64)), dim3(64), stream,
+  return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)((M * N / 8 + 63) / 64)), dim3(256), stream,
                        (const float*)parts, (int64_t)(M * N), (int)a.splits, (uint16_t*)out);
 }
 

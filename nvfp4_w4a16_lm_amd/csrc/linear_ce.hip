@@ -123,24 +123,15 @@ __global__ __launch_bounds__(256) void ce_join_kernel(const float2* __restrict__
   }
 }
 
-// dx: the splits' sums, rounded once, back in their rows; a thread eight columns of a row
-__global__ __launch_bounds__(64) void ce_dx_kernel(const float* __restrict__ parts, int M, int K, int splits,
-                                                   const int32_t* __restrict__ index,
-                                                   const int32_t* __restrict__ count, uint16_t* __restrict__ dx) {
-  const int row = blockIdx.x, k = 8 * (blockIdx.y * 64 + threadIdx.x);
-  if (row >= *count || k >= K) return;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const f32x4* const p = reinterpret_cast<const f32x4*>(parts + ((int64_t)s * M + row) * K + k);
-    const f32x4 lo = p[0], hi = p[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] += lo[e];
-      v[4 + e] += hi[e];
-    }
-  }
-  *reinterpret_cast<u32x4*>(dx + (int64_t)index[row] * K + k) = pack8(v);
+// dx: the splits' sums, rounded once, back in their rows; a workgroup 512 columns of a row
+__global__ __launch_bounds__(256) void ce_dx_kernel(const float* __restrict__ parts, int M, int K, int splits,
+                                                    const int32_t* __restrict__ index,
+                                                    const int32_t* __restrict__ count, uint16_t* __restrict__ dx) {
+  const int row = blockIdx.x, k = 8 * (blockIdx.y * 64 + (threadIdx.x & 63));
+  if (row >= *count) return;
+  float v[8];
+  tile_join(parts, (int64_t)row * K + k, (int64_t)M * K, splits, k < K, v);
+  if (threadIdx.x < 64 && k < K) *reinterpret_cast<u32x4*>(dx + (int64_t)index[row] * K + k) = pack8(v);
 }
 
 // db of a piece: column sums of dz, 64 columns a workgroup
@@ -355,7 +346,7 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
     }
   }
   if (dx == nullptr) return hipSuccess;
-  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M, (unsigned)((K + 511) / 512)), dim3(64), stream, (const float*)(ws + l.acc),
+  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M, (unsigned)((K + 511) / 512)), dim3(256), stream, (const float*)(ws + l.acc),
                        (int)M, (int)K, l.dx.splits, (const int32_t*)g.index, (const int32_t*)g.count,
                        (uint16_t*)dx);
 }
