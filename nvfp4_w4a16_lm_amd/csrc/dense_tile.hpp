@@ -136,6 +136,7 @@ struct TileCfg {
   static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;      // workgroups meant to share a compute unit
   static_assert(WN * WM == 4 && kLds <= 160 * 1024, "tile");
   static_assert(!I8 || (!PT && !QT), "int8 operands are straight");
+  static_assert((!PT || 512 % BN == 0) && (!QT || 512 % BM == 0), "a copy fills whole rows of a transposed tile");
   static_assert(kUnits ? BN >= BM : R >= 2 && R <= 4 && R * kCopies < 64, "ring");
 };
 
@@ -671,7 +672,8 @@ constexpr int kTileCus = 256;      // fixed, so that a workspace's size does not
 // for two of 128 x 128 (one's epilogue under the other's steps), or 0.65 and 6 where those have a compute
 // unit each.  4096 x 28672 over 64 steps: 740 us in 256 x 256, 890 in 128 x 128; 333 x 32003 over 33: 59, 52 (192 x 256),
 // 67; 333 x 11232 over 33: 46, 37, 32; 32003 x 2080 over 6: 76, 72, 67.
-inline TileSize tile_size(int64_t M, int64_t N, int64_t steps, int64_t splits) {
+// 192 rows are not for a transposed m side (`whole`), whose rows of 192 columns do not fill a copy.
+inline TileSize tile_size(int64_t M, int64_t N, int64_t steps, int64_t splits, bool whole = false) {
   if (M <= 32) return kTile32;
   if (M <= 64) return kTile64;
   const int64_t t256 = tile_count(kTile256, M, N) * splits, t128 = tile_count(kTile128, M, N) * splits;
@@ -680,7 +682,7 @@ inline TileSize tile_size(int64_t M, int64_t N, int64_t steps, int64_t splits) {
                                         : (double)((t128 + 2 * kTileCus - 1) / (2 * kTileCus)) * (1.0 * (double)steps + 2.5);
   const int64_t t192 = tile_count(kTile192, M, N) * splits;
   const double mid = (double)((t192 + kTileCus - 1) / kTileCus) * (1.0 * (double)steps + 7.0);
-  if (mid < big && mid < small) return kTile192;
+  if (!whole && mid < big && mid < small) return kTile192;
   return small < big ? kTile128 : kTile256;
 }
 
@@ -767,7 +769,8 @@ inline hipError_t launch_tile(const TileArgs& a, TileSize size, hipStream_t stre
     if (size == kTile64) return launch_tile_cfg<TileCfg<2, 1, 2, 2, PT, QT, EPI, 3>>(a, stream);
   }
   if (size <= kTile128) return launch_tile_cfg<TileCfg<2, 2, 2, 2, PT, QT, EPI, 0>>(a, stream);
-  if (size == kTile192) return launch_tile_cfg<TileCfg<4, 3, 2, 2, PT, QT, EPI, 0>>(a, stream);
+  if constexpr (!QT)
+    if (size == kTile192) return launch_tile_cfg<TileCfg<4, 3, 2, 2, PT, QT, EPI, 0>>(a, stream);
   return launch_tile_cfg<TileCfg<4, 4, 2, 2, PT, QT, EPI, 0>>(a, stream);
 }
 

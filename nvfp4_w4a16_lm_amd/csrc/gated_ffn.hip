@@ -94,7 +94,7 @@ static hipError_t gated_weight_grad(const void* q, int64_t M, const void* p, int
   a.k_split = (int)((K + 63) / 64 * 64);
   a.out = out;
   a.out_pitch = N;
-  return launch_tile<kTileBf16, true, true>(a, tile_size(M, N, (K + 63) / 64, 1), stream);
+  return launch_tile<kTileBf16, true, true>(a, tile_size(M, N, (K + 63) / 64, 1, true), stream);
 }
 
 hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I, void* h,

@@ -335,7 +335,7 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
       b.k_split = (int)((M + 63) / 64 * 64);
       b.out = (uint16_t*)dw + v0 * K;
       b.out_pitch = K;
-      e = launch_tile<kTileBf16, true, true>(b, tile_size(width, K, (M + 63) / 64, 1), stream);
+      e = launch_tile<kTileBf16, true, true>(b, tile_size(width, K, (M + 63) / 64, 1, true), stream);
       if (e != hipSuccess) return e;
     }
     if (db != nullptr) {

@@ -58,6 +58,12 @@ def test_sizes(t, h, i):
     check(t, h, i, seed=t + h + i)
 
 
+@pytest.mark.parametrize("t,h,i", [(333, 208, 11008), (333, 208, 22016), (700, 528, 8208), (1100, 2080, 2064), (450, 2080, 5616)])
+def test_wide_tiles(t, h, i):
+    """Sizes at which the widest tiles are taken: 192 and 256 rows, 256 of the weights' gradients."""
+    check(t, h, i, seed=t + i)
+
+
 @pytest.mark.parametrize("t", [1, 16, 100])
 def test_saturated_gates(t):
     """Gates of hundreds: the logistic function at 0 and 1, its exponential at infinity."""

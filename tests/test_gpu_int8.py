@@ -70,7 +70,7 @@ def check(m, n, k, seed, bias=False):
 @pytest.mark.parametrize("m,n,k", [
     (1, 1, 16), (1, 17, 48), (2, 255, 112), (3, 1003, 528), (7, 300, 2080), (15, 513, 256), (16, 64, 1040), (17, 257, 128),
     (31, 100, 144), (32, 515, 640), (33, 1003, 528), (64, 33, 272), (65, 300, 1040), (100, 257, 96), (128, 511, 384),
-    (129, 400, 528), (255, 129, 1040), (257, 515, 656), (520, 770, 144), (1, 4099, 8208), (5, 20011, 128)])
+    (333, 22003, 528), (700, 33000, 144), (2000, 9001, 656), (129, 400, 528), (255, 129, 1040), (257, 515, 656), (520, 770, 144), (1, 4099, 8208), (5, 20011, 128)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_sizes(m, n, k, bias):
     check(m, n, k, seed=m * 100 + n + k, bias=bias)

@@ -83,6 +83,12 @@ def test_sizes(m, v, k, full):
     check(make(m, v, k, seed=m + v + k, bias=full, gone=0.3 if full else 0.0), dlse=full)
 
 
+@pytest.mark.parametrize("m,v,k", [(333, 22003, 208), (700, 30003, 272), (400, 8000, 4096), (1100, 9000, 144)])
+def test_wide_tiles(m, v, k):
+    """Sizes at which the widest tiles are taken: 192 and 256 rows of logits, 256 of the weight's gradient."""
+    check(make(m, v, k, seed=m, gone=0.1))
+
+
 def test_several_pieces():
     """Enough rows that the vocabulary is taken in pieces, the last one ragged."""
     m, v, k = 40000, 4003, 32
