@@ -29,12 +29,12 @@ from nvfp4_w4a16_lm_amd import binding as B  # noqa: E402
 
 def gradients(x, w13, w2, head, targets, dloss):
     """Loss and gradients of block, residual and head; everything stays on the device and the stream."""
-    y, h = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
     hidden = x + y
     ce = B.nvfp4_linear_ce(hidden, head, targets)
     dhidden, dhead, _ = B.nvfp4_linear_ce_backward(hidden, head, targets, ce.stats, dloss)
-    dx, dw13, dw2 = B.nvfp4_gated_ffn_backward(x, h, w13, w2, dhidden)
-    return dict(hidden=hidden, h=h, ce=ce, dhidden=dhidden, dhead=dhead, dx=dhidden + dx, dw13=dw13, dw2=dw2)
+    dx, dw13, dw2 = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dhidden)
+    return dict(hidden=hidden, kept=kept, ce=ce, dhidden=dhidden, dhead=dhead, dx=dhidden + dx, dw13=dw13, dw2=dw2)
 
 
 def served(hidden, head, nvfp4_copy, targets):

@@ -608,16 +608,16 @@ nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const
  * Gated feed-forward block on bf16 weights: the dense block beside the expert
  * layer, with the experts' layout of w13 (rows [w1; w3]).
  *   [g, u] = x w13^T,  a = silu(g) * u,  y = bf16_rne(a w2^T)
- * float32 sums; a enters its product rounded to bf16.  h, where given, receives [g, u, a]
- * rounded to bf16 for the backward pass:
+ * float32 sums; a enters its product rounded to bf16.  h and act, where given, receive
+ * [g, u] in float32 and the rounded a for the backward pass:
  *   da = dy w2,  dg = da * u * silu'(g),  du = da * silu(g)
  *   dx = [dg, du] w13,  dw13 = [dg, du]^T x,  dw2 = dy^T a
- * with g, u and a from h, and dg and du rounded to bf16 as operands of the products.
+ * with g and u from h and a from act, and dg and du rounded to bf16 as operands of the products.
  *
  *   x          in  bf16 [T, H]; 0 <= T <= 2^22 (T == 0 enqueues nothing: dw13 and dw2 stay as they
  *                  are)
  *   w13, w2    in  bf16 [2 I, H], [H, I]; H and I multiples of 16, H <= 2^20, I <= 2^19, I * H <= 0x38000000
- *   h          out (forward, or NULL) / in (backward)  bf16 [T, 3 I]
+ *   h, act     out (forward, both or neither NULL) / in (backward)  float [T, 2 I], bf16 [T, I]
  *   dy         in  bf16 [T, H]
  *   workspace  tmp nvfp4_gated_ffn_workspace_bytes(T, H, I, backward) bytes; its contents need no
  *                  preparation, and the two calls may share one of the larger size
@@ -627,10 +627,10 @@ nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const
  */
 int64_t nvfp4_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, int backward);
 nvfp4_status nvfp4_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I,
-                             void* h, void* workspace, void* y, void* stream);
-nvfp4_status nvfp4_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
-                                      const void* w2, int64_t I, const void* dy, void* workspace, void* dx,
-                                      void* dw13, void* dw2, void* stream);
+                             float* h, void* act, void* workspace, void* y, void* stream);
+nvfp4_status nvfp4_gated_ffn_backward(const void* x, int64_t T, int64_t H, const float* h, const void* act,
+                                      const void* w13, const void* w2, int64_t I, const void* dy, void* workspace,
+                                      void* dx, void* dw13, void* dw2, void* stream);
 
 /* Host-side helpers (no device work). */
 const char* nvfp4_status_string(int status);   /* static string for a status code        */

@@ -152,9 +152,9 @@ def load_library() -> ctypes.CDLL:
     lib.nvfp4_linear_ce.restype = ctypes.c_int
     lib.nvfp4_linear_ce_backward.argtypes = [vp, i64, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.nvfp4_linear_ce_backward.restype = ctypes.c_int
-    lib.nvfp4_gated_ffn.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp]
+    lib.nvfp4_gated_ffn.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp]
     lib.nvfp4_gated_ffn.restype = ctypes.c_int
-    lib.nvfp4_gated_ffn_backward.argtypes = [vp, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]
+    lib.nvfp4_gated_ffn_backward.argtypes = [vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp]
     lib.nvfp4_gated_ffn_backward.restype = ctypes.c_int
     lib.nvfp4_status_string.argtypes = [ctypes.c_int]
     lib.nvfp4_status_string.restype = ctypes.c_char_p
@@ -211,8 +211,12 @@ def _on_its_stream(fn):
         caller = torch.cuda.current_stream(device)
         with torch.cuda.stream(_torch_stream(stream, device)):
             result = fn(*args, **kwargs)
-        for t in (result if isinstance(result, tuple) else (result,)):
-            if t is not None:
+        held = [result]
+        while held:
+            t = held.pop()
+            if isinstance(t, tuple):
+                held.extend(t)
+            elif t is not None:
                 t.record_stream(caller)
         return result
     return call
@@ -1011,6 +1015,12 @@ def nvfp4_linear_ce_backward(x: torch.Tensor, weight: torch.Tensor, targets: tor
 # Gated feed-forward block
 # ---------------------------------------------------------------------------
 
+class GatedKept(NamedTuple):
+    """What nvfp4_gated_ffn keeps for its backward pass."""
+    h: torch.Tensor         # float32 [T, 2 I]: gate and up projections
+    act: torch.Tensor       # bfloat16 [T, I]: their activation and product
+
+
 def gated_ffn_workspace(t: int, h: int, i: int, device, backward: bool = True) -> torch.Tensor:
     """Workspace of nvfp4_gated_ffn, and with ``backward`` of nvfp4_gated_ffn_backward too, to be kept."""
     need = int(load_library().nvfp4_gated_ffn_workspace_bytes(t, h, i, int(backward)))
@@ -1033,29 +1043,30 @@ def _check_gated_ffn(x, w13, w2):
 def nvfp4_gated_ffn(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, keep_h: bool = False,
                     workspace: torch.Tensor | None = None, stream=None):
     """The gated block: bf16 x [T, H], w13 [2 I, H] (rows [w1; w3]), w2 [H, I] -> bf16 y [T, H] =
-    (silu(x w1^T) * (x w3^T)) w2^T; with ``keep_h`` (y, h), h = bf16 [T, 3 I] for the backward pass (gate, up, activation)."""
+    (silu(x w1^T) * (x w3^T)) w2^T; with ``keep_h`` (y, GatedKept for the backward pass)."""
     x, w13, w2, t, hdim, i, dev = _check_gated_ffn(x, w13, w2)
     lib = load_library()
     need = int(lib.nvfp4_gated_ffn_workspace_bytes(t, hdim, i, 0))
     workspace = _workspace(need, workspace, dev, "nvfp4_gated_ffn", f"T={t}, H={hdim}, I={i}")
     y = torch.empty((t, hdim), dtype=torch.bfloat16, device=dev)
-    h = torch.empty((t, 3 * i), dtype=torch.bfloat16, device=dev) if keep_h else None
+    kept = GatedKept(torch.empty((t, 2 * i), dtype=torch.float32, device=dev),
+                     torch.empty((t, i), dtype=torch.bfloat16, device=dev)) if keep_h else (None, None)
     _check("nvfp4_gated_ffn",
-           lib.nvfp4_gated_ffn(_ptr(x), t, hdim, _ptr(w13), _ptr(w2), i, _ptr(h), _ptr(workspace), _ptr(y),
+           lib.nvfp4_gated_ffn(_ptr(x), t, hdim, _ptr(w13), _ptr(w2), i, *map(_ptr, kept), _ptr(workspace), _ptr(y),
                                _stream_of(x, stream)))
-    return (y, h) if keep_h else y
+    return (y, kept) if keep_h else y
 
 
 @_on_its_stream
-def nvfp4_gated_ffn_backward(x: torch.Tensor, h: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, dy: torch.Tensor,
+def nvfp4_gated_ffn_backward(x: torch.Tensor, kept: GatedKept, w13: torch.Tensor, w2: torch.Tensor, dy: torch.Tensor,
                              workspace: torch.Tensor | None = None, stream=None):
     """Gradients of nvfp4_gated_ffn: (dx [T, H], dw13 [2 I, H], dw2 [H, I]), all bfloat16, from dy
-    [T, H] and the h that the forward pass kept."""
+    [T, H] and what the forward pass kept."""
     x, w13, w2, t, hdim, i, dev = _check_gated_ffn(x, w13, w2)
     dy = _as_bf16_2d(dy, "dy")
-    h = _as_bf16_2d(h, "h")
     _check_out(dy, (t, hdim), (torch.bfloat16,), dev, "dy")
-    _check_out(h, (t, 3 * i), (torch.bfloat16,), dev, "h")
+    _check_out(kept.h, (t, 2 * i), (torch.float32,), dev, "kept.h")
+    _check_out(kept.act, (t, i), (torch.bfloat16,), dev, "kept.act")
     lib = load_library()
     need = int(lib.nvfp4_gated_ffn_workspace_bytes(t, hdim, i, 1))
     workspace = _workspace(need, workspace, dev, "nvfp4_gated_ffn_backward", f"T={t}, H={hdim}, I={i}")
@@ -1064,6 +1075,7 @@ def nvfp4_gated_ffn_backward(x: torch.Tensor, h: torch.Tensor, w13: torch.Tensor
     dw13 = make((2 * i, hdim), dtype=torch.bfloat16, device=dev)
     dw2 = make((hdim, i), dtype=torch.bfloat16, device=dev)
     _check("nvfp4_gated_ffn_backward",
-           lib.nvfp4_gated_ffn_backward(_ptr(x), t, hdim, _ptr(h), _ptr(w13), _ptr(w2), i, _ptr(dy), _ptr(workspace),
-                                        _ptr(dx), _ptr(dw13), _ptr(dw2), _stream_of(x, stream)))
+           lib.nvfp4_gated_ffn_backward(_ptr(x), t, hdim, _ptr(kept.h), _ptr(kept.act), _ptr(w13), _ptr(w2), i,
+                                        _ptr(dy), _ptr(workspace), _ptr(dx), _ptr(dw13), _ptr(dw2),
+                                        _stream_of(x, stream)))
     return dx, dw13, dw2

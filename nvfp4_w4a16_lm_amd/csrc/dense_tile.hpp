@@ -42,7 +42,7 @@ enum TileEpilogue : int {
   kTileBf16,        // out bf16 [m][n]
   kTileF32,         // out float [split][m][n], added to what is there if accumulate
   kTileInt8,        // out bf16 [m][n] = acc * sx[m] * sw[n] + bias[n]
-  kTileGated,       // P = [gate; up]: out a = silu(g) u, optionally h = [g, u, .]
+  kTileGated,       // P = [gate; up]: out a = silu(g) u, optionally h = [g, u] in float32
   kTileGatedBack,   // acc = da: dh = [da u silu'(g), da silu(g)], from h
   kTileCeStats,     // per (m, tile of n): maximum and sum of exp, and the target's logit
   kTileCeGrad       // out bf16 [m][n] = gradient of the logits
@@ -66,7 +66,7 @@ struct TileArgs {
   const float* sw;
   const uint16_t* bias;      // [n]
   int32_t I;                 // gated: width of a half
-  uint16_t* h;               // gated: [m][3 I], its first 2 I written (forward, may be NULL) or read (backward)
+  float* h;                  // gated: [m][2 I], written (forward, may be NULL) or read (backward)
   uint16_t* dh;              // gated backward [m][2 I]
   const int32_t* tok;        // [m] target of each row
   float2* parts;             // [m][part_pitch]
@@ -126,11 +126,12 @@ struct TileCfg {
   static constexpr int kRingBytes = kUnits ? 5 * kPBytes : R * kBuf;
   static constexpr int p_at(int ph) { return kUnits ? 2 * ph % 5 * kPBytes : ph * kBuf; }
   static constexpr int q_at(int ph) { return kUnits ? (2 * ph + 1) % 5 * kPBytes : ph * kBuf + kPBytes; }
-  // epilogue: rows in float32, 32 of each wavefront at a time, or bf16 outputs, all of them (gated: h beside them, half)
+  // epilogue: rows in float32, 32 of each wavefront at a time, or bf16 outputs, all of them (gated: 32, with g and u
+  // in float32 before them)
   static constexpr bool kStageF32 = EPI == kTileF32 || EPI == kTileGatedBack;
   static constexpr int kStageRows = 32 * WM, kStagePitch = BN + 4;
-  static constexpr int kStageJ = EPI == kTileGated && JT > 1 ? JT / 2 : JT;
-  static constexpr int kOutPitch = (EPI == kTileGated ? BN / 2 * 3 : BN) + 8;
+  static constexpr int kStageJ = EPI == kTileGated ? 1 : JT;
+  static constexpr int kOutPitch = (EPI == kTileGated ? BN / 2 * 5 : BN) + 8;   // in bf16
   static constexpr int kStage = kStageF32 ? kStageRows * kStagePitch * 4 : 32 * kStageJ * WM * kOutPitch * 2;
   static constexpr int kLds = kRingBytes > kStage ? kRingBytes : kStage;
   static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;      // workgroups meant to share a compute unit
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
     const int c = tid % kChunks, n = n0 + 8 * c;
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
-      u32x4 in[kIters][2];
+      f32x4 in[kIters][C::EPI == kTileF32 ? 2 : 4];
       int64_t at[kIters];
       bool on[kIters];
 #pragma unroll
@@ -475,14 +476,17 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         if constexpr (C::EPI == kTileF32) {
           at[it] = ((int64_t)split * a.M + m) * a.out_pitch + n;
           if (on[it] && a.accumulate) {
-            in[it][0] = *reinterpret_cast<const u32x4*>((const float*)a.out + at[it]);
-            in[it][1] = *reinterpret_cast<const u32x4*>((const float*)a.out + at[it] + 4);
+            in[it][0] = *reinterpret_cast<const f32x4*>((const float*)a.out + at[it]);
+            in[it][1] = *reinterpret_cast<const f32x4*>((const float*)a.out + at[it] + 4);
           }
         } else {
           at[it] = m;
           if (on[it]) {
-            in[it][0] = *reinterpret_cast<const u32x4*>(a.h + (int64_t)m * 3 * a.I + n);
-            in[it][1] = *reinterpret_cast<const u32x4*>(a.h + (int64_t)m * 3 * a.I + a.I + n);
+            const float* const hp = a.h + (int64_t)m * 2 * a.I + n;
+            in[it][0] = *reinterpret_cast<const f32x4*>(hp);
+            in[it][1] = *reinterpret_cast<const f32x4*>(hp + 4);
+            in[it][2] = *reinterpret_cast<const f32x4*>(hp + a.I);
+            in[it][3] = *reinterpret_cast<const f32x4*>(hp + a.I + 4);
           }
         }
       }
@@ -505,21 +509,19 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         if (!on[it]) continue;
         if constexpr (C::EPI == kTileF32) {
           if (a.accumulate) {
-            lo += __builtin_bit_cast(f32x4, in[it][0]);
-            hi += __builtin_bit_cast(f32x4, in[it][1]);
+            lo += in[it][0];
+            hi += in[it][1];
           }
           *reinterpret_cast<f32x4*>((float*)a.out + at[it]) = lo;
           *reinterpret_cast<f32x4*>((float*)a.out + at[it] + 4) = hi;
         } else {
-          float g[8], u[8], dg[8], du[8];
-          unpack8(in[it][0], g);
-          unpack8(in[it][1], u);
+          float dg[8], du[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float v = e < 4 ? lo[e & 3] : hi[e & 3];
-            const float s = sigmoid_fast(g[e]), gs = g[e] * s;
+            const float v = e < 4 ? lo[e & 3] : hi[e & 3], g = in[it][e >> 2][e & 3], u = in[it][2 + (e >> 2)][e & 3];
+            const float s = sigmoid_fast(g), gs = g * s;
             du[e] = v * gs;
-            dg[e] = v * u[e] * (s + gs * (1.0f - s));
+            dg[e] = v * u * (s + gs * (1.0f - s));
           }
           *reinterpret_cast<u32x4*>(a.dh + at[it] * 2 * a.I + n) = pack8(dg);
           *reinterpret_cast<u32x4*>(a.dh + at[it] * 2 * a.I + a.I + n) = pack8(du);
@@ -560,17 +562,18 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int at = 32 * (IT / 2 * wn + i) + 8 * q + 4 * h;
-              float g[4], u[4], o[4];
+              f32x4 g, u;
+              float o[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 g[e] = acc[i][j][4 * q + e];
                 u[e] = acc[i + IT / 2][j][4 * q + e];
                 o[e] = g[e] * sigmoid_fast(g[e]) * u[e];
               }
-              *reinterpret_cast<uint2*>(to + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+              *reinterpret_cast<uint2*>(to + 4 * kW + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
               if (a.h != nullptr) {
-                *reinterpret_cast<uint2*>(to + kW + at) = make_uint2(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]));
-                *reinterpret_cast<uint2*>(to + 2 * kW + at) = make_uint2(pack_bf16(u[0], u[1]), pack_bf16(u[2], u[3]));
+                *reinterpret_cast<f32x4*>((float*)to + at) = g;
+                *reinterpret_cast<f32x4*>((float*)to + kW + at) = u;
               }
             }
         } else {
@@ -620,9 +623,9 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         const int row = tid / kChunks + it * (kTileThreads / kChunks);
         const int m = m0 + 32 * (JT * (row / (32 * kJP)) + j0) + row % (32 * kJP);
         if (m >= M) continue;
-        const u32x4* const src = reinterpret_cast<const u32x4*>(stage + row * C::kOutPitch + 8 * c);
+        const uint16_t* const from = stage + row * C::kOutPitch;
         uint16_t* const o = (uint16_t*)a.out + (int64_t)m * a.out_pitch + n;
-        u32x4 w = src[0];
+        u32x4 w = *reinterpret_cast<const u32x4*>(from + (C::EPI == kTileGated ? 4 * kW : 0) + 8 * c);
         if constexpr (C::EPI == kTileCeGrad) {                   // columns past the vocabulary: zero operands
           if (n + 8 > a.N) {
 #pragma unroll
@@ -640,9 +643,12 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         }
         if constexpr (C::EPI == kTileGated) {
           if (a.h != nullptr) {
-            uint16_t* const hp = a.h + (int64_t)m * 3 * a.I + n;
-            *reinterpret_cast<u32x4*>(hp) = src[kChunks];
-            *reinterpret_cast<u32x4*>(hp + a.I) = src[2 * kChunks];
+            float* const hp = a.h + (int64_t)m * 2 * a.I + n;
+            const f32x4* const src = reinterpret_cast<const f32x4*>((const float*)from + 8 * c);
+            *reinterpret_cast<f32x4*>(hp) = src[0];
+            *reinterpret_cast<f32x4*>(hp + 4) = src[1];
+            *reinterpret_cast<f32x4*>(hp + a.I) = src[kW / 4];
+            *reinterpret_cast<f32x4*>(hp + a.I + 4) = src[kW / 4 + 1];
           }
         }
       }

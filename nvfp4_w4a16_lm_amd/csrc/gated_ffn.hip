@@ -7,9 +7,10 @@
 // Forward: both projections, the activation and the product are one kernel
 // whose tile holds matching rows of the gate and the up projection; the
 // activation enters the down projection rounded to bf16.  Kept for the
-// backward pass: h = [g, u, a] in bf16 (a is an operand of dW2; made again from
-// the rounded g and u it would be off by two roundings more).  Backward: the
-// kernel of da = dy W2 ends in [dg, du], in bf16; then three products.
+// backward pass: h = [g, u] in float32 and a in bf16, as the operand of dW2 that it
+// is.  (With h in bf16 the gradients of x and W13 are off by 0.0030 of their norm instead
+// of 0.0024, where one rounding of the result is 0.0017; the step is 2 % faster.)  Backward:
+// the kernel of da = dy W2 ends in [dg, du], in bf16 as operands; then three products.
 #include "dense_tile.hpp"
 
 namespace nvfp4 {
@@ -51,13 +52,13 @@ int64_t gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, bool backward
 
 // out bf16 [M, N] = q [M, K] p^T or q p (PT), K split where the tiles are few
 template <bool PT>
-static hipError_t gated_product(const void* q, int64_t q_pitch, const void* p, int64_t M, int64_t N, int64_t K, void* out,
+static hipError_t gated_product(const void* q, const void* p, int64_t M, int64_t N, int64_t K, void* out,
                                 float* parts, hipStream_t stream) {
   TileArgs a = {};
   a.p = (const uint8_t*)p;
   a.q = (const uint8_t*)q;
   a.p_pitch = 2 * (PT ? N : K);
-  a.q_pitch = 2 * q_pitch;
+  a.q_pitch = 2 * K;
   a.p_rows = PT ? K : N;
   a.q_rows = M;
   a.M = (int)M;
@@ -79,12 +80,12 @@ static hipError_t gated_product(const void* q, int64_t q_pitch, const void* p, i
 }
 
 // out bf16 [M, N] = q^T p, q [K, M], p [K, N]
-static hipError_t gated_weight_grad(const void* q, int64_t M, const void* p, int64_t p_pitch, int64_t N, int64_t K,
-                                    void* out, hipStream_t stream) {
+static hipError_t gated_weight_grad(const void* q, int64_t M, const void* p, int64_t N, int64_t K, void* out,
+                                    hipStream_t stream) {
   TileArgs a = {};
   a.p = (const uint8_t*)p;
   a.q = (const uint8_t*)q;
-  a.p_pitch = 2 * p_pitch;
+  a.p_pitch = 2 * N;
   a.q_pitch = 2 * M;
   a.p_rows = a.q_rows = K;
   a.M = (int)M;
@@ -97,8 +98,8 @@ static hipError_t gated_weight_grad(const void* q, int64_t M, const void* p, int
   return launch_tile<kTileBf16, true, true>(a, tile_size(M, N, (K + 63) / 64, 1, true), stream);
 }
 
-hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I, void* h,
-                            void* workspace, void* y, hipStream_t stream) {
+hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I,
+                            float* h, void* act, void* workspace, void* y, hipStream_t stream) {
   const GatedLayout l = gated_layout(T, H, I, false);
   uint8_t* const ws = (uint8_t*)workspace;
   TileArgs a = {};
@@ -113,17 +114,17 @@ hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13
   a.K = (int)H;
   a.splits = 1;
   a.k_split = (int)((H + 63) / 64 * 64);
-  a.out = h == nullptr ? (void*)ws : (void*)((uint16_t*)h + 2 * I);
-  a.out_pitch = h == nullptr ? I : 3 * I;
-  a.h = (uint16_t*)h;
+  a.out = act == nullptr ? ws : act;
+  a.out_pitch = I;
+  a.h = h;
   const hipError_t e = launch_tile<kTileGated, false, false>(a, tile_size(T, 2 * I, (H + 63) / 64, 1), stream);
   if (e != hipSuccess) return e;
-  return gated_product<false>(a.out, a.out_pitch, w2, T, H, I, y, (float*)(ws + l.parts), stream);
+  return gated_product<false>(a.out, w2, T, H, I, y, (float*)(ws + l.parts), stream);
 }
 
-hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
-                                     const void* w2, int64_t I, const void* dy, void* workspace, void* dx, void* dw13,
-                                     void* dw2, hipStream_t stream) {
+hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const float* h, const void* act,
+                                     const void* w13, const void* w2, int64_t I, const void* dy, void* workspace,
+                                     void* dx, void* dw13, void* dw2, hipStream_t stream) {
   const GatedLayout l = gated_layout(T, H, I, true);
   uint8_t* const ws = (uint8_t*)workspace;
   TileArgs a = {};
@@ -139,19 +140,19 @@ hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const 
   a.K = (int)H;
   a.splits = 1;
   a.k_split = (int)((H + 63) / 64 * 64);
-  a.h = (uint16_t*)const_cast<void*>(h);
+  a.h = const_cast<float*>(h);
   a.dh = (uint16_t*)ws;
   hipError_t e = launch_tile<kTileGatedBack, true, false>(a, tile_size(T, I, (H + 63) / 64, 1), stream);
   if (e != hipSuccess) return e;
   if (dw2 != nullptr) {
-    e = gated_weight_grad(dy, H, (const uint16_t*)h + 2 * I, 3 * I, I, T, dw2, stream);
+    e = gated_weight_grad(dy, H, act, I, T, dw2, stream);
     if (e != hipSuccess) return e;
   }
   if (dx != nullptr) {
-    e = gated_product<true>(ws, 2 * I, w13, T, H, 2 * I, dx, (float*)(ws + l.parts), stream);
+    e = gated_product<true>(ws, w13, T, H, 2 * I, dx, (float*)(ws + l.parts), stream);
     if (e != hipSuccess) return e;
   }
-  return dw13 == nullptr ? hipSuccess : gated_weight_grad(ws, 2 * I, x, H, H, T, dw13, stream);
+  return dw13 == nullptr ? hipSuccess : gated_weight_grad(ws, 2 * I, x, H, T, dw13, stream);
 }
 
 }  // namespace nvfp4

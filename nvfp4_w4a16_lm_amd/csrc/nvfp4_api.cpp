@@ -772,40 +772,40 @@ int64_t nvfp4_gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, int bac
 }
 
 nvfp4_status nvfp4_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I,
-                             void* h, void* workspace, void* y, void* stream) {
-  if (!w13 || !w2 || (T != 0 && (!x || !workspace || !y))) return NVFP4_ERR_NULL;
+                             float* h, void* act, void* workspace, void* y, void* stream) {
+  if (!w13 || !w2 || (T != 0 && (!x || !workspace || !y || !h != !act))) return NVFP4_ERR_NULL;
   const nvfp4_status s = check_gated_ffn(T, H, I);
   if (s != NVFP4_OK) return s;
   if (T == 0) return NVFP4_OK;
-  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(h, 16) || !aligned(workspace, 16) ||
-      !aligned(y, 16))
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(h, 16) || !aligned(act, 16) ||
+      !aligned(workspace, 16) || !aligned(y, 16))
     return NVFP4_ERR_ALIGN;
   const Range outs[] = {span(workspace, nvfp4::gated_ffn_workspace_bytes(T, H, I, false)),
-                        optional_span(h, T * I * 6), span(y, T * H * 2)};
+                        optional_span(h, T * I * 8), optional_span(act, T * I * 2), span(y, T * H * 2)};
   const Range ins[] = {span(x, T * H * 2), span(w13, I * H * 4), span(w2, I * H * 2)};
-  if (any_overlap(outs, 3, ins, 3)) return NVFP4_ERR_ALIAS;
+  if (any_overlap(outs, 4, ins, 3)) return NVFP4_ERR_ALIAS;
   g_last_hip_error[0] = '\0';
-  return finish(nvfp4::launch_gated_ffn(x, T, H, w13, w2, I, h, workspace, y, (hipStream_t)stream));
+  return finish(nvfp4::launch_gated_ffn(x, T, H, w13, w2, I, h, act, workspace, y, (hipStream_t)stream));
 }
 
-nvfp4_status nvfp4_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
-                                      const void* w2, int64_t I, const void* dy, void* workspace, void* dx,
-                                      void* dw13, void* dw2, void* stream) {
-  if (T != 0 && (!x || !h || !w13 || !w2 || !dy || !workspace)) return NVFP4_ERR_NULL;
+nvfp4_status nvfp4_gated_ffn_backward(const void* x, int64_t T, int64_t H, const float* h, const void* act,
+                                      const void* w13, const void* w2, int64_t I, const void* dy, void* workspace,
+                                      void* dx, void* dw13, void* dw2, void* stream) {
+  if (T != 0 && (!x || !h || !act || !w13 || !w2 || !dy || !workspace)) return NVFP4_ERR_NULL;
   const nvfp4_status s = check_gated_ffn(T, H, I);
   if (s != NVFP4_OK) return s;
   if (T == 0) return NVFP4_OK;
-  if (!aligned(x, 16) || !aligned(h, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(dy, 16) ||
-      !aligned(workspace, 16) || !aligned(dx, 16) || !aligned(dw13, 16) || !aligned(dw2, 16))
+  if (!aligned(x, 16) || !aligned(h, 16) || !aligned(act, 16) || !aligned(w13, 16) || !aligned(w2, 16) ||
+      !aligned(dy, 16) || !aligned(workspace, 16) || !aligned(dx, 16) || !aligned(dw13, 16) || !aligned(dw2, 16))
     return NVFP4_ERR_ALIGN;
   const Range outs[] = {span(workspace, nvfp4::gated_ffn_workspace_bytes(T, H, I, true)),
                         optional_span(dx, T * H * 2), optional_span(dw13, I * H * 4), optional_span(dw2, I * H * 2)};
-  const Range ins[] = {span(x, T * H * 2), span(h, T * I * 6), span(w13, I * H * 4), span(w2, I * H * 2),
-                       span(dy, T * H * 2)};
-  if (any_overlap(outs, 4, ins, 5)) return NVFP4_ERR_ALIAS;
+  const Range ins[] = {span(x, T * H * 2),   span(h, T * I * 8),  span(act, T * I * 2),
+                       span(w13, I * H * 4), span(w2, I * H * 2), span(dy, T * H * 2)};
+  if (any_overlap(outs, 4, ins, 6)) return NVFP4_ERR_ALIAS;
   if (!dx && !dw13 && !dw2) return NVFP4_OK;
   g_last_hip_error[0] = '\0';
-  return finish(nvfp4::launch_gated_ffn_backward(x, T, H, h, w13, w2, I, dy, workspace, dx, dw13, dw2,
+  return finish(nvfp4::launch_gated_ffn_backward(x, T, H, h, act, w13, w2, I, dy, workspace, dx, dw13, dw2,
                                                  (hipStream_t)stream));
 }
 

@@ -282,10 +282,10 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
 
 // Gated feed-forward block on bf16 weights (gated_ffn.hip).
 int64_t gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, bool backward);
-hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I, void* h,
-                            void* workspace, void* y, hipStream_t stream);
-hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const void* h, const void* w13,
-                                     const void* w2, int64_t I, const void* dy, void* workspace, void* dx, void* dw13,
-                                     void* dw2, hipStream_t stream);
+hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13, const void* w2, int64_t I,
+                            float* h, void* act, void* workspace, void* y, hipStream_t stream);
+hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const float* h, const void* act,
+                                     const void* w13, const void* w2, int64_t I, const void* dy, void* workspace,
+                                     void* dx, void* dw13, void* dw2, hipStream_t stream);
 
 }  // namespace nvfp4

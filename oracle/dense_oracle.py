@@ -154,7 +154,7 @@ def sigmoid(g):
 
 
 def gated_ffn(x, w13, w2):
-    """(y, h) and their bounds, h = [g, u, a]."""
+    """(y, h, a) and their bounds, h = [g, u] (float32) and a (bf16) as they are kept."""
     i = w2.shape[1]
     hu = x @ w13.T
     e = acc(x.shape[1]) * (np.abs(x) @ np.abs(w13).T)
@@ -168,15 +168,14 @@ def gated_ffn(x, w13, w2):
     ea = ea + HALF * (np.abs(a) + ea) + TINY
     y = a @ w2.T
     ey = ea @ np.abs(w2).T + acc(i, JOINS) * ((np.abs(a) + ea) @ np.abs(w2).T)
-    h, eh = np.concatenate((hu, a), 1), np.concatenate((e + HALF * (np.abs(hu) + e) + TINY, ea), 1)
-    return (y, h), (ey + HALF * (np.abs(y) + ey) + TINY, eh)
+    return (y, hu, a), (ey + HALF * (np.abs(y) + ey) + TINY, e + U * np.abs(hu) + TINY, ea)
 
 
-def gated_ffn_backward(x, h, w13, w2, dy):
-    """((dx, dw13, dw2), bounds) from the h that the forward pass kept, dg and du rounded to bf16 as operands."""
+def gated_ffn_backward(x, h, a, w13, w2, dy):
+    """((dx, dw13, dw2), bounds) from the h and a that the forward pass kept, dg and du rounded to bf16 as operands."""
     i = w2.shape[1]
     hd = w2.shape[0]
-    g, u, a = h[:, :i], h[:, i:2 * i], h[:, 2 * i:]
+    g, u = h[:, :i], h[:, i:]
     da = dy @ w2
     ed = acc(hd) * (np.abs(dy) @ np.abs(w2))
     s = sigmoid(g)

@@ -44,13 +44,14 @@ def ceb(**kw):
 
 
 def ffn(**kw):
-    a = dict(x=P[0], T=4, H=512, w13=P[1], w2=P[2], I=1024, h=P[3], ws=P[4], y=P[5])
+    a = dict(x=P[0], T=4, H=512, w13=P[1], w2=P[2], I=1024, h=P[3], act=P[6], ws=P[4], y=P[5])
     a.update(kw)
     return lib().nvfp4_gated_ffn(*a.values(), None)
 
 
 def ffnb(**kw):
-    a = dict(x=P[0], T=4, H=512, h=P[1], w13=P[2], w2=P[3], I=1024, dy=P[4], ws=P[5], dx=P[6], dw13=P[7], dw2=P[8])
+    a = dict(x=P[0], T=4, H=512, h=P[1], act=P[9], w13=P[2], w2=P[3], I=1024, dy=P[4], ws=P[5], dx=P[6], dw13=P[7],
+             dw2=P[8])
     a.update(kw)
     return lib().nvfp4_gated_ffn_backward(*a.values(), None)
 
@@ -106,21 +107,21 @@ def test_linear_ce_refusals():
 
 
 def test_gated_ffn_refusals():
-    for n in ("x", "w13", "w2", "ws", "y"):
+    for n in ("x", "w13", "w2", "ws", "y", "h", "act"):  # h and act: both or neither
         assert ffn(**{n: 0}) == ERR_NULL, n
-    for n in ("x", "h", "w13", "w2", "dy", "ws"):
+    for n in ("x", "h", "act", "w13", "w2", "dy", "ws"):
         assert ffnb(**{n: 0}) == ERR_NULL, n
     for kw in (dict(T=-1), dict(T=(1 << 22) + 1), dict(H=8), dict(H=520), dict(I=0), dict(I=24), dict(H=(1 << 20) + 16),
                dict(I=(1 << 19) + 16), dict(H=1 << 16, I=1 << 14)):
         assert ffn(**kw) == ERR_SHAPE and ffnb(**kw) == ERR_SHAPE, kw
-    for n in ("x", "w13", "w2", "h", "ws", "y"):
+    for n in ("x", "w13", "w2", "h", "act", "ws", "y"):
         assert ffn(**{n: P[11] + 8}) == ERR_ALIGN, n
-    for n in ("x", "h", "w13", "w2", "dy", "ws", "dx", "dw13", "dw2"):
+    for n in ("x", "h", "act", "w13", "w2", "dy", "ws", "dx", "dw13", "dw2"):
         assert ffnb(**{n: P[11] + 8}) == ERR_ALIGN, n
     assert ffn(y=P[0]) == ERR_ALIAS and ffn(h=P[1] + 2 * 1024 * 512 * 2 - 16) == ERR_ALIAS
-    assert ffn(ws=P[3] + 4 * 3072 * 2 - 16) == ERR_ALIAS
+    assert ffn(ws=P[3] + 4 * 2048 * 4 - 16) == ERR_ALIAS and ffn(act=P[3] + 64) == ERR_ALIAS
     assert ffnb(dx=P[4]) == ERR_ALIAS and ffnb(dw2=P[7] + 1024) == ERR_ALIAS and ffnb(dw13=P[1]) == ERR_ALIAS
-    assert ffn(T=0) == OK and ffn(T=0, x=0, h=0, ws=0, y=0) == OK and ffnb(T=0) == OK
+    assert ffn(T=0) == OK and ffn(T=0, x=0, h=0, act=0, ws=0, y=0) == OK and ffnb(T=0) == OK
     assert ffnb(dx=0, dw13=0, dw2=0) == OK
     size = lib().nvfp4_gated_ffn_workspace_bytes
     assert size(4, 512, 24, 0) == 0 and size(4, 512, 1024, -1) == 0 and size(0, 512, 1024, 0) >= 16
@@ -226,13 +227,13 @@ def test_linear_ce_with_masked_tokens():
 def test_gated_ffn_against_torch_and_differences():
     rng = np.random.default_rng(3)
     x, w13, w2, dy = bf16(rng, 5, 16), bf16(rng, 64, 16), bf16(rng, 16, 32), bf16(rng, 5, 16)
-    (y, h), _ = D.gated_ffn(x, w13, w2)
+    (y, h, a), _ = D.gated_ffn(x, w13, w2)
     tx, t13, t2 = (torch.from_numpy(a).requires_grad_() for a in (x, w13, w2))
     g, u = (tx @ t13.T).chunk(2, 1)
     ref = (torch.nn.functional.silu(g) * u) @ t2.T
-    assert np.allclose(y, ref.detach()) and np.allclose(h[:, :64], torch.cat((g, u), 1).detach())
+    assert np.allclose(y, ref.detach()) and np.allclose(h, torch.cat((g, u), 1).detach())
     (ref * torch.from_numpy(dy)).sum().backward()
-    grads, _ = D.gated_ffn_backward(x, h, w13, w2, dy)
+    grads, _ = D.gated_ffn_backward(x, h, a, w13, w2, dy)
     for a, b in zip(grads, (tx, t13, t2)):
         assert np.allclose(a, b.grad, atol=1e-12)
     f = lambda *a: (D.gated_ffn(*a)[0][0] * dy).sum()

@@ -39,12 +39,13 @@ def check(t, h, i, seed, gate=1.3):
     a = make(t, h, i, seed, gate)
     x, w13, w2, dy = (v.to(DEV) for v in a)
     y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
-    (wy, wh), (by, bh) = D.gated_ffn(*map(f64, a[:3]))
+    (wy, wh, wa), (by, bh, ba) = D.gated_ffn(*map(f64, a[:3]))
     within(y, wy, by, "y")
-    within(kept, wh, bh, "h")
+    within(kept.h, wh, bh, "h")
+    within(kept.act, wa, ba, "act")
     assert torch.equal(y, B.nvfp4_gated_ffn(x, w13, w2))
     grads = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy)
-    want, bounds = D.gated_ffn_backward(f64(x), f64(kept), f64(w13), f64(w2), f64(dy))
+    want, bounds = D.gated_ffn_backward(f64(x), f64(kept.h), f64(kept.act), f64(w13), f64(w2), f64(dy))
     for g, v, b, what in zip(grads, want, bounds, ("dx", "dw13", "dw2")):
         within(g, v, b, what)
     return (x, w13, w2, dy), kept, grads
@@ -79,16 +80,14 @@ def test_gradient_against_differences():
     a = make(20, 64, 96, seed=3)
     n = [f64(v) for v in a]
     (x, w13, w2, dy), kept, grads = check(20, 64, 96, seed=3)
-    # h is rounded between the passes: each of dg, du and a moves by its slope times that
+    # kept values are a little off between the passes: h by its sums, a by its rounding too
+    (_, h, act), (_, bh, ba) = D.gated_ffn(*n[:3])
     i = 96
-    g, u = (n[0] @ n[1].T)[:, :i], (n[0] @ n[1].T)[:, i:]
-    da = np.abs(n[3] @ n[2])
-    r = 2.0 ** -8 * 1.01
-    s = D.sigmoid(g)
-    slope = np.abs(s * (1 + g * (1 - s)))
-    e = np.concatenate((da * (np.abs(u) * 0.55 * np.abs(g) + np.abs(u) * slope) * r * 1.2, da * 1.2 * np.abs(g) * r), 1)
-    extra = (e @ np.abs(n[1]), e.T @ np.abs(n[0]), np.abs(n[3]).T @ (np.abs(g * s * u) * r))
-    _, bounds = D.gated_ffn_backward(n[0], f64(kept), n[1], n[2], n[3])
+    g, u, da, s = h[:, :i], h[:, i:], np.abs(n[3] @ n[2]), D.sigmoid(h[:, :i])
+    eg, eu = bh[:, :i], bh[:, i:]                        # |silu'| <= 1.1, |silu''| <= 0.5
+    e = 1.1 * np.concatenate((da * (1.1 * eu + 0.5 * np.abs(u) * eg), da * 1.1 * eg), 1)
+    extra = (e @ np.abs(n[1]), e.T @ np.abs(n[0]), np.abs(n[3]).T @ ba)
+    _, bounds = D.gated_ffn_backward(n[0], f64(kept.h), f64(kept.act), n[1], n[2], n[3])
     rng = np.random.default_rng(1)
     f = lambda *p: (D.gated_ffn(*p)[0][0] * n[3]).sum()
     for which, grad in enumerate(grads):
@@ -119,23 +118,25 @@ def test_buffers_are_written_exactly(t):
     want = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy)
     size = int(lib.nvfp4_gated_ffn_workspace_bytes(t, h, i, 1))
     ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device=DEV)
-    outs = [torch.full((n + 32,), 3.0, dtype=BF16, device=DEV) for n in (t * h, 3 * t * i, t * h, 2 * i * h, h * i)]
+    outs = [torch.full((n + 32,), 3.0, dtype=dt, device=DEV)
+            for n, dt in ((t * h, BF16), (2 * t * i, torch.float32), (t * i, BF16), (t * h, BF16), (2 * i * h, BF16),
+                          (h * i, BF16))]
     p = [o.data_ptr() for o in outs]
     s = torch.cuda.current_stream().cuda_stream
     xp, w13p, w2p, dyp = (v.data_ptr() for v in (x, w13, w2, dy))
-    assert lib.nvfp4_gated_ffn(xp, t, h, w13p, w2p, i, p[1], ws.data_ptr(), p[0], s) == 0
-    assert lib.nvfp4_gated_ffn_backward(xp, t, h, p[1], w13p, w2p, i, dyp, ws.data_ptr(), p[2], p[3], p[4], s) == 0
+    assert lib.nvfp4_gated_ffn(xp, t, h, w13p, w2p, i, p[1], p[2], ws.data_ptr(), p[0], s) == 0
+    assert lib.nvfp4_gated_ffn_backward(xp, t, h, p[1], p[2], w13p, w2p, i, dyp, ws.data_ptr(), *p[3:], s) == 0
     torch.cuda.synchronize()
-    for got, ref in zip(outs, (y, kept, *want)):
+    for got, ref in zip(outs, (y, *kept, *want)):
         assert torch.equal(got[:ref.numel()], ref.flatten()) and torch.all(got[ref.numel():] == 3.0)
     assert torch.all(ws[size:] == 0xFF)
     for keep in range(3):                                # each gradient alone
-        alone = [torch.full_like(o, 3.0) for o in outs[2:]]
+        alone = [torch.full_like(o, 3.0) for o in outs[3:]]
         a = [o.data_ptr() if j == keep else None for j, o in enumerate(alone)]
-        assert lib.nvfp4_gated_ffn_backward(xp, t, h, p[1], w13p, w2p, i, dyp, ws.data_ptr(), *a, s) == 0
+        assert lib.nvfp4_gated_ffn_backward(xp, t, h, p[1], p[2], w13p, w2p, i, dyp, ws.data_ptr(), *a, s) == 0
         torch.cuda.synchronize()
         for j, o in enumerate(alone):
-            assert torch.equal(o, outs[2 + j]) if j == keep else torch.all(o == 3.0)
+            assert torch.equal(o, outs[3 + j]) if j == keep else torch.all(o == 3.0)
 
 
 @pytest.mark.parametrize("t", [1, 16, 100, 300])
@@ -147,7 +148,7 @@ def test_graph_replays(t):
 
     def call():
         y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True, workspace=ws)
-        return (y, kept, *B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy, workspace=ws))
+        return (y, *kept, *B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy, workspace=ws))
     graph = capture(lambda: held.append(call()))
     rng = np.random.default_rng(t)
     for _ in range(3):
@@ -170,13 +171,13 @@ def test_given_stream_with_wide_input():
     y2, h2 = B.nvfp4_gated_ffn(wide(x), wide(w13), wide(w2), keep_h=True, stream=side)
     g2 = B.nvfp4_gated_ffn_backward(wide(x), h2, wide(w13), wide(w2), wide(dy), stream=side)
     side.synchronize()
-    assert all(torch.equal(a, b) for a, b in zip((y, kept, *want), (y2, h2, *g2)))
+    assert all(torch.equal(a, b) for a, b in zip((y, *kept, *want), (y2, *h2, *g2)))
 
 
 def test_empty_batch_and_refusals():
     x, w13, w2, dy = (v.to(DEV) for v in make(4, 32, 48, seed=9))
     y, kept = B.nvfp4_gated_ffn(x[:0], w13, w2, keep_h=True)
-    assert y.shape == (0, 32) and kept.shape == (0, 144)
+    assert y.shape == (0, 32) and kept.h.shape == (0, 96) and kept.act.shape == (0, 48)
     dx, d13, d2 = B.nvfp4_gated_ffn_backward(x[:0], kept, w13, w2, dy[:0])
     assert dx.shape == (0, 32) and not d13.any() and not d2.any()
     y, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
@@ -184,7 +185,7 @@ def test_empty_batch_and_refusals():
         with pytest.raises(ValueError):
             B.nvfp4_gated_ffn(*bad)
     with pytest.raises(ValueError):
-        B.nvfp4_gated_ffn_backward(x, kept[:, :96].contiguous(), w13, w2, dy)
+        B.nvfp4_gated_ffn_backward(x, B.GatedKept(kept.h.to(BF16), kept.act), w13, w2, dy)
     with pytest.raises(ValueError):
         B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy[:3])
     with pytest.raises(ValueError):

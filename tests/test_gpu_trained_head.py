@@ -47,8 +47,9 @@ def test_step_stage_by_stage(example, tokens, vocab, hidden, inner):
     t = a["targets"].cpu().numpy().astype(np.int64)
     rate = 0.25
     g, logits, scored = example.step(**a, rate=rate)
-    (y, h), (by, bh) = D.gated_ffn(w["x"], w["w13"], w["w2"])
-    within(g["h"], h, bh)
+    (y, h, act), (by, bh, ba) = D.gated_ffn(w["x"], w["w13"], w["w2"])
+    within(g["kept"].h, h, bh)
+    within(g["kept"].act, act, ba)
     total = w["x"] + y
     within(g["hidden"], total, by + D.HALF * (np.abs(total) + by))              # one more rounding: the residual's
     hid = f64(g["hidden"])
@@ -58,7 +59,8 @@ def test_step_stage_by_stage(example, tokens, vocab, hidden, inner):
     (dh, dw, _), (bdh, bdw, _) = D.linear_ce_backward(hid, w["head"], t, w["dloss"])
     within(g["dhidden"], dh, bdh)
     within(g["dhead"], dw, bdw)
-    (dx, d13, d2), (bx, b13, b2) = D.gated_ffn_backward(w["x"], f64(g["h"]), w["w13"], w["w2"], f64(g["dhidden"]))
+    (dx, d13, d2), (bx, b13, b2) = D.gated_ffn_backward(w["x"], f64(g["kept"].h), f64(g["kept"].act), w["w13"], w["w2"],
+                                                                f64(g["dhidden"]))
     within(g["dw13"], d13, b13)
     within(g["dw2"], d2, b2)
     sum_dx = f64(g["dhidden"]) + dx
