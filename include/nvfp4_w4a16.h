@@ -546,14 +546,14 @@ nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, i
  * nvfp4_int8_quantize_rows -- row-wise int8 quantization of a bf16 [R, K] matrix:
  *   scales[r] = max(fl32(amax_r / 127), 1e-12),  q = rne(127 a / amax_r) in [-127, 127]
  * The codes are those of the exact ratio (nearest, ties to even); in a row whose scale is 1e-12 they
- * are rne(fl32(a / scale)).  Non-finite values are outside the contract.  R == 0 enqueues nothing.
+ * are rne(fl32(a / scale)).  Non-finite values are outside the contract.  0 <= R <= 2^23 (0 enqueues nothing).
  * K as below; a and q 16-byte aligned.
  *
  * nvfp4_int8_gemm
  *   y[m, n] = bf16_rne( x_scales[m] * w_scales[n] * sum_k xq[m, k] * wq[n, k] + bias[n] )
  * The sum is exact (any int8 codes, -128 among them), scaling and bias are float32.
  *   xq       in  int8 [M, K], 16-byte aligned; 0 <= M <= 2^22 (M == 0 enqueues nothing)
- *   wq       in  int8 [N, K], 16-byte aligned; K % 16 == 0, 16 <= K < 2^17
+ *   wq       in  int8 [N, K], 16-byte aligned; K % 16 == 0, 16 <= K < 2^17; M * N <= 2^37
  *   x_scales, w_scales  in  float [M], [N]
  *   bias     in  bf16 [N] or NULL
  *   y        out bf16 [M, N], 16-byte aligned
@@ -586,7 +586,8 @@ nvfp4_status nvfp4_int8_gemm(const int8_t* xq, const float* x_scales, int64_t M,
  *
  *   x          in  bf16 [M, K], 16-byte aligned; 0 <= M <= 2^22 (M == 0 enqueues nothing: a
  *                  caller's dweight and dbias stay as they are)
- *   weight     in  bf16 [V, K], 16-byte aligned; K % 16 == 0, 16 <= K <= 2^20
+ *   weight     in  bf16 [V, K], 16-byte aligned; K % 16 == 0, 16 <= K <= 2^20; M * K, V * K and M * V
+ *                  at most 2^37
  *   bias       in  bf16 [V] or NULL
  *   targets    in  int32 [M]
  *   workspace  tmp nvfp4_linear_ce_workspace_bytes(M, V, K, backward) bytes, 16-byte aligned; its
@@ -616,7 +617,8 @@ nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const
  *
  *   x          in  bf16 [T, H]; 0 <= T <= 2^22 (T == 0 enqueues nothing: dw13 and dw2 stay as they
  *                  are)
- *   w13, w2    in  bf16 [2 I, H], [H, I]; H and I multiples of 16, H <= 2^20, I <= 2^19, I * H <= 0x38000000
+ *   w13, w2    in  bf16 [2 I, H], [H, I]; H and I multiples of 16, H <= 2^20, I <= 2^19, I * H <= 0x38000000;
+ *                  T * H and 2 T * I at most 2^37
  *   h, act     out (forward, both or neither NULL) / in (backward)  float [T, 2 I], bf16 [T, I]
  *   dy         in  bf16 [T, H]
  *   workspace  tmp nvfp4_gated_ffn_workspace_bytes(T, H, I, backward) bytes; its contents need no

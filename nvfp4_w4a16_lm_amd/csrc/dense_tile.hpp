@@ -634,7 +634,8 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
           }
         }
         if (whole) {
-          if constexpr (C::I8) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));
+          // logits and weight gradients are not read back here (32003 x 2080 of 333 tokens, whole step: 267 -> 254 us)
+          if constexpr (C::I8 || QT) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(o));
           else *reinterpret_cast<u32x4*>(o) = w;
         } else {
 #pragma unroll

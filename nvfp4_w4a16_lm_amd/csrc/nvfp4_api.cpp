@@ -657,20 +657,23 @@ namespace {
 
 constexpr int64_t kMaxDenseM = (int64_t)1 << 22;     // rows of the dense calls
 constexpr int64_t kMaxDenseK = (int64_t)1 << 20;     // bf16 row length: 32-bit offsets inside a tile
+constexpr int64_t kMaxDenseOut = (int64_t)1 << 37;   // elements of a product: fewer than 2^32 threads
+constexpr int64_t kMaxQuantRows = (int64_t)1 << 23;  // rows of the int8 quantizer: the same
 constexpr int64_t kMaxInt8K = ((int64_t)1 << 17) - 16;  // 128 * 128 * K < 2^31
 constexpr int64_t kMaxGated = 0x38000000;            // I * H: 32-bit offsets between gate and up rows
 
 bool dense_width(int64_t k, int64_t most) { return k >= NVFP4_GROUP && k % NVFP4_GROUP == 0 && k <= most; }
 
 nvfp4_status check_linear_ce(int64_t M, int64_t V, int64_t K) {
-  if (M < 0 || M > kMaxDenseM || V < 1 || V > kMaxDim || !dense_width(K, kMaxDenseK) || V * K > kMaxElems ||
-      M * K > kMaxElems || M * V > kMaxElems)
+  if (M < 0 || M > kMaxDenseM || V < 1 || V > kMaxDim || !dense_width(K, kMaxDenseK) || V * K > kMaxDenseOut ||
+      M * K > kMaxDenseOut || M * V > kMaxDenseOut)
     return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
 
 nvfp4_status check_gated_ffn(int64_t T, int64_t H, int64_t I) {
-  if (T < 0 || T > kMaxDenseM || !dense_width(H, kMaxDenseK) || !dense_width(I, kMaxDenseK / 2) || H * I > kMaxGated)
+  if (T < 0 || T > kMaxDenseM || !dense_width(H, kMaxDenseK) || !dense_width(I, kMaxDenseK / 2) || H * I > kMaxGated ||
+      T * H > kMaxDenseOut || 2 * T * I > kMaxDenseOut)
     return NVFP4_ERR_SHAPE;
   return NVFP4_OK;
 }
@@ -681,7 +684,7 @@ extern "C" {
 
 nvfp4_status nvfp4_int8_quantize_rows(const void* a, int64_t R, int64_t K, int8_t* q, float* scales, void* stream) {
   if (R != 0 && (!a || !q || !scales)) return NVFP4_ERR_NULL;
-  if (R < 0 || R > kMaxDim || !dense_width(K, kMaxInt8K) || R * K > kMaxElems) return NVFP4_ERR_SHAPE;
+  if (R < 0 || R > kMaxQuantRows || !dense_width(K, kMaxInt8K)) return NVFP4_ERR_SHAPE;
   if (R == 0) return NVFP4_OK;
   if (!aligned(a, 16) || !aligned(q, 16) || !aligned(scales, 4)) return NVFP4_ERR_ALIGN;
   const Range outs[] = {span(q, R * K), span(scales, R * 4)};
@@ -695,7 +698,7 @@ nvfp4_status nvfp4_int8_gemm(const int8_t* xq, const float* x_scales, int64_t M,
                              const float* w_scales, int64_t N, const void* bias, void* y, void* stream) {
   if (!wq || !w_scales || (M != 0 && (!xq || !x_scales || !y))) return NVFP4_ERR_NULL;
   if (M < 0 || M > kMaxDenseM || N < 1 || N > kMaxDim || !dense_width(K, kMaxInt8K) || N * K > kMaxElems ||
-      M * N > kMaxElems)
+      M * N > kMaxDenseOut)
     return NVFP4_ERR_SHAPE;
   if (M == 0) return NVFP4_OK;
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(bias, 2) ||

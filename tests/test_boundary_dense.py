@@ -59,7 +59,7 @@ def ffnb(**kw):
 def test_int8_refusals():
     for n in ("a", "q", "s"):
         assert quant(**{n: 0}) == ERR_NULL
-    for kw in (dict(R=-1), dict(K=0), dict(K=24), dict(K=1 << 17), dict(R=1 << 31)):
+    for kw in (dict(R=-1), dict(K=0), dict(K=24), dict(K=1 << 17), dict(R=(1 << 23) + 1)):
         assert quant(**kw) == ERR_SHAPE, kw
     assert quant(a=P[0] + 8) == ERR_ALIGN and quant(q=P[1] + 8) == ERR_ALIGN and quant(s=P[2] + 2) == ERR_ALIGN
     assert quant(q=P[0] + 4 * 512 * 2 - 16) == ERR_ALIAS and quant(s=P[1] + 4 * 512 - 4) == ERR_ALIAS
@@ -67,7 +67,7 @@ def test_int8_refusals():
     for n in ("xq", "sx", "wq", "sw", "y"):
         assert gemm(**{n: 0}) == ERR_NULL, n
     for kw in (dict(M=-1), dict(M=(1 << 22) + 1), dict(N=0), dict(K=8), dict(K=520), dict(K=1 << 17), dict(N=1 << 31),
-               dict(M=1 << 22, N=1 << 20)):
+               dict(M=1 << 22, N=1 << 16)):
         assert gemm(**kw) == ERR_SHAPE, kw
     for n in ("xq", "wq", "y"):
         assert gemm(**{n: P[7] + 8}) == ERR_ALIGN, n
@@ -85,7 +85,7 @@ def test_linear_ce_refusals():
     for n in ("x", "w", "t", "st", "dl", "ws"):
         assert ceb(**{n: 0}) == ERR_NULL, n
     for kw in (dict(M=-1), dict(M=(1 << 22) + 1), dict(V=0), dict(V=(1 << 30) + 1), dict(K=8), dict(K=520),
-               dict(K=(1 << 20) + 16), dict(V=1 << 30, K=1040), dict(M=1 << 22, V=1 << 19)):
+               dict(K=(1 << 20) + 16), dict(V=1 << 30, K=144), dict(M=1 << 22, V=(1 << 15) + 1), dict(M=1 << 22, K=1 << 16)):
         assert ce(**kw) == ERR_SHAPE and ceb(**kw) == ERR_SHAPE, kw
     for n in ("x", "w", "ws"):
         assert ce(**{n: P[11] + 8}) == ERR_ALIGN and ceb(**{n: P[11] + 8}) == ERR_ALIGN, n
@@ -112,7 +112,7 @@ def test_gated_ffn_refusals():
     for n in ("x", "h", "act", "w13", "w2", "dy", "ws"):
         assert ffnb(**{n: 0}) == ERR_NULL, n
     for kw in (dict(T=-1), dict(T=(1 << 22) + 1), dict(H=8), dict(H=520), dict(I=0), dict(I=24), dict(H=(1 << 20) + 16),
-               dict(I=(1 << 19) + 16), dict(H=1 << 16, I=1 << 14)):
+               dict(I=(1 << 19) + 16), dict(H=1 << 16, I=1 << 14), dict(T=1 << 22, H=1 << 16, I=16), dict(T=1 << 22, H=16, I=1 << 15)):
         assert ffn(**kw) == ERR_SHAPE and ffnb(**kw) == ERR_SHAPE, kw
     for n in ("x", "w13", "w2", "h", "act", "ws", "y"):
         assert ffn(**{n: P[11] + 8}) == ERR_ALIGN, n
