@@ -609,8 +609,9 @@ nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const
  * Gated feed-forward block on bf16 weights: the dense block beside the expert
  * layer, with the experts' layout of w13 (rows [w1; w3]).
  *   [g, u] = x w13^T,  a = silu(g) * u,  y = bf16_rne(a w2^T)
- * float32 sums; a enters its product rounded to bf16.  h and act, where given, receive
- * [g, u] in float32 and the rounded a for the backward pass:
+ * float32 sums; a enters its product rounded to bf16, for up to 16 tokens as a pair of bf16
+ * that keeps 16 bits of it.  h and act, where given, receive [g, u] in float32 and the
+ * a rounded to bf16 for the backward pass:
  *   da = dy w2,  dg = da * u * silu'(g),  du = da * silu(g)
  *   dx = [dg, du] w13,  dw13 = [dg, du]^T x,  dw2 = dy^T a
  * with g and u from h and a from act, and dg and du rounded to bf16 as operands of the products.

@@ -74,6 +74,8 @@ struct TileArgs {
   const float* sw;
   const uint16_t* bias;      // [n]
   int32_t I;                 // gated: width of a half
+  int32_t pair_rows;         // gated: where not 0, out row pair_rows + m receives what rounding took from row m
+  uint16_t* act;             // gated: the rounded a once more [m][I], or NULL
   float* h;                  // gated: [m][2 I], written (forward, may be NULL) or read (backward)
   uint16_t* dh;              // gated backward [m][2 I]
   const int32_t* tok;        // [m] target of each row
@@ -105,6 +107,8 @@ __device__ __forceinline__ void tile_copy16(__amdgpu_buffer_rsrc_t r, tile_lds_t
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {      // nearest even; NaN stays NaN
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2t));
 }
+// What rounding v to hi left over; nothing where hi is not finite (an infinity's product is the one of hi alone).
+__device__ __forceinline__ float rest_bf16(float v, float hi) { return fabsf(hi) < INFINITY ? v - hi : 0.0f; }
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
@@ -139,7 +143,7 @@ struct TileCfg {
   static constexpr bool kStageF32 = EPI == kTileF32 || EPI == kTileGatedBack;
   static constexpr int kStageRows = 32 * WM, kStagePitch = BN + 4;
   static constexpr int kStageJ = EPI == kTileGated ? 1 : JT;
-  static constexpr int kOutPitch = (EPI == kTileGated ? BN / 2 * 5 : BN) + 8;   // in bf16
+  static constexpr int kOutPitch = (EPI == kTileGated ? BN / 2 * 6 : BN) + 8;   // in bf16
   static constexpr int kStage = kStageF32 ? kStageRows * kStagePitch * 4 : 32 * kStageJ * WM * kOutPitch * 2;
   static constexpr int kLds = kRingBytes > kStage ? kRingBytes : kStage;
   static constexpr int kPerCu = kLds <= 80 * 1024 ? 2 : 1;      // workgroups meant to share a compute unit
@@ -578,7 +582,12 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
                 u[e] = acc[i + IT / 2][j][4 * q + e];
                 o[e] = g[e] * sigmoid_fast(g[e]) * u[e];
               }
-              *reinterpret_cast<uint2*>(to + 4 * kW + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+              const uint2 hi = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+              *reinterpret_cast<uint2*>(to + 4 * kW + at) = hi;
+              if (a.pair_rows != 0)
+                *reinterpret_cast<uint2*>(to + 5 * kW + at) =
+                    make_uint2(pack_bf16(rest_bf16(o[0], bf16_lo(hi.x)), rest_bf16(o[1], bf16_hi(hi.x))),
+                               pack_bf16(rest_bf16(o[2], bf16_lo(hi.y)), rest_bf16(o[3], bf16_hi(hi.y))));
               if (a.h != nullptr) {
                 *reinterpret_cast<f32x4*>((float*)to + at) = g;
                 *reinterpret_cast<f32x4*>((float*)to + kW + at) = u;
@@ -651,6 +660,10 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
             if (n + e < a.N) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
         }
         if constexpr (C::EPI == kTileGated) {
+          if (a.pair_rows != 0)
+            *reinterpret_cast<u32x4*>(o + (int64_t)a.pair_rows * a.out_pitch) =
+                *reinterpret_cast<const u32x4*>(from + 5 * kW + 8 * c);
+          if (a.act != nullptr) *reinterpret_cast<u32x4*>(a.act + (int64_t)m * a.I + n) = w;
           if (a.h != nullptr) {
             float* const hp = a.h + (int64_t)m * 2 * a.I + n;
             const f32x4* const src = reinterpret_cast<const f32x4*>((const float*)from + 8 * c);

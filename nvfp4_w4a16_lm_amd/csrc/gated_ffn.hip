@@ -6,7 +6,8 @@
 //
 // Forward: both projections, the activation and the product are one kernel
 // whose tile holds matching rows of the gate and the up projection; the
-// activation enters the down projection rounded to bf16.  Kept for the
+// activation enters the down projection rounded to bf16, up to 16 tokens as a pair
+// of bf16.  Kept for the
 // backward pass: h = [g, u] in float32 and a in bf16, as the operand of dW2 that it
 // is.  (With h in bf16 the gradients of x and W13 are off by 0.0030 of their norm instead
 // of 0.0024, where one rounding of the result is 0.0017; the step of 4096 tokens is 4 % faster.)  Backward:
@@ -36,14 +37,20 @@ static TileSplit gated_split(int64_t M, int64_t N, int64_t K) { return tile_spli
 struct GatedLayout {
   int64_t parts, bytes;
 };
+// Up to 16 tokens the activation enters the down projection as a pair of bf16, 16 bits of it: its second rows fill
+// the tile of 32 (one token 69 us with and without).
+constexpr int64_t kGatedPair = 16;
+
 static GatedLayout gated_layout(int64_t T, int64_t H, int64_t I, bool backward) {
   GatedLayout l = {};
   int64_t at = 0;
+  const bool pair = T <= kGatedPair;
   // the forward pass's a and the backward's [dg, du] share a place
-  at += up256((backward ? 4 : 2) * T * I);
+  at += up256((backward || pair ? 4 : 2) * T * I);
   l.parts = at;
-  const int sd = gated_split(T, H, I).splits, sx = gated_split(T, H, 2 * I).splits;
-  const int s = backward && sx > sd ? sx : sd;
+  const int64_t sd = pair ? 2 * gated_split(2 * T, H, I).splits : gated_split(T, H, I).splits;
+  const int64_t sx = gated_split(T, H, 2 * I).splits;
+  const int64_t s = backward && sx > sd ? sx : sd;
   if (s > 1) at += up256(4 * s * T * H);
   l.bytes = at;
   return l;
@@ -54,25 +61,27 @@ int64_t gated_ffn_workspace_bytes(int64_t T, int64_t H, int64_t I, bool backward
   return b < 16 ? 16 : b;
 }
 
-// out bf16 [M, N] = q [M, K] p^T or q p (PT), K split where the tiles are few
+// out bf16 [M, N] = q [M, K] p^T or q p (PT), K split where the tiles are few; with `pair` q has M rows more, whose
+// products are added
 template <bool PT>
-static hipError_t gated_product(const void* q, const void* p, int64_t M, int64_t N, int64_t K, void* out,
+static hipError_t gated_product(const void* q, const void* p, int64_t M, int64_t N, int64_t K, bool pair, void* out,
                                 float* parts, hipStream_t stream) {
+  const int64_t rows = pair ? 2 * M : M;
   TileArgs a = {};
   a.p = (const uint8_t*)p;
   a.q = (const uint8_t*)q;
   a.p_pitch = 2 * (PT ? N : K);
   a.q_pitch = 2 * K;
   a.p_rows = PT ? K : N;
-  a.q_rows = M;
-  a.M = (int)M;
+  a.q_rows = rows;
+  a.M = (int)rows;
   a.N = (int)N;
   a.K = (int)K;
   a.out_pitch = N;
-  const TileSplit s = gated_split(M, N, K);
+  const TileSplit s = gated_split(rows, N, K);
   a.k_split = s.k_split;
   a.splits = s.splits;
-  if (a.splits == 1) {
+  if (a.splits == 1 && !pair) {
     a.out = out;
     return launch_tile<kTileBf16, PT, false>(a, s.size, stream);
   }
@@ -80,7 +89,7 @@ static hipError_t gated_product(const void* q, const void* p, int64_t M, int64_t
   const hipError_t e = launch_tile<kTileF32, PT, false>(a, s.size, stream);
   if (e != hipSuccess) return e;
   return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)((M * N / 8 + 63) / 64)), dim3(256), stream,
-                       (const float*)parts, (int64_t)(M * N), (int)a.splits, (uint16_t*)out);
+                       (const float*)parts, (int64_t)(M * N), (int)(pair ? 2 * a.splits : a.splits), (uint16_t*)out);
 }
 
 // out bf16 [M, N] = q^T p, q [K, M], p [K, N]
@@ -118,12 +127,15 @@ hipError_t launch_gated_ffn(const void* x, int64_t T, int64_t H, const void* w13
   a.K = (int)H;
   a.splits = 1;
   a.k_split = (int)((H + 63) / 64 * 64);
-  a.out = act == nullptr ? ws : act;
+  const bool pair = T <= kGatedPair;
+  a.out = act == nullptr || pair ? ws : act;
   a.out_pitch = I;
+  a.pair_rows = pair ? (int)T : 0;
+  a.act = pair ? (uint16_t*)act : nullptr;
   a.h = h;
   const hipError_t e = launch_tile<kTileGated, false, false>(a, tile_size(T, 2 * I, (H + 63) / 64, 1), stream);
   if (e != hipSuccess) return e;
-  return gated_product<false>(a.out, w2, T, H, I, y, (float*)(ws + l.parts), stream);
+  return gated_product<false>(a.out, w2, T, H, I, pair, y, (float*)(ws + l.parts), stream);
 }
 
 hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const float* h, const void* act,
@@ -153,7 +165,7 @@ hipError_t launch_gated_ffn_backward(const void* x, int64_t T, int64_t H, const 
     if (e != hipSuccess) return e;
   }
   if (dx != nullptr) {
-    e = gated_product<true>(ws, w13, T, H, 2 * I, dx, (float*)(ws + l.parts), stream);
+    e = gated_product<true>(ws, w13, T, H, 2 * I, false, dx, (float*)(ws + l.parts), stream);
     if (e != hipSuccess) return e;
   }
   return dw13 == nullptr ? hipSuccess : gated_weight_grad(ws, 2 * I, x, H, T, dw13, stream);
