@@ -74,7 +74,8 @@ struct TileArgs {
   const float* sw;
   const uint16_t* bias;      // [n]
   int32_t I;                 // gated: width of a half
-  int32_t pair_rows;         // gated: where not 0, out row pair_rows + m receives what rounding took from row m
+  int32_t pair_rows;         // where not 0: gated, out row pair_rows + m receives what rounding took from row m; float32,
+                             // row pair_rows + m of the product is added to row m (M = 2 pair_rows, within one pass)
   uint16_t* act;             // gated: the rounded a once more [m][I], or NULL
   float* h;                  // gated: [m][2 I], written (forward, may be NULL) or read (backward)
   uint16_t* dh;              // gated backward [m][2 I]
@@ -486,7 +487,8 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         const int m = m0 + 32 * (JT * (row >> 5) + j) + (row & 31);
         on[it] = m < M && n < a.N;
         if constexpr (C::EPI == kTileF32) {
-          at[it] = ((int64_t)split * a.M + m) * a.out_pitch + n;
+          if (a.pair_rows != 0) on[it] = on[it] && m < a.pair_rows;
+          at[it] = ((int64_t)split * (a.pair_rows != 0 ? a.pair_rows : a.M) + m) * a.out_pitch + n;
           if (on[it] && a.accumulate) {
             in[it][0] = *reinterpret_cast<const f32x4*>((const float*)a.out + at[it]);
             in[it][1] = *reinterpret_cast<const f32x4*>((const float*)a.out + at[it] + 4);
@@ -520,6 +522,11 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         f32x4 lo = src[0], hi = src[1];
         if (!on[it]) continue;
         if constexpr (C::EPI == kTileF32) {
+          if (a.pair_rows != 0) {
+            const f32x4* const low = reinterpret_cast<const f32x4*>(stage + (row + a.pair_rows) * C::kStagePitch + 8 * c);
+            lo += low[0];
+            hi += low[1];
+          }
           if (a.accumulate) {
             lo += in[it][0];
             hi += in[it][1];

@@ -13,8 +13,8 @@
 // of 0.0024, where one rounding of the result is 0.0017; the step of 4096 tokens is 4 % faster.)  Backward:
 // the kernel of da = dy W2 ends in [dg, du], in bf16 as operands; then three products.
 //
-// Measured: one token of (4096, 14336) 69 us (5.1 TB/s: 42 us both projections at 5.5 TB/s, 22 the down projection in
-// 16 parts, 5 their join), 16 tokens 70 us; the step of 4096 tokens 3.4 ms (1.27 PFLOP/s: 0.83, 0.36, 0.54, 0.43,
+// Measured: one token of (4096, 14336) 68 us (5.2 TB/s: 42 us both projections at 5.5 TB/s, 22 the down projection in
+// 16 parts, 5 their join), 16 tokens 71 us; the step of 4096 tokens 3.4 ms (1.27 PFLOP/s: 0.83, 0.36, 0.54, 0.43,
 // 0.72, 0.75 ms in the order above); of 333 tokens of (2080, 5616) 167 us.
 #include "dense_tile.hpp"
 
@@ -38,7 +38,7 @@ struct GatedLayout {
   int64_t parts, bytes;
 };
 // Up to 16 tokens the activation enters the down projection as a pair of bf16, 16 bits of it: its second rows fill
-// the tile of 32 (one token 69 us with and without).
+// the tile of 32 (one token 67.2 us rounded to bf16, 67.6 so; 16 tokens 70.6, 71.2).
 constexpr int64_t kGatedPair = 16;
 
 static GatedLayout gated_layout(int64_t T, int64_t H, int64_t I, bool backward) {
@@ -48,10 +48,10 @@ static GatedLayout gated_layout(int64_t T, int64_t H, int64_t I, bool backward) 
   // the forward pass's a and the backward's [dg, du] share a place
   at += up256((backward || pair ? 4 : 2) * T * I);
   l.parts = at;
-  const int64_t sd = pair ? 2 * gated_split(2 * T, H, I).splits : gated_split(T, H, I).splits;
+  const int64_t sd = gated_split(pair ? 2 * T : T, H, I).splits;
   const int64_t sx = gated_split(T, H, 2 * I).splits;
   const int64_t s = backward && sx > sd ? sx : sd;
-  if (s > 1) at += up256(4 * s * T * H);
+  if (s > 1 || pair) at += up256(4 * s * T * H);
   l.bytes = at;
   return l;
 }
@@ -78,6 +78,7 @@ static hipError_t gated_product(const void* q, const void* p, int64_t M, int64_t
   a.N = (int)N;
   a.K = (int)K;
   a.out_pitch = N;
+  a.pair_rows = pair ? (int)M : 0;
   const TileSplit s = gated_split(rows, N, K);
   a.k_split = s.k_split;
   a.splits = s.splits;
@@ -89,7 +90,7 @@ static hipError_t gated_product(const void* q, const void* p, int64_t M, int64_t
   const hipError_t e = launch_tile<kTileF32, PT, false>(a, s.size, stream);
   if (e != hipSuccess) return e;
   return launch_kernel((const void*)gated_join_kernel, dim3((unsigned)((M * N / 8 + 63) / 64)), dim3(256), stream,
-                       (const float*)parts, (int64_t)(M * N), (int)(pair ? 2 * a.splits : a.splits), (uint16_t*)out);
+                       (const float*)parts, (int64_t)(M * N), (int)a.splits, (uint16_t*)out);
 }
 
 // out bf16 [M, N] = q^T p, q [K, M], p [K, N]

@@ -169,7 +169,7 @@ def gated_ffn(x, w13, w2):
     ep = ea + (HALF * HALF if x.shape[0] <= 16 else HALF) * (np.abs(a) + ea) + TINY
     ea = ea + HALF * (np.abs(a) + ea) + TINY
     y = a @ w2.T
-    ey = ep @ np.abs(w2).T + acc(i, JOINS) * ((np.abs(a) + ep) @ np.abs(w2).T) * (2 if x.shape[0] <= 16 else 1)
+    ey = ep @ np.abs(w2).T + acc(i, JOINS + 1) * ((np.abs(a) + ep) @ np.abs(w2).T)
     return (y, hu, a), (ey + HALF * (np.abs(y) + ey) + TINY, e + U * np.abs(hu) + TINY, ea)
 
 
