@@ -85,6 +85,7 @@ struct TileArgs {
   float* tlogit;             // [m]
   const float2* stats;       // [m] (maximum, sum)
   const float2* coef;        // [m] (dloss + dlse, dloss)
+  float* rest;               // [m] what rounding took from the gradient of the target's logit, or NULL
 };
 
 // s_waitcnt immediate: vmcnt(vm) lgkmcnt(0), expcnt left alone
@@ -601,7 +602,7 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
               }
             }
         } else {
-          float sx = 1.0f, top = 0.0f, scale = 0.0f, minus = 0.0f;
+          float sx = 1.0f, top = 0.0f, scale = 0.0f, minus = 0.0f, at_target = 0.0f;
           int tok = -1;
           if constexpr (C::I8) sx = a.sx[min(m, M - 1)];
           if constexpr (C::EPI == kTileCeGrad) {
@@ -630,11 +631,16 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
                   const float p = v[e] == -INFINITY ? 0.0f : exp_fast(v[e] - top) * scale;
                   const bool target = tok == 32 * i + 8 * q + e && v[e] != -INFINITY;
                   v[e] = p - (target ? minus : 0.0f);
+                  at_target = target ? v[e] : at_target;
                 }
               }
               *reinterpret_cast<uint2*>(to + 32 * (IT * wn + i) + 8 * q + 4 * h) =
                   make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
             }
+          if constexpr (C::EPI == kTileCeGrad) {
+            if (a.rest != nullptr && m < M && tok >= 0 && tok < 32 * IT && (tok & 4) == 0)
+              a.rest[m] = at_target - bf16_lo(pack_bf16(at_target, 0.0f));
+          }
         }
       }
       __syncthreads();
