@@ -546,7 +546,8 @@ nvfp4_status nvfp4_logprobs_backward(const void* logits, int dtype, int64_t M, i
  * nvfp4_int8_quantize_rows -- row-wise int8 quantization of a bf16 [R, K] matrix:
  *   scales[r] = max(fl32(amax_r / 127), 1e-12),  q = rne(127 a / amax_r) in [-127, 127]
  * The codes are those of the exact ratio (nearest, ties to even); in a row whose scale is 1e-12 they
- * are rne(fl32(a / scale)).  Non-finite values are outside the contract.  0 <= R <= 2^23 (0 enqueues nothing).
+ * are rne(fl32(a / scale)).  A row that holds a NaN or an infinity has the scale NaN and codes 0: each of its
+ * products is NaN.  0 <= R <= 2^23 (0 enqueues nothing).
  * K as below; a and q 16-byte aligned.
  *
  * nvfp4_int8_gemm

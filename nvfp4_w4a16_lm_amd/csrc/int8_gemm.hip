@@ -1,7 +1,8 @@
 // 8-bit integer weights and activations (gfx950): one scale for each token and
 // each channel.
 //
-//   quantizer   s = max(max_k |a| / 127, 1e-12),  q = round(127 a / max_k |a|), nearest even
+//   quantizer   s = max(max_k |a| / 127, 1e-12),  q = round(127 a / max_k |a|), nearest even;
+//               with a NaN or an infinity in the row s = NaN and q = 0, so that all its products are NaN
 //   product     y[m, n] = bf16( sx[m] sw[n] sum_k xq[m, k] wq[n, k] + bias[n] )
 //
 // The sums are exact in 32 bits: |q| <= 128 and K < 2^17.  Measured, quantizer and product: 1 x
@@ -51,8 +52,10 @@ __global__ __launch_bounds__(kQ8Threads) void int8_quant_rows_kernel(const uint1
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kQ8Threads / 64; ++w) mx = pk_max_u16(mx, part[w]);
+  // the bits of magnitudes order as the magnitudes, infinity and then the NaN above all: such a row shows in amax
   const float amax = __uint_as_float(max(mx & 0xFFFFu, mx >> 16) << 16);
-  const float s = fmaxf(__fdiv_rn(amax, 127.0f), 1e-12f);
+  const bool finite = amax < INFINITY;
+  const float s = finite ? fmaxf(__fdiv_rn(amax, 127.0f), 1e-12f) : NAN;
   if (tid == 0) scales[row] = s;
   // where the scale is the smallest one, a / s; where 127 a could overflow, everything 2^-8 as large
   const bool least = s == 1e-12f, large = amax > 0x1p100f;
@@ -62,6 +65,7 @@ __global__ __launch_bounds__(kQ8Threads) void int8_quant_rows_kernel(const uint1
     return (uint32_t)(int)fminf(fmaxf(rintf(__fdiv_rn(v * factor, over)), -127.0f), 127.0f) & 0xFFu;
   };
   auto codes = [&](u32x4 v) __attribute__((always_inline)) {
+    if (!finite) return make_uint2(0, 0);
     uint2 o;
     o.x = code(bf16_lo(v[0])) | code(bf16_hi(v[0])) << 8 | code(bf16_lo(v[1])) << 16 | code(bf16_hi(v[1])) << 24;
     o.y = code(bf16_lo(v[2])) | code(bf16_hi(v[2])) << 8 | code(bf16_lo(v[3])) << 16 | code(bf16_hi(v[3])) << 24;

@@ -36,18 +36,23 @@ def acc(k: int, joins: int = 0) -> float:
 
 def int8_scale(row: np.ndarray) -> np.float32:
     amax = np.float32(np.abs(row).max()) if row.size else np.float32(0)
+    if not np.isfinite(amax):
+        return np.float32(np.nan)
     return max(np.float32(amax / np.float32(127.0)), np.float32(1e-12))
 
 
 def int8_quantize_rows(a: np.ndarray):
     """float64 values of a bf16 matrix -> (codes int8, scales float32): the nearest code to the exact
-    ratio 127 a / amax, ties to even (where the scale is the smallest one, to a / scale in float32)."""
+    ratio 127 a / amax, ties to even (where the scale is the smallest one, to a / scale in float32).  A row with
+    a NaN or an infinity: codes 0, scale NaN."""
     codes = np.empty(a.shape, np.int8)
     scales = np.empty(a.shape[0], np.float32)
     for i, row in enumerate(a):
         s = scales[i] = int8_scale(row)
         amax = float(np.abs(row).max()) if row.size else 0.0
-        if np.float32(np.float32(amax) / np.float32(127.0)) > np.float32(1e-12):
+        if np.isnan(s):
+            codes[i] = 0
+        elif np.float32(np.float32(amax) / np.float32(127.0)) > np.float32(1e-12):
             top = Fraction(amax)
             uniq = {v: round(Fraction(127) * Fraction(v) / top) for v in set(row.tolist())}  # Python rounds half to even
             codes[i] = [uniq[v] for v in row.tolist()]

@@ -172,6 +172,15 @@ def test_int8_codes_by_hand():
     assert abs(Fraction(y[0, 0]) - want) < Fraction(1, 10 ** 12) and b[0, 0] < 2.0 ** -7 * abs(y[0, 0])
 
 
+def test_int8_rows_that_are_not_finite():
+    a = np.ones((3, 16))
+    a[0, 3], a[2, 5] = np.nan, -np.inf
+    q, s = D.int8_quantize_rows(a)
+    assert np.isnan(s[[0, 2]]).all() and not q[[0, 2]].any() and np.all(q[1] == 127) and np.isfinite(s[1])
+    y, _ = D.int8_gemm(q, s, q[1:2], s[1:2])
+    assert np.isnan(y[[0, 2]]).all() and abs(y[1, 0] - 16) < 1e-5
+
+
 def test_float32_codes_are_those_of_the_exact_ratio():
     """One float32 division against exact rational arithmetic, over every significand of the maximum and of the
     element, and the element's scales at which it has a nonzero code."""

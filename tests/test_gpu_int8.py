@@ -51,6 +51,33 @@ def test_quantizer_special_rows():
     check_quant(rows.to(BF16))
 
 
+@pytest.mark.parametrize("k", [16, 528, 8208, 20016])
+@pytest.mark.parametrize("bad", [float("nan"), -float("nan"), float("inf"), -float("inf")])
+def test_rows_that_are_not_finite_stay_so(k, bad):
+    """A NaN or an infinity anywhere in a row: scale NaN, codes 0, and all its products NaN, as a row of x and as
+    a row of the weight; the other rows as without it."""
+    rng = np.random.default_rng(k)
+    a = bf16(rng, 40, k)
+    want = [t.clone() for t in B.nvfp4_int8_quantize_rows(a.to(DEV))]
+    rows = {0: 0, 7: k - 1, 20: k // 2, 39: min(k - 1, 8195)}
+    for row, at in rows.items():
+        a[row, at] = bad
+    q, s = B.nvfp4_int8_quantize_rows(a.to(DEV))
+    wq, ws = D.int8_quantize_rows(a.double().numpy())
+    assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws, equal_nan=True)
+    gone = torch.zeros(40, dtype=torch.bool, device=DEV)
+    gone[list(rows)] = True
+    assert torch.isnan(s[gone]).all() and not q[gone].any()
+    assert torch.equal(q[~gone], want[0][~gone]) and torch.equal(s[~gone], want[1][~gone])
+    other = codes(rng, 33, k).to(DEV)
+    one = torch.full((33,), 0.01, device=DEV)
+    bias = bf16(rng, 33).to(DEV)
+    y = B.nvfp4_int8_gemm(q, s, other, one, bias)
+    assert torch.isnan(y[gone]).all() and torch.isfinite(y[~gone]).all()
+    y = B.nvfp4_int8_gemm(other, one, q, s)
+    assert torch.isnan(y[:, gone]).all() and torch.isfinite(y[:, ~gone]).all()
+
+
 def codes(rng, *shape):
     return torch.from_numpy(rng.integers(-128, 128, shape).astype(np.int8))
 
