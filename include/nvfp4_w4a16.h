@@ -593,7 +593,10 @@ nvfp4_status nvfp4_int8_gemm(const int8_t* xq, const float* x_scales, int64_t M,
  *   bias       in  bf16 [V] or NULL
  *   targets    in  int32 [M]
  *   workspace  tmp nvfp4_linear_ce_workspace_bytes(M, V, K, backward) bytes, 16-byte aligned; its
- *                  contents need no preparation, and the two calls may share one of the larger size
+ *                  contents need no preparation.  The size never falls as M grows, and the backward
+ *                  pass's is the larger one, so that one workspace serves both calls and every batch
+ *                  up to its own.  The backward pass keeps dz of a piece of the vocabulary in it: 128 MiB
+ *                  at most up to 65536 rows, 2 KiB a row beyond
  *   loss       out float [M];  lse out float [M] or NULL;  stats out float [M, 2], 8-byte aligned
  *   dloss      in  float [M];  dlse in float [M] or NULL (0)
  *   dx, dweight, dbias  out  bf16, each optional (NULL), dx and dweight 16-byte aligned
@@ -625,7 +628,8 @@ nvfp4_status nvfp4_linear_ce_backward(const void* x, int64_t M, int64_t K, const
  *   h, act     out (forward, both or neither NULL) / in (backward)  float [T, 2 I], bf16 [T, I]
  *   dy         in  bf16 [T, H]
  *   workspace  tmp nvfp4_gated_ffn_workspace_bytes(T, H, I, backward) bytes; its contents need no
- *                  preparation, and the two calls may share one of the larger size
+ *                  preparation.  The size never falls as T grows, and the backward pass's is the larger
+ *                  one, so that one workspace serves both calls and every batch up to its own
  *   y          out bf16 [T, H]
  *   dx, dw13, dw2  out  bf16 as x, w13 and w2, each optional (NULL)
  * Every pointer is 16-byte aligned.

@@ -950,7 +950,8 @@ def _workspace(need: int, workspace, dev, fn: str, sizes: str) -> torch.Tensor:
 
 
 def linear_ce_workspace(m: int, v: int, k: int, device, backward: bool = True) -> torch.Tensor:
-    """Workspace of nvfp4_linear_ce, and with ``backward`` of nvfp4_linear_ce_backward too, to be kept."""
+    """Workspace of nvfp4_linear_ce, and with ``backward`` of nvfp4_linear_ce_backward too, to be kept: it serves
+    every batch up to this one."""
     need = int(load_library().nvfp4_linear_ce_workspace_bytes(m, v, k, int(backward)))
     return _workspace(need, None, device, "nvfp4_linear_ce", f"M={m}, V={v}, K={k}")
 
@@ -1022,7 +1023,8 @@ class GatedKept(NamedTuple):
 
 
 def gated_ffn_workspace(t: int, h: int, i: int, device, backward: bool = True) -> torch.Tensor:
-    """Workspace of nvfp4_gated_ffn, and with ``backward`` of nvfp4_gated_ffn_backward too, to be kept."""
+    """Workspace of nvfp4_gated_ffn, and with ``backward`` of nvfp4_gated_ffn_backward too, to be kept: it serves
+    every batch up to this one."""
     need = int(load_library().nvfp4_gated_ffn_workspace_bytes(t, h, i, int(backward)))
     return _workspace(need, None, device, "nvfp4_gated_ffn", f"T={t}, H={h}, I={i}")
 

@@ -752,6 +752,15 @@ inline TileSplit tile_split(int64_t M, int64_t N, int64_t K, int64_t least, int6
   return best;
 }
 
+// Floats that hold the parts of every [m, N] product, m <= M, that tile_split cuts in two or more (0: none is): a size
+// that does not fall as M grows.  There are at most 2 kTileCus / tiles parts, and a tile is at most 128 x 128.
+inline int64_t tile_split_floats(int64_t M, int64_t N, int64_t K, int64_t least, int64_t most) {
+  int64_t s = (K + 63) / 64 / least;
+  s = s > most ? most : s;
+  const int64_t limit = (int64_t)kTileCus * 2 * 128 * 128;
+  return s <= 1 ? 0 : s * M * N < limit ? s * M * N : limit;
+}
+
 // Eight columns from `at` of the sum of `splits` partial products `stride` floats apart, by 256 threads: thread
 // t's wavefront adds every fourth part, the first wavefront the four sums.  Only lanes with `on` read; the sum
 // is the first wavefront's.

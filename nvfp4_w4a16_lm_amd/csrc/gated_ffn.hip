@@ -33,6 +33,7 @@ static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // The down projection and dx: K split where the tiles are few, at least 8 steps a part.
 static TileSplit gated_split(int64_t M, int64_t N, int64_t K) { return tile_split(M, N, K, 8, 16); }
+static int64_t gated_split_floats(int64_t M, int64_t N, int64_t K) { return tile_split_floats(M, N, K, 8, 16); }
 
 struct GatedLayout {
   int64_t parts, bytes;
@@ -41,18 +42,17 @@ struct GatedLayout {
 // the tile of 32 (one token 67.2 us rounded to bf16, 67.6 so; 16 tokens 70.6, 71.2).
 constexpr int64_t kGatedPair = 16;
 
+// No part's size falls as T grows, though the pair ends and the splits change: a workspace kept for the largest batch
+// holds every smaller one.
 static GatedLayout gated_layout(int64_t T, int64_t H, int64_t I, bool backward) {
   GatedLayout l = {};
-  int64_t at = 0;
-  const bool pair = T <= kGatedPair;
-  // the forward pass's a and the backward's [dg, du] share a place
-  at += up256((backward || pair ? 4 : 2) * T * I);
-  l.parts = at;
-  const int64_t sd = gated_split(pair ? 2 * T : T, H, I).splits;
-  const int64_t sx = gated_split(T, H, 2 * I).splits;
-  const int64_t s = backward && sx > sd ? sx : sd;
-  if (s > 1 || pair) at += up256(4 * s * T * H);
-  l.bytes = at;
+  const int64_t pairs = T < kGatedPair ? T : kGatedPair;
+  // the forward pass's a, for few tokens a pair, and the backward's [dg, du] share a place
+  const int64_t rows = backward ? 2 * T : T > 2 * pairs ? T : 2 * pairs;
+  l.parts = up256(2 * rows * I);
+  // the joined products: of a pair always, else where K is split
+  const int64_t split = gated_split_floats(T, H, backward ? 2 * I : I);
+  l.bytes = l.parts + up256(4 * (split > pairs * H ? split : pairs * H));
   return l;
 }
 

@@ -194,6 +194,8 @@ struct CeLayout {
   TileSplit dx;
 };
 
+// No part's size falls as M grows, though tiles, pieces and splits change with it: a workspace kept for the largest
+// batch holds every smaller one.
 static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
   CeLayout l = {};
   int64_t at = 0;
@@ -210,7 +212,7 @@ static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
   l.tiles = (V + tile_shape(l.logits).bn - 1) / tile_shape(l.logits).bn;
   // the forward pass's part and the backward's overlap
   const int64_t common = at;
-  l.parts = take(8 * M * l.tiles);
+  l.parts = take(8 * M * ((V + 127) / 128));               // tiles are 128 columns at least
   l.tlogit = take(4 * M);
   if (backward) {
     const int64_t forward_end = at;
@@ -222,10 +224,13 @@ static CeLayout ce_layout(int64_t M, int64_t V, int64_t K, bool backward) {
     most = most < 1024 ? 1024 : most > kCePieceMost ? kCePieceMost : most;
     const int64_t pieces = (V + most - 1) / most;
     l.piece = up256((V + pieces - 1) / pieces);
-    l.d = take(2 * M * l.piece);
+    const int64_t widest = up256(V) < kCePieceMost ? up256(V) : kCePieceMost;
+    const int64_t limit = 2048 * M > kCePieceBytes ? 2048 * M : kCePieceBytes;
+    l.d = take(2 * M * widest < limit ? 2 * M * widest : limit);
     l.grad = tile_size(M, l.piece, (K + 63) / 64, 1);
     l.dx = tile_split(M, K, l.piece, 8, 64);
-    l.acc = take(4 * l.dx.splits * M * K);
+    const int64_t split = tile_split_floats(M, K, widest, 8, 64);
+    l.acc = take(4 * (split > M * K ? split : M * K));
     if (at < forward_end) at = forward_end;
   }
   l.bytes = at;

@@ -128,6 +128,23 @@ def test_gated_ffn_refusals():
     assert size(333, 2080, 5616, 1) >= size(333, 2080, 5616, 0) >= 2 * 333 * 5616
 
 
+@pytest.mark.parametrize("back", [0, 1])
+@pytest.mark.parametrize("call,a,b", [
+    ("linear_ce", 32003, 512), ("linear_ce", 32003, 2080), ("linear_ce", 128256, 4096), ("linear_ce", 151936, 16),
+    ("linear_ce", 1, 16), ("linear_ce", 1 << 20, 64), ("gated_ffn", 4096, 14336), ("gated_ffn", 2080, 5616), ("gated_ffn", 64, 96),
+    ("gated_ffn", 16, 16), ("gated_ffn", 512, 1024), ("gated_ffn", 16384, 16), ("gated_ffn", 16, 65536)])
+def test_workspace_of_a_batch_serves_every_smaller_one(call, a, b, back):
+    """Sizes do not fall as the batch grows, and the backward pass's is the larger one."""
+    size = getattr(lib(), f"nvfp4_{call}_workspace_bytes")
+    rng = np.random.default_rng(a + b)
+    ms = sorted({*range(2200), *(2 ** rng.uniform(11, 17, 300)).astype(int).tolist(), *(1 << e for e in range(11, 18))})
+    last = 0
+    for m in ms:
+        n = size(m, a, b, back)
+        assert n >= last and n >= size(m, a, b, 0) >= 16, (m, n, last)
+        last = n
+
+
 def bf(*shape):
     return torch.zeros(shape, dtype=torch.bfloat16)
 

@@ -174,6 +174,19 @@ def test_given_stream_with_wide_input():
     assert all(torch.equal(a, b) for a, b in zip((y, *kept, *want), (y2, *h2, *g2)))
 
 
+def test_workspace_kept_for_the_largest_batch():
+    """One workspace of the largest batch, for every smaller one: the results are those of a fresh one."""
+    h, i = 144, 1040
+    x, w13, w2, dy = (v.to(DEV) for v in make(1025, h, i, seed=10))
+    ws = B.gated_ffn_workspace(1025, h, i, DEV)
+    for t in (1025, 1024, 513, 257, 256, 129, 128, 65, 33, 32, 17, 16, 1):
+        y, kept = B.nvfp4_gated_ffn(x[:t], w13, w2, keep_h=True)
+        want = (y, *kept, *B.nvfp4_gated_ffn_backward(x[:t], kept, w13, w2, dy[:t]))
+        y, kept = B.nvfp4_gated_ffn(x[:t], w13, w2, keep_h=True, workspace=ws)
+        got = (y, *kept, *B.nvfp4_gated_ffn_backward(x[:t], kept, w13, w2, dy[:t], workspace=ws))
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), t
+
+
 def test_empty_batch_and_refusals():
     x, w13, w2, dy = (v.to(DEV) for v in make(4, 32, 48, seed=9))
     y, kept = B.nvfp4_gated_ffn(x[:0], w13, w2, keep_h=True)

@@ -266,6 +266,19 @@ def test_given_stream_and_small_workspace():
         backward(d, want.stats, workspace=B.linear_ce_workspace(33, 700, 96, DEV, backward=False)[:64])
 
 
+def test_workspace_kept_for_the_largest_batch():
+    """One workspace of the largest batch, for every smaller one: the results are those of a fresh one."""
+    v, k = 2003, 144
+    ws = B.linear_ce_workspace(1025, v, k, DEV)
+    for m in (1025, 1024, 513, 257, 256, 129, 128, 65, 64, 33, 32, 1):
+        d = dev(make(m, v, k, seed=m, gone=0.1))
+        r = forward(d)
+        want = (*r, *backward(d, r.stats)[:2])
+        s = forward(d, workspace=ws)
+        got = (*s, *backward(d, s.stats, workspace=ws)[:2])
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), m
+
+
 def test_empty_batch():
     d = dev(make(2, 100, 32, seed=1, bias=True))
     e = {n: t if n in ("w", "bias") else t[:0] for n, t in d.items()}
