@@ -118,7 +118,7 @@ def linear_ce(x, w, targets, bias=None):
 
 
 def linear_ce_backward(x, w, targets, dloss, dlse=None, bias=None):
-    """((dx, dw, db), bounds of each) with dz rounded to bf16 as an operand."""
+    """((dx, dw, db), bounds of each) with dz rounded to bf16 as an operand; in db the targets' dz count unrounded."""
     m, v = x.shape[0], w.shape[0]
     k = x.shape[1]
     rows = _rows(targets, v)
@@ -137,6 +137,7 @@ def linear_ce_backward(x, w, targets, dloss, dlse=None, bias=None):
     rel = e + _row_error(z, e, top)[:, None] + 2.0 ** -20 + \
         4 * U * np.abs(np.where(np.isfinite(z), z - top, 0.0)) + (v / 64.0 + 300.0) * U
     ez = np.abs(c) * p * np.expm1(np.minimum(rel, 50.0)) + 2 * U * np.abs(d) * one
+    unrounded = ez + TINY
     ez = ez + HALF * (np.abs(dz) + ez) + TINY
     az = np.abs(dz) + ez
     dx, bx = np.zeros((m, k)), np.zeros((m, k))
@@ -145,7 +146,7 @@ def linear_ce_backward(x, w, targets, dloss, dlse=None, bias=None):
     dw = dz.T @ xr
     bw = ez.T @ np.abs(xr) + acc(len(rows)) * (az.T @ np.abs(xr))
     db = dz.sum(0)
-    bb = ez.sum(0) + acc(len(rows)) * az.sum(0)
+    bb = np.where(one > 0, unrounded, ez).sum(0) + acc(len(rows)) * az.sum(0)
     return (dx, dw, db), tuple(b + HALF * (np.abs(y) + b) + TINY for y, b in ((dx, bx), (dw, bw), (db, bb)))
 
 

@@ -250,6 +250,40 @@ def test_linear_ce_with_masked_tokens():
     assert np.all(db[[1, 3]] == 0) and np.all(dw[[1, 3]] == 0) and np.isfinite(dx).all()
 
 
+def shared_targets(m, v, k, seed):
+    """Rows that share a few targets (in no order, so in all groups of rows), their dloss such that each target's dz add up
+    to about nothing: its column of db is a small sum of large terms."""
+    rng = np.random.default_rng(seed)
+    x, w, bias = bf16(rng, m, k), bf16(rng, v, k, sigma=0.5 / np.sqrt(k)), bf16(rng, v, sigma=0.2)
+    t = rng.choice(np.linspace(0, v - 1, max(1, min(7, m // 4))).astype(int), m)
+    dloss = np.where(rng.random(m) < 0.5, 1.0, -1.0) * rng.uniform(0.5, 1.0, m)
+    z = x @ w.T + bias
+    p = np.exp(z[np.arange(m), t] - np.log(np.exp(z).sum(1)))
+    for u in np.unique(t):
+        rows = np.nonzero(t == u)[0]
+        dloss[rows[-1]] = -(dloss[rows[:-1]] * (1 - p[rows[:-1]])).sum() / (1 - p[rows[-1]])
+    return x, w, bias, t, dloss.astype(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("m,v,k", [(5, 300, 16), (20, 1003, 64), (130, 1003, 16), (700, 2003, 144)])
+def test_bound_of_the_bias_gradient_tells_rounded_targets(m, v, k):
+    """db summed from dz as the products take it, with the targets' dz rounded, is outside its bound; with them
+    unrounded it is inside."""
+    x, w, bias, t, dloss = shared_targets(m, v, k, seed=m)
+    (_, _, db), (_, _, bound) = D.linear_ce_backward(x, w, t, dloss, None, bias)
+    z = x @ w.T + bias
+    dz = np.exp(z - z.max(1, keepdims=True))
+    dz *= (dloss / dz.sum(1))[:, None]
+    one = np.zeros_like(dz)
+    one[np.arange(m), t] = 1.0
+    dz -= dloss[:, None] * one
+    low = lambda a: torch.from_numpy(a).to(torch.bfloat16).double().numpy()
+    off = lambda terms: np.abs(low(terms.sum(0)) - db) / bound
+    assert off(np.where(one > 0, dz, low(dz))).max() <= 1.0
+    lost = off(low(dz))
+    assert lost[np.unique(t)].max() > 2.0 and np.delete(lost, np.unique(t)).max() <= 1.0
+
+
 def test_gated_ffn_against_torch_and_differences():
     rng = np.random.default_rng(3)
     x, w13, w2, dy = bf16(rng, 5, 16), bf16(rng, 64, 16), bf16(rng, 16, 32), bf16(rng, 5, 16)

@@ -11,6 +11,7 @@ import oracle.dense_oracle as D
 from nvfp4_w4a16_lm_amd import binding as B
 
 from gpu_util import DEV
+from test_boundary_dense import shared_targets
 from test_gpu_graphs import capture
 
 pytestmark = pytest.mark.gpu
@@ -94,6 +95,16 @@ def test_several_pieces():
     m, v, k = 40000, 4003, 32
     assert int(B.load_library().nvfp4_linear_ce_workspace_bytes(m, v, k, 1)) < 2 * m * v + 8 * m * k
     check(make(m, v, k, seed=3, bias=True, gone=0.05))
+
+
+@pytest.mark.parametrize("m,v,k", [(5, 300, 16), (20, 1003, 64), (130, 1003, 16), (333, 3003, 528), (700, 2003, 144),
+                                   (140, 300003, 16)])
+def test_bias_gradient_takes_the_targets_unrounded(m, v, k):
+    """Rows that share a few targets, again in other groups of rows and in both pieces of a wide vocabulary, with dz
+    that add up to about nothing: what rounding takes from them is several times the bound of their sum."""
+    x, w, bias, t, dloss = (torch.from_numpy(n) for n in shared_targets(m, v, k, seed=m))
+    check(dict(x=x.to(BF16), w=w.to(BF16), bias=bias.to(BF16), t=t.to(torch.int32), dloss=dloss.float(), dlse=None),
+          dlse=False)
 
 
 @pytest.mark.parametrize("m", [1, 40, 300])
