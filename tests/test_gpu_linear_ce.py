@@ -97,6 +97,15 @@ def test_several_pieces():
     check(make(m, v, k, seed=3, bias=True, gone=0.05))
 
 
+@pytest.mark.parametrize("m,v,k", [(3, 265795, 16), (1500, 50003, 32)])
+def test_several_pieces_with_a_split_gradient_of_x(m, v, k):
+    """Two pieces of the vocabulary, dx cut into parts (64 of 3 rows, 40 of 1500) that both pieces add to; the second
+    piece is narrower, so that it leaves the last part as the first one made it."""
+    a = make(m, v, k, seed=m, bias=True, gone=0.0 if m < 10 else 0.1)
+    a["t"][:3] = torch.tensor([5, v // 2 + 1000, v - 1], dtype=torch.int32)
+    check(a)
+
+
 @pytest.mark.parametrize("m,v,k", [(5, 300, 16), (20, 1003, 64), (130, 1003, 16), (333, 3003, 528), (700, 2003, 144),
                                    (140, 300003, 16)])
 def test_bias_gradient_takes_the_targets_unrounded(m, v, k):
