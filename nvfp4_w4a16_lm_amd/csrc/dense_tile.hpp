@@ -525,8 +525,13 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         if constexpr (C::EPI == kTileF32) {
           if (a.pair_rows != 0) {
             const f32x4* const low = reinterpret_cast<const f32x4*>(stage + (row + a.pair_rows) * C::kStagePitch + 8 * c);
-            lo += low[0];
-            hi += low[1];
+            // of an infinite weight too the product is the one of the first half alone: the rest's is infinite of any
+            // sign, or NaN where it is 0
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              lo[e] += fabsf(low[0][e]) < INFINITY ? low[0][e] : 0.0f;
+              hi[e] += fabsf(low[1][e]) < INFINITY ? low[1][e] : 0.0f;
+            }
           }
           if (a.accumulate) {
             lo += in[it][0];

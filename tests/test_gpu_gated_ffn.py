@@ -109,6 +109,29 @@ def test_infinite_and_nan_rows_stay_alone():
     assert torch.isfinite(dx[~bad]).all()
 
 
+@pytest.mark.parametrize("t", [1, 15, 16, 17, 40])
+def test_infinite_weights_of_the_down_projection(t):
+    """An infinity in w2 makes its column infinite with the activation's sign, whether the activation enters as a pair
+    or rounded; two of opposite signs make it NaN; the other columns are what they were."""
+    h, i = 64, 1040
+    n = make(t, h, i, seed=11)
+    n[2][5, 3], n[2][9, 1000], n[2][40, 7], n[2][63, 0] = float("inf"), -float("inf"), float("inf"), float("nan")
+    n[2][40, 8] = float("inf")
+    x, w13, w2, _ = (v.to(DEV) for v in n)
+    y = f64(B.nvfp4_gated_ffn(x, w13, w2))
+    (_, _, a), (_, _, ba) = D.gated_ffn(f64(n[0]), f64(n[1]), np.zeros((h, i)))
+    assert np.all(np.abs(a[:, [3, 7, 8, 1000]]) > ba[:, [3, 7, 8, 1000]])           # their signs are sure
+    sign = np.sign(a)
+    assert np.array_equal(y[:, 5], sign[:, 3] * np.inf) and np.array_equal(y[:, 9], -sign[:, 1000] * np.inf)
+    want = np.where(sign[:, 7] == sign[:, 8], sign[:, 7] * np.inf, np.nan)
+    assert np.array_equal(y[:, 40], want, equal_nan=True) and np.isnan(y[:, 63]).all()
+    rest = np.setdiff1d(np.arange(h), [5, 9, 40, 63])
+    w2 = f64(n[2]).copy()
+    w2[[5, 9, 40, 63]] = 0.0
+    (wy, _, _), (by, _, _) = D.gated_ffn(f64(n[0]), f64(n[1]), w2)
+    assert np.all(np.abs(y[:, rest] - wy[:, rest]) <= by[:, rest])
+
+
 @pytest.mark.parametrize("t", [1, 20, 150])
 def test_buffers_are_written_exactly(t):
     lib = B.load_library()
