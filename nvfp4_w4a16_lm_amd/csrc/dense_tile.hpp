@@ -109,7 +109,7 @@ __device__ __forceinline__ void tile_copy16(__amdgpu_buffer_rsrc_t r, tile_lds_t
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {      // nearest even; NaN stays NaN
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2t));
 }
-// What rounding v to hi left over; nothing where hi is not finite (an infinity's product is the one of hi alone).
+// What rounding v to hi left over; nothing where hi is not finite (an infinity's product or sum is the one of hi alone).
 __device__ __forceinline__ float rest_bf16(float v, float hi) { return fabsf(hi) < INFINITY ? v - hi : 0.0f; }
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
@@ -644,7 +644,7 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
             }
           if constexpr (C::EPI == kTileCeGrad) {
             if (a.rest != nullptr && m < M && tok >= 0 && tok < 32 * IT && (tok & 4) == 0)
-              a.rest[m] = at_target - bf16_lo(pack_bf16(at_target, 0.0f));
+              a.rest[m] = rest_bf16(at_target, bf16_lo(pack_bf16(at_target, 0.0f)));
           }
         }
       }

@@ -196,6 +196,21 @@ def test_infinite_and_nan_logits_stay_in_their_row():
     assert torch.isfinite(dx[~bad]).all() and torch.isnan(dx[bad]).any(1).all()
 
 
+def test_a_target_whose_dz_rounds_to_infinity():
+    """The gradient of the bias is then the infinity, without a remainder that would make it NaN.  bfloat16 takes what is
+    past 2^128 (1 - 2^-9) to infinity; the largest dloss less its part p is."""
+    a = make(1, 300, 64, seed=19, bias=True)
+    t, top = int(a["t"][0]), float(torch.finfo(torch.float32).max)
+    a["dloss"][:] = top
+    a["bias"][t] = -32.0
+    n = {k: f64(v) for k, v in a.items()}
+    loss = D.linear_ce(n["x"], n["w"], np.array([t]), n["bias"])[0][0]
+    assert top * (1 - np.exp(-loss)) > 2.0 ** 128 * (1 - 2.0 ** -10)
+    d = dev(a)
+    _, _, db = backward(d, forward(d).stats, dlse=False)
+    assert float(db[t]) == -float("inf") and torch.isfinite(torch.cat((db[:t], db[t + 1:]))).all()
+
+
 def test_gradient_against_differences():
     """The gradients along a direction against central differences of the oracle's loss."""
     a = make(20, 300, 64, seed=14, bias=True, gone=0.2)
