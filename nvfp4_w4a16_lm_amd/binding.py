@@ -949,6 +949,16 @@ def _workspace(need: int, workspace, dev, fn: str, sizes: str) -> torch.Tensor:
     return workspace
 
 
+def _gradient(want, shape, rows: int, dev, what: str):
+    """A gradient's buffer: made for True, none for False, or the caller's.  A batch without rows leaves zeros."""
+    if want is None or want is False:
+        return None
+    if want is True:
+        return (torch.empty if rows else torch.zeros)(shape, dtype=torch.bfloat16, device=dev)
+    _check_out(want, shape, (torch.bfloat16,), dev, what)
+    return want if rows else want.zero_()
+
+
 def linear_ce_workspace(m: int, v: int, k: int, device, backward: bool = True) -> torch.Tensor:
     """Workspace of nvfp4_linear_ce, and with ``backward`` of nvfp4_linear_ce_backward too, to be kept: it serves
     every batch up to this one."""
@@ -991,9 +1001,12 @@ def nvfp4_linear_ce(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor
 @_on_its_stream
 def nvfp4_linear_ce_backward(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor,
                              dloss: torch.Tensor, bias: torch.Tensor | None = None, dlse: torch.Tensor | None = None,
-                             workspace: torch.Tensor | None = None, stream=None):
+                             workspace: torch.Tensor | None = None, stream=None, *, dx=True, dweight=True,
+                             dbias=True):
     """Gradients of nvfp4_linear_ce: (dx [M, K], dweight [V, K], dbias [V] or None without a bias), all
-    bfloat16, from the gradients of its loss and lse (float32 [M], dlse or None) and its stats."""
+    bfloat16, from the gradients of its loss and lse (float32 [M], dlse or None) and its stats.  Each of ``dx``,
+    ``dweight`` and ``dbias`` may be False (left out, not computed, None returned: a frozen head needs no
+    dweight) or a buffer to write."""
     x, weight, m, v, k, dev = _check_linear_ce(x, weight, targets, bias)
     _check_out(stats, (m, 2), (torch.float32,), dev, "stats")
     _check_vec(dloss, m, torch.float32, dev, "dloss")
@@ -1001,10 +1014,9 @@ def nvfp4_linear_ce_backward(x: torch.Tensor, weight: torch.Tensor, targets: tor
     lib = load_library()
     need = int(lib.nvfp4_linear_ce_workspace_bytes(m, v, k, 1))
     workspace = _workspace(need, workspace, dev, "nvfp4_linear_ce_backward", f"M={m}, V={v}, K={k}")
-    make = torch.empty if m else torch.zeros           # no rows: the gradients are zero
-    dx = make((m, k), dtype=torch.bfloat16, device=dev)
-    dw = make((v, k), dtype=torch.bfloat16, device=dev)
-    db = make((v,), dtype=torch.bfloat16, device=dev) if bias is not None else None
+    dx = _gradient(dx, (m, k), m, dev, "dx")
+    dw = _gradient(dweight, (v, k), m, dev, "dweight")
+    db = _gradient(dbias if bias is not None or torch.is_tensor(dbias) else False, (v,), m, dev, "dbias")
     _check("nvfp4_linear_ce_backward",
            lib.nvfp4_linear_ce_backward(_ptr(x), m, k, _ptr(weight), v, _ptr(bias), _ptr(targets), _ptr(stats),
                                         _ptr(dloss), _ptr(dlse), _ptr(workspace), _ptr(dx), _ptr(dw), _ptr(db),
@@ -1061,9 +1073,10 @@ def nvfp4_gated_ffn(x: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, keep_h
 
 @_on_its_stream
 def nvfp4_gated_ffn_backward(x: torch.Tensor, kept: GatedKept, w13: torch.Tensor, w2: torch.Tensor, dy: torch.Tensor,
-                             workspace: torch.Tensor | None = None, stream=None):
+                             workspace: torch.Tensor | None = None, stream=None, *, dx=True, dw13=True, dw2=True):
     """Gradients of nvfp4_gated_ffn: (dx [T, H], dw13 [2 I, H], dw2 [H, I]), all bfloat16, from dy
-    [T, H] and what the forward pass kept."""
+    [T, H] and what the forward pass kept.  Each of ``dx``, ``dw13`` and ``dw2`` may be False (left out, not
+    computed, None returned) or a buffer to write."""
     x, w13, w2, t, hdim, i, dev = _check_gated_ffn(x, w13, w2)
     dy = _as_bf16_2d(dy, "dy")
     _check_out(dy, (t, hdim), (torch.bfloat16,), dev, "dy")
@@ -1072,10 +1085,9 @@ def nvfp4_gated_ffn_backward(x: torch.Tensor, kept: GatedKept, w13: torch.Tensor
     lib = load_library()
     need = int(lib.nvfp4_gated_ffn_workspace_bytes(t, hdim, i, 1))
     workspace = _workspace(need, workspace, dev, "nvfp4_gated_ffn_backward", f"T={t}, H={hdim}, I={i}")
-    make = torch.empty if t else torch.zeros           # no rows: the gradients are zero
-    dx = make((t, hdim), dtype=torch.bfloat16, device=dev)
-    dw13 = make((2 * i, hdim), dtype=torch.bfloat16, device=dev)
-    dw2 = make((hdim, i), dtype=torch.bfloat16, device=dev)
+    dx = _gradient(dx, (t, hdim), t, dev, "dx")
+    dw13 = _gradient(dw13, (2 * i, hdim), t, dev, "dw13")
+    dw2 = _gradient(dw2, (hdim, i), t, dev, "dw2")
     _check("nvfp4_gated_ffn_backward",
            lib.nvfp4_gated_ffn_backward(_ptr(x), t, hdim, _ptr(kept.h), _ptr(kept.act), _ptr(w13), _ptr(w2), i,
                                         _ptr(dy), _ptr(workspace), _ptr(dx), _ptr(dw13), _ptr(dw2),

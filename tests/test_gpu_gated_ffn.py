@@ -210,6 +210,28 @@ def test_workspace_kept_for_the_largest_batch():
         assert all(torch.equal(a, b) for a, b in zip(got, want)), t
 
 
+@pytest.mark.parametrize("t", [1, 40])
+def test_gradients_left_out_and_given_buffers(t):
+    """Every choice of gradients through the binding: those left out are None, the others are what they are together,
+    made or in the caller's buffers; of an empty batch a buffer becomes zero."""
+    x, w13, w2, dy = (v.to(DEV) for v in make(t, 80, 112, seed=12))
+    _, kept = B.nvfp4_gated_ffn(x, w13, w2, keep_h=True)
+    want = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy)
+    names = ("dx", "dw13", "dw2")
+    for mask in range(8):
+        got = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy, **{n: bool(mask >> j & 1) for j, n in enumerate(names)})
+        assert all(torch.equal(g, w) if mask >> j & 1 else g is None for j, (g, w) in enumerate(zip(got, want)))
+    bufs = [torch.full_like(v, 3.0) for v in want]
+    got = B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy, **dict(zip(names, bufs)))
+    assert all(g is b and torch.equal(g, w) for g, b, w in zip(got, bufs, want))
+    none = B.GatedKept(kept.h[:0], kept.act[:0])
+    dx, d13, d2 = B.nvfp4_gated_ffn_backward(x[:0], none, w13, w2, dy[:0], dw13=bufs[1].fill_(3.0), dw2=False)
+    assert dx.shape == (0, 80) and d13 is bufs[1] and not d13.any() and d2 is None
+    for bad in (dict(dx=bufs[0][:-1].T), dict(dw13=bufs[1].float()), dict(dw2=bufs[2].cpu())):
+        with pytest.raises(ValueError):
+            B.nvfp4_gated_ffn_backward(x, kept, w13, w2, dy, **bad)
+
+
 def test_empty_batch_and_refusals():
     x, w13, w2, dy = (v.to(DEV) for v in make(4, 32, 48, seed=9))
     y, kept = B.nvfp4_gated_ffn(x[:0], w13, w2, keep_h=True)

@@ -314,6 +314,38 @@ def test_workspace_kept_for_the_largest_batch():
         assert all(torch.equal(x, y) for x, y in zip(got, want)), m
 
 
+@pytest.mark.parametrize("m", [3, 200])
+def test_gradients_left_out_and_given_buffers(m):
+    """Every choice of gradients through the binding: those left out are None, the others are what they are together,
+    made or in the caller's buffers; of an empty batch a buffer becomes zero."""
+    d = dev(make(m, 515, 80, seed=m, bias=True, gone=0.2))
+    stats = forward(d).stats
+    want = backward(d, stats)
+    names = ("dx", "dweight", "dbias")
+    for mask in range(8):
+        got = backward(d, stats, **{n: bool(mask >> i & 1) for i, n in enumerate(names)})
+        assert all(torch.equal(g, w) if mask >> i & 1 else g is None for i, (g, w) in enumerate(zip(got, want)))
+    bufs = [torch.full_like(t, 3.0) for t in want]
+    got = backward(d, stats, **dict(zip(names, bufs)))
+    assert all(g is b and torch.equal(g, w) for g, b, w in zip(got, bufs, want))
+    plain = backward(dict(d, bias=None), stats, dx=False, dweight=False)
+    assert plain == (None, None, None)                   # without a bias there is no dbias, unless a buffer asks for it
+    db = backward(dict(d, bias=None), forward(dict(d, bias=None)).stats, dx=False, dweight=False, dbias=bufs[2])[2]
+    assert db is bufs[2] and torch.isfinite(db).all()
+    side = torch.cuda.Stream()
+    bufs[0].fill_(3.0)
+    torch.cuda.synchronize()
+    got = backward(d, stats, stream=side, dweight=False, dx=bufs[0])
+    side.synchronize()
+    assert got[0] is bufs[0] and got[1] is None and torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    empty = {n: t if n in ("w", "bias") else t[:0] for n, t in d.items()}
+    dx, dw, db = backward(empty, stats[:0], dx=False, dweight=bufs[1].fill_(3.0))
+    assert dx is None and dw is bufs[1] and not dw.any() and not db.any()
+    for bad in (dict(dx=bufs[0][:-1]), dict(dweight=bufs[1].float()), dict(dbias=bufs[2].cpu())):
+        with pytest.raises(ValueError):
+            backward(d, stats, **bad)
+
+
 def test_empty_batch():
     d = dev(make(2, 100, 32, seed=1, bias=True))
     e = {n: t if n in ("w", "bias") else t[:0] for n, t in d.items()}
