@@ -583,8 +583,8 @@ nvfp4_status nvfp4_int8_gemm(const int8_t* xq, const float* x_scales, int64_t M,
  *   dz[i, j]    = bf16_rne( (dloss[i] + dlse[i]) * p[i, j] - dloss[i] * 1[j = t] )
  *   dx[i, k]    = bf16_rne( sum_j dz[i, j] * weight[j, k] )
  *   dweight[j, k] = bf16_rne( sum_i dz[i, j] * x[i, k] ),  dbias[j] = bf16_rne( sum_i dz[i, j] )
- * float32 sums.  dz is rounded to bf16 because it is an operand of the two products; in
- * dbias the targets' dz count unrounded.
+ * float32 sums.  dz is rounded to bf16 because it is an operand of the two products; what that takes from
+ * the targets' dz, the large ones, is added to all three sums (to dweight's rounded to bf16 itself).
  *
  *   x          in  bf16 [M, K], 16-byte aligned; 0 <= M <= 2^22 (M == 0 enqueues nothing: a
  *                  caller's dweight and dbias stay as they are)

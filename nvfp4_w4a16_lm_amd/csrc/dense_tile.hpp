@@ -53,7 +53,8 @@ enum TileEpilogue : int {
   kTileGated,       // P = [gate; up]: out a = silu(g) u, optionally h = [g, u] in float32
   kTileGatedBack,   // acc = da: dh = [da u silu'(g), da silu(g)], from h
   kTileCeStats,     // per (m, tile of n): maximum and sum of exp, and the target's logit
-  kTileCeGrad       // out bf16 [m][n] = gradient of the logits
+  kTileCeGrad,      // out bf16 [m][n] = gradient of the logits
+  kTileCeWeight     // out bf16 [m][n], m a token: acc + sum over the rows i with that target of bf16(rest[i]) * P[i][n]
 };
 
 struct TileArgs {
@@ -85,8 +86,12 @@ struct TileArgs {
   float* tlogit;             // [m]
   const float2* stats;       // [m] (maximum, sum)
   const float2* coef;        // [m] (dloss + dlse, dloss)
-  float* rest;               // [m] what rounding took from the gradient of the target's logit, or NULL
+  float* rest;               // [row] what rounding took from the gradient of the target's logit
+  uint32_t* hits;            // [block of kTileHitBlock tokens][hit_words] bits of the rows whose target is in the block:
+                             // written by the gradient of the logits (may be NULL), read by the weight's
+  int32_t hit_words;
 };
+constexpr int kTileHitBlock = 128;
 
 // s_waitcnt immediate: vmcnt(vm) lgkmcnt(0), expcnt left alone
 constexpr int tile_wait(int vm) { return (vm & 15) | ((vm >> 4) << 14) | 0x0070; }
@@ -111,6 +116,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {      // neares
 }
 // What rounding v to hi left over; nothing where hi is not finite (an infinity's product or sum is the one of hi alone).
 __device__ __forceinline__ float rest_bf16(float v, float hi) { return fabsf(hi) < INFINITY ? v - hi : 0.0f; }
+// A remainder's product: with an infinite factor the result is the one of the rounded value alone, the remainder's
+// being infinite of either sign, or NaN where it is 0.
+__device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) < INFINITY ? v : 0.0f; }
 __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
@@ -366,6 +374,18 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
     }
   };
 
+  // kTileCeWeight: bits of the rows 32 word .. + 31 that have their target in this tile, the first ones under way early
+  constexpr int kHitBlocks = C::EPI == kTileCeWeight ? BM / kTileHitBlock : 1;
+  const int hit_words = C::EPI == kTileCeWeight ? (K + 31) / 32 : 0;
+  uint32_t hit[kHitBlocks] = {};
+  auto read_hits = [&](int word) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < kHitBlocks; ++b)
+      hit[b] = word < hit_words && m0 + kTileHitBlock * b < M
+                   ? a.hits[(int64_t)(m0 / kTileHitBlock + b) * a.hit_words + word] : 0u;
+  };
+  if constexpr (C::EPI == kTileCeWeight) read_hits(tid);
+
   if constexpr (C::kUnits) {
     constexpr int early = (C::kCopies + 3) / 4;                 // what sub-step 3 before the first would have copied
     static_assert(C::copy_slot(early - 1) < kMf && C::copy_slot(early) >= kMf && early <= kQC, "copies before sub-step 0");
@@ -414,6 +434,72 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
   __builtin_amdgcn_s_waitcnt(tile_wait(0));
   __syncthreads();
 
+  if constexpr (C::EPI == kTileCeWeight) {
+    // The remainders, as steps of their own: the rows that have their target in this tile, in order, 64 at a time, P of
+    // them against one remainder each, rounded to bf16.  Few tiles have any: of 4096 rows 8 have their target among 256
+    // of 128256 tokens.  Rows lie so that a sub-step takes 16 of them (333 x 32003 x 2080, dW: whole steps 75 us, so 70).
+    static_assert(C::kUnits && PT && QT && BM % kTileHitBlock == 0, "remainders");
+    constexpr int kEnd = kPPr * 1024 + kQPr * 1024;              // of a step's P and Q
+    uint8_t* const pb = lds + C::p_at(0);
+    uint8_t* const qb = lds + C::q_at(0);
+    static_assert(C::p_at(0) == 0 && C::q_at(0) == C::kPBytes && kEnd + 512 <= C::kLds, "remainders");
+    int* const from = reinterpret_cast<int*>(lds + kEnd);
+    int* const part = from + 64;
+    for (int base = 0; base < hit_words; base += kTileThreads) {
+      const int word = base + tid;
+      if (base > 0) read_hits(word);
+      uint32_t bits = 0;
+#pragma unroll
+      for (int b = 0; b < kHitBlocks; ++b) bits |= hit[b];
+      int sum = __popc(bits);                                    // up to and with this thread's
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int below = __shfl_up(sum, d, 64);
+        sum += lane >= d ? below : 0;
+      }
+      if (lane == 63) part[wave] = sum;
+      __syncthreads();
+      int first = sum - __popc(bits), total = 0;
+#pragma unroll
+      for (int w = 0; w < kTileThreads / 64; ++w) {
+        first += w < wave ? part[w] : 0;
+        total += part[w];
+      }
+      for (int done = 0; done < total; done += 64) {
+        const int count = min(total - done, 64);
+        int at = first - done;
+        for (uint32_t left = bits; left != 0; left &= left - 1, ++at)
+          if ((uint32_t)at < 64u) from[at] = 32 * word + __ffs((int)left) - 1;
+        const int steps = (count + 15) / 16;                     // sub-steps, 16 rows each
+        auto place = [&](int x) __attribute__((always_inline)) { return 8 * (x >> 4) + 32 * ((x >> 3) & 1) + (x & 7); };
+        for (int e = tid; e < 16 * steps * kQPr; e += kTileThreads)
+          *reinterpret_cast<u32x4*>(qb + 16 * (place(e / kQPr) * kQPr + e % kQPr)) = u32x4{0, 0, 0, 0};
+        __syncthreads();
+        if (tid < count) {
+          const int i = from[tid], m = a.tok[i] - a.n_first - m0, k = place(tid);
+          *reinterpret_cast<uint16_t*>(qb + 16 * (k * kQPr + ((m >> 3) ^ tr_swizzle(k, kQPr))) + 2 * (m & 7)) =
+              (uint16_t)pack_bf16(a.rest[i], 0.0f);
+        }
+        for (int e = tid; e < 16 * steps * kPPr; e += kTileThreads) {
+          const int x = e / kPPr, k = place(x), n = n0 + 8 * (e % kPPr ^ tr_swizzle(k, kPPr));
+          u32x4 v = {0, 0, 0, 0};
+          if (x < count && n < a.N) v = *reinterpret_cast<const u32x4*>(a.p + from[x] * a.p_pitch + 2 * n);
+          *reinterpret_cast<u32x4*>(pb + 16 * (k * kPPr + e % kPPr)) = v;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (u >= steps) break;
+#pragma unroll
+          for (int x = 0; x < kReads; ++x) read_one(0, u, x, pf[u & 1], qf[u & 1]);
+#pragma unroll
+          for (int s = 0; s < kMf; ++s) acc[s / JT][s % JT] = mfma(pf[u & 1][s / JT], qf[u & 1][s % JT], acc[s / JT][s % JT]);
+        }
+        __syncthreads();                                         // before the next ones take their places
+      }
+      if (total == 0) __syncthreads();                           // part is read before it is written again
+    }
+  }
   if constexpr (C::EPI == kTileCeStats) {
     // Each lane holds 16 IT logits of each of its JT rows; wavefronts of a row meet in LDS.
     float2* const red = reinterpret_cast<float2*>(lds);          // [WN][BM]
@@ -525,12 +611,10 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
         if constexpr (C::EPI == kTileF32) {
           if (a.pair_rows != 0) {
             const f32x4* const low = reinterpret_cast<const f32x4*>(stage + (row + a.pair_rows) * C::kStagePitch + 8 * c);
-            // of an infinite weight too the product is the one of the first half alone: the rest's is infinite of any
-            // sign, or NaN where it is 0
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              lo[e] += fabsf(low[0][e]) < INFINITY ? low[0][e] : 0.0f;
-              hi[e] += fabsf(low[1][e]) < INFINITY ? low[1][e] : 0.0f;
+              lo[e] += finite_or_0(low[0][e]);
+              hi[e] += finite_or_0(low[1][e]);
             }
           }
           if (a.accumulate) {
@@ -558,6 +642,18 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
     constexpr int kW = C::EPI == kTileGated ? BN / 2 : BN;       // columns written
     constexpr int kJP = C::kStageJ;                              // column tiles of a wavefront per pass
     uint16_t* const stage = reinterpret_cast<uint16_t*>(lds);
+    if constexpr (C::EPI == kTileCeGrad) {
+      const int m = m0 + tid, t = tid < BM && m < M ? a.tok[m] - a.n_first - n0 : -1;
+      if (a.hits != nullptr && 64 * wave < BM) {
+#pragma unroll
+        for (int b = 0; b < BN / kTileHitBlock; ++b) {
+          const uint64_t bits = __ballot(t >= 0 && t / kTileHitBlock == b);
+          const int word = m0 / 32 + 2 * wave + h;
+          if (r == 0 && 32 * (2 * wave + h) < BM && word < a.hit_words)
+            a.hits[(int64_t)(n0 / kTileHitBlock + b) * a.hit_words + word] = (uint32_t)(bits >> (32 * h));
+        }
+      }
+    }
     float cs[C::I8 ? IT : 1][4][4], cb[C::I8 || C::EPI == kTileCeGrad ? IT : 1][4][4];
     const bool has_bias = (C::I8 || C::EPI == kTileCeGrad) && a.bias != nullptr;
     if constexpr (C::I8 || C::EPI == kTileCeGrad) {
@@ -643,7 +739,7 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
                   make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
             }
           if constexpr (C::EPI == kTileCeGrad) {
-            if (a.rest != nullptr && m < M && tok >= 0 && tok < 32 * IT && (tok & 4) == 0)
+            if (m < M && tok >= 0 && tok < 32 * IT && (tok & 4) == 0)
               a.rest[m] = rest_bf16(at_target, bf16_lo(pack_bf16(at_target, 0.0f)));
           }
         }

@@ -118,7 +118,8 @@ def linear_ce(x, w, targets, bias=None):
 
 
 def linear_ce_backward(x, w, targets, dloss, dlse=None, bias=None):
-    """((dx, dw, db), bounds of each) with dz rounded to bf16 as an operand; in db the targets' dz count unrounded."""
+    """((dx, dw, db), bounds of each): dz rounded to bf16 as an operand, and what rounding took from the targets' dz added
+    to each result (for dw rounded to bf16 itself)."""
     m, v = x.shape[0], w.shape[0]
     k = x.shape[1]
     rows = _rows(targets, v)
@@ -140,13 +141,15 @@ def linear_ce_backward(x, w, targets, dloss, dlse=None, bias=None):
     unrounded = ez + TINY
     ez = ez + HALF * (np.abs(dz) + ez) + TINY
     az = np.abs(dz) + ez
+    ez = np.where(one > 0, unrounded, ez)
     dx, bx = np.zeros((m, k)), np.zeros((m, k))
     dx[rows] = dz @ w
-    bx[rows] = ez @ np.abs(w) + acc(v, JOINS) * (az @ np.abs(w))
+    bx[rows] = ez @ np.abs(w) + acc(v, JOINS + 1) * (az @ np.abs(w))
+    hits = one.sum(0)[:, None]                           # more terms of a row of dw
     dw = dz.T @ xr
-    bw = ez.T @ np.abs(xr) + acc(len(rows)) * (az.T @ np.abs(xr))
+    bw = (ez + HALF * HALF * az * one).T @ np.abs(xr) + (acc(len(rows)) + 2.0 * U * (hits + 1.0)) * (az.T @ np.abs(xr))
     db = dz.sum(0)
-    bb = np.where(one > 0, unrounded, ez).sum(0) + acc(len(rows)) * az.sum(0)
+    bb = ez.sum(0) + acc(len(rows)) * az.sum(0)
     return (dx, dw, db), tuple(b + HALF * (np.abs(y) + b) + TINY for y, b in ((dx, bx), (dw, bw), (db, bb)))
 
 

@@ -284,6 +284,43 @@ def test_bound_of_the_bias_gradient_tells_rounded_targets(m, v, k):
     assert lost[np.unique(t)].max() > 2.0 and np.delete(lost, np.unique(t)).max() <= 1.0
 
 
+def tied_targets(m, v, k, seed):
+    """Few targets, of larger weights than the other tokens.  Rows of a target share their x, and their dz at it add up to
+    about nothing: its row of dw is a small sum of large terms."""
+    x, w, bias, t, _ = shared_targets(m, v, k, seed)
+    rng = np.random.default_rng(seed + 1)
+    targets = np.unique(t)
+    x = bf16(rng, v, k)[t]
+    w[:] = bf16(rng, v, k, sigma=0.02)
+    w[targets] = bf16(rng, len(targets), k, sigma=1.2 / np.sqrt(k))
+    dloss = np.where(rng.random(m) < 0.5, 1.0, -1.0) * rng.uniform(0.5, 1.0, m)
+    for u in targets:
+        rows = np.nonzero(t == u)[0]
+        z = x[rows[0]] @ w.T + bias
+        p = np.exp(z[u] - np.log(np.exp(z).sum()))
+        # one row alone: a dz nearly half a step (2^-8) above 161/128
+        dloss[rows[-1]] = -dloss[rows[:-1]].sum() if len(rows) > 1 else -(161 / 128 + 0.95 / 256) / (1.0 - p)
+    return x, w, bias, t, dloss.astype(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("m,v,k", [(1, 1003, 64), (5, 300, 16), (20, 1003, 64), (130, 4003, 16), (700, 6003, 144)])
+def test_bounds_of_the_gradients_tell_rounded_targets(m, v, k):
+    """dx and dw from dz rounded everywhere are outside their bounds; with the targets' dz unrounded inside."""
+    x, w, bias, t, dloss = tied_targets(m, v, k, seed=m)
+    (dx, dw, _), (bx, bw, _) = D.linear_ce_backward(x, w, t, dloss, None, bias)
+    z = x @ w.T + bias
+    dz = np.exp(z - z.max(1, keepdims=True))
+    dz *= (dloss / dz.sum(1))[:, None]
+    one = np.zeros_like(dz)
+    one[np.arange(m), t] = 1.0
+    dz -= dloss[:, None] * one
+    low = lambda a: torch.from_numpy(a).to(torch.bfloat16).double().numpy()
+    off = lambda q: [(np.abs(low(y) - want) / bound).max() for y, want, bound in ((q @ w, dx, bx), (q.T @ x, dw, bw))]
+    assert max(off(np.where(one > 0, dz, low(dz)))) <= 1.0
+    lost = off(low(dz))
+    assert min(lost) > 1.2, lost
+
+
 def test_gated_ffn_against_torch_and_differences():
     rng = np.random.default_rng(3)
     x, w13, w2, dy = bf16(rng, 5, 16), bf16(rng, 64, 16), bf16(rng, 16, 32), bf16(rng, 5, 16)

@@ -11,7 +11,7 @@ import oracle.dense_oracle as D
 from nvfp4_w4a16_lm_amd import binding as B
 
 from gpu_util import DEV
-from test_boundary_dense import shared_targets
+from test_boundary_dense import shared_targets, tied_targets
 from test_gpu_graphs import capture
 
 pytestmark = pytest.mark.gpu
@@ -114,6 +114,25 @@ def test_bias_gradient_takes_the_targets_unrounded(m, v, k):
     x, w, bias, t, dloss = (torch.from_numpy(n) for n in shared_targets(m, v, k, seed=m))
     check(dict(x=x.to(BF16), w=w.to(BF16), bias=bias.to(BF16), t=t.to(torch.int32), dloss=dloss.float(), dlse=None),
           dlse=False)
+
+
+@pytest.mark.parametrize("m,v,k", [(1, 1003, 64), (5, 300, 16), (20, 1003, 64), (40, 300003, 16), (130, 4003, 16), (333, 22003, 208),
+                                   (700, 6003, 144), (1100, 9000, 144), (8500, 9003, 16)])
+def test_gradients_take_the_targets_unrounded(m, v, k):
+    """Rows of a target share their x, and their dz at it add up to about nothing: what rounding takes from them is
+    several times the bounds of dx and of the target's row of dweight.  One to some thousand rows a target, in both pieces of
+    a wide vocabulary, in every tile of the logits and of the weight's gradient."""
+    x, w, bias, t, dloss = (torch.from_numpy(n) for n in tied_targets(m, v, k, seed=m))
+    check(dict(x=x.to(BF16), w=w.to(BF16), bias=bias.to(BF16), t=t.to(torch.int32), dloss=dloss.float(), dlse=None),
+          dlse=False)
+
+
+@pytest.mark.parametrize("m", [150, 4000])
+def test_one_target_for_all_rows(m):
+    a = make(m, 1003, 144, seed=m, bias=True)
+    a["t"][:] = 700
+    a["t"][:m // 3] = -1
+    check(a)
 
 
 @pytest.mark.parametrize("m", [1, 40, 300])
