@@ -31,7 +31,9 @@
 // What bounds it.  Large products: the card's power.  With the matrix units 66 to 82 % busy
 // the clock falls to 1.3 to 1.5 GHz (1.2 to 1.38 PFLOP/s, int8 2.3 POPS; a library product reaches 1.18 to
 // 1.47 and 2.5; the same products of zeros run 1.4 times as fast).  Few rows: HBM, 5.2 to 5.7 TB/s.  Between, from 65 to
-// some 500 rows: rows of padding, starts and epilogues of one or two rounds of workgroups.
+// some 500 rows: rows of padding, starts and epilogues of one or two rounds of workgroups.  Few columns too: the compute units
+// without a tile, where K is not split.  The 256 x 256 forms with the softmax's sums, the gate and the scales spill 34,
+// 16 and 4 registers a lane around their epilogues, none in the steps (the sums of 3890 x 128256 write 290 MB for it).
 #pragma once
 
 #include <type_traits>
@@ -437,7 +439,8 @@ __global__ __launch_bounds__(kTileThreads, C::kPerCu) void dense_tile_kernel(Til
   if constexpr (C::EPI == kTileCeWeight) {
     // The remainders, as steps of their own: the rows that have their target in this tile, in order, 64 at a time, P of
     // them against one remainder each, rounded to bf16.  Few tiles have any: of 4096 rows 8 have their target among 256
-    // of 128256 tokens.  Rows lie so that a sub-step takes 16 of them (333 x 32003 x 2080, dW: whole steps 75 us, so 70).
+    // of 128256 tokens.  Rows lie so that a sub-step takes 16 of them (step of 333 x 32003 x 2080: 253 us; with
+    // four sub-steps always 265, without the remainders 243).
     static_assert(C::kUnits && PT && QT && BM % kTileHitBlock == 0, "remainders");
     constexpr int kEnd = kPPr * 1024 + kQPr * 1024;              // of a step's P and Q
     uint8_t* const pb = lds + C::p_at(0);
@@ -805,6 +808,8 @@ inline int64_t tile_count(TileSize t, int64_t M, int64_t N) {
   const TileShape s = tile_shape(t);
   return (M + s.bm - 1) / s.bm * ((N + s.bn - 1) / s.bn);
 }
+
+inline int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }   // a workspace's parts start at multiples of 256
 
 constexpr int kTileCus = 256;      // fixed, so that a workspace's size does not depend on the device that is current
 

@@ -13,9 +13,10 @@
 // of 0.0024, where one rounding of the result is 0.0017; the step of 4096 tokens is 4 % faster.)  Backward:
 // the kernel of da = dy W2 ends in [dg, du], in bf16 as operands; then three products.
 //
-// Measured: one token of (4096, 14336) 68 us (5.2 TB/s: 42 us both projections at 5.5 TB/s, 22 the down projection in
-// 16 parts, 5 their join), 16 tokens 71 us; the step of 4096 tokens 3.4 ms (1.27 PFLOP/s: 0.83, 0.36, 0.54, 0.43,
-// 0.72, 0.75 ms in the order above); of 333 tokens of (2080, 5616) 167 us.
+// Measured: one token of (4096, 14336) 69 us (5.1 TB/s: 43 us both projections at 5.5 TB/s, 22 the down projection in
+// 16 parts, 5 their join), 16 tokens 72 us; the step of 4096 tokens 3.4 ms (1.26 PFLOP/s: 0.85, 0.37, 0.54, 0.43,
+// 0.73, 0.77 ms in the order above); of 333 tokens of (2080, 5616) 153 us on inputs in the last-level cache, 175 us from
+// memory.  Small I: both projections are a workgroup for 64 columns, one token of (4096, 1408) 40 us, floor 7.
 #include "dense_tile.hpp"
 
 namespace nvfp4 {
@@ -28,8 +29,6 @@ __global__ __launch_bounds__(256) void gated_join_kernel(const float* __restrict
   tile_join(parts, i, count, splits, i < count, v);
   if (threadIdx.x < 64 && i < count) *reinterpret_cast<u32x4*>(out + i) = pack8(v);
 }
-
-static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // The down projection and dx: K split where the tiles are few, at least 8 steps a part.
 static TileSplit gated_split(int64_t M, int64_t N, int64_t K) { return tile_split(M, N, K, 8, 16); }

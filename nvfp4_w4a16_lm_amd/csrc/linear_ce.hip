@@ -8,7 +8,7 @@
 // dz enters the products rounded to bf16.  A row's target has by far its largest dz, and what rounding takes from it is
 // the same share of all it adds to a row of dx and of dW: it is kept (rest) and added to each result.  Gradients are
 // then off by 0.0017 of their norm, which is their own rounding (without: 0.0024, 0.0028 of 17 rows, up to 0.0032 of one).
-// It costs 0.4 % of the step of 4096 rows, 4 % of that of 333 (dW 62 -> 70 us).
+// It costs 0.4 % of the step of 4096 rows, 4 % of that of 333 (243 -> 253 us, in dW).
 //
 // Rows whose target is outside the vocabulary have no loss and no gradient: the
 // rows that count are gathered first, and only they enter the products.
@@ -16,17 +16,15 @@
 // Forward: tiles of logits end as one maximum and one sum per row and tile,
 // which a second kernel joins.  Backward, for each piece of the vocabulary: the
 // logits again, ending in dz (bf16, the operand type of what follows); dx gains dz W
-// in float32; the piece of dW is dz^T x.  A piece's dz is 128 MB at most, half of the last-level
-// cache.
+// in float32; the piece of dW is dz^T x.  A piece's dz is 128 MB at most up to 65536 rows, 2 KB a row beyond.
 //
 // Measured: loss of 2048 x 128256 x 4096 1.65 ms (1.31 PFLOP/s), with gradients at 4096 rows, 5 % of them
-// without a target, 12.6 ms (1.3 PFLOP/s: logits 3.2, again 3.5, dx 3.2, dW 3.2 ms); both bound by the
-// card's power.  333 x 32003 x 2080 258 us; 17 x 32003 x 512 44 us in eight launches, the host's pace.
+// without a target, 12.9 ms (1.26 PFLOP/s: logits 3.2, again 3.6, dx 3.2, dW 3.2 ms); both bound by the
+// card's power.  333 x 32003 x 2080 253 us on inputs in the last-level cache, 279 us from memory.  17 x 32003 x 512
+// 44 us: eight launches, whose kernels take 46 us one after the other.
 #include "dense_tile.hpp"
 
 namespace nvfp4 {
-
-static int64_t up256(int64_t b) { return (b + 255) / 256 * 256; }
 
 struct CeGather {
   const uint16_t* x;
@@ -197,7 +195,9 @@ __global__ __launch_bounds__(256) void ce_bias_kernel(const uint16_t* __restrict
   }
 }
 
-constexpr int64_t kCePieceBytes = (int64_t)128 << 20;   // dz of a piece: stays in the last-level cache
+// dz of a piece.  It bounds the workspace: 4096 x 128256 x 4096 takes 13.9 ms in pieces of 32 MB, 12.9 of 128 and 512 MB, 12.8
+// of 2 GB; 16384 rows 70.8, 52.5, 51.0, 51.4 ms.
+constexpr int64_t kCePieceBytes = (int64_t)128 << 20;
 constexpr int64_t kCePieceMost = 1 << 18;               // its columns: 32-bit offsets
 
 struct CeLayout {
@@ -401,9 +401,10 @@ hipError_t launch_linear_ce_backward(const void* x, int64_t M, int64_t K, const 
     }
   }
   if (dx == nullptr) return hipSuccess;
-  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M, (unsigned)((K + 511) / 512)), dim3(256), stream, (const float*)(ws + l.acc),
-                       (int)M, (int)K, l.dx.splits, (const uint16_t*)w, (const int32_t*)g.ctok,
-                       (const float*)(ws + l.rest), (const int32_t*)g.index, (const int32_t*)g.count, (uint16_t*)dx);
+  return launch_kernel((const void*)ce_dx_kernel, dim3((unsigned)M, (unsigned)((K + 511) / 512)), dim3(256), stream,
+                       (const float*)(ws + l.acc), (int)M, (int)K, l.dx.splits, (const uint16_t*)w,
+                       (const int32_t*)g.ctok, (const float*)(ws + l.rest), (const int32_t*)g.index,
+                       (const int32_t*)g.count, (uint16_t*)dx);
 }
 
 }  // namespace nvfp4
