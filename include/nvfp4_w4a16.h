@@ -496,7 +496,8 @@ typedef enum {
  *                      word j / 32 is set; logits of the others are not looked at, whatever
  *                      they hold (NULL = all allowed)
  *   topk           in  0 .. 64 alternatives
- *   workspace      tmp nvfp4_logprobs_workspace_bytes(M, V, topk) bytes, 16-byte aligned
+ *   workspace      tmp nvfp4_logprobs_workspace_bytes(M, V, topk) bytes, 16-byte aligned; the size never falls
+ *                      as M grows, so that one workspace serves every batch up to its own
  *   token_logprobs, token_ranks, lse, entropy   out  float / int32 [M], each optional (NULL)
  *   top_logprobs, top_ids   out  float / int32 [M, topk] (NULL only if topk == 0)
  *

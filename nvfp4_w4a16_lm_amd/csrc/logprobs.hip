@@ -713,10 +713,13 @@ int64_t logprobs_segments(int64_t M, int64_t V) {
   return (steps + per - 1) / per;
 }
 
+// Holds M rows' segments and those of every smaller batch: a row has as many as a single one at most, and from two
+// segments a row on they are fewer than 2048 + M, M below 2048.
 int64_t logprobs_workspace_bytes(int64_t M, int64_t V, int64_t topk) {
-  const int64_t segs = logprobs_segments(M, V);
-  if (segs == 1) return 16;
-  return std::max<int64_t>(16, M * segs * ((int64_t)sizeof(LogprobsPart) + 8 * topk));   // 0 would be a refusal
+  const int64_t most = logprobs_segments(1, V);
+  if (most == 1) return 16;
+  const int64_t parts = std::min(M * most, 2048 + std::min<int64_t>(M, 2047));
+  return std::max<int64_t>(16, parts * ((int64_t)sizeof(LogprobsPart) + 8 * topk));      // 0 would be a refusal
 }
 
 hipError_t launch_logprobs(LogprobsArgs a, int dtype, int64_t M, void* workspace, hipStream_t stream) {

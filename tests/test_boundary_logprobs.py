@@ -121,3 +121,14 @@ def test_workspace_of_every_accepted_size(lib):
                 assert lib.nvfp4_logprobs_workspace_bytes(m, v, topk) >= 16, (m, v, topk)
     b = B.logprobs_buffers(0, 128256, 5, "cpu")
     assert b.lse.shape == (0,) and b.top_ids.shape == (0, 5)
+
+
+@pytest.mark.parametrize("v", [1, 4096, 4097, 32003, 128256, 151936, 1 << 20, 1 << 30])
+@pytest.mark.parametrize("topk", [0, 5, 64])
+def test_workspace_of_a_batch_serves_every_smaller_one(lib, v, topk):
+    """Sizes do not fall as the batch grows."""
+    last = 0
+    for m in [*range(4200), 1 << 14, 1 << 17, 1 << 23]:
+        n = lib.nvfp4_logprobs_workspace_bytes(m, v, topk)
+        assert n >= last, (m, n, last)
+        last = n

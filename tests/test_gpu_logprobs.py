@@ -477,3 +477,17 @@ def test_backward_mixes_rows_of_either_kind():
     x[4] -= 1e6
     temps = np.float32([1.0, 1.0, 1e-3, 0.8, 1.0, 1e-38])
     check_backward_relative(x, np.arange(m, dtype=np.int32), temps)
+
+
+def test_workspace_kept_for_the_largest_batch():
+    """One workspace of the largest batch for every smaller one, and nothing behind it is written."""
+    v, topk, most = 70001, 20, 2100
+    size = int(B.load_library().nvfp4_logprobs_workspace_bytes(most, v, topk))
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    x = make_logits(most, v, BF16, 21)
+    ids = torch.arange(most, dtype=torch.int32, device=DEV) % v
+    for m in (most, 2048, 2047, 1025, 1024, 700, 64, 2, 1):
+        want = B.nvfp4_logprobs(x[:m], ids[:m], topk=topk)
+        got = B.nvfp4_logprobs(x[:m], ids[:m], topk=topk, out=B.logprobs_buffers(m, v, topk, DEV)._replace(workspace=ws[:size]))
+        assert all(torch.equal(a, b) for a, b in zip(got[:6], want[:6])), m
+        assert torch.all(ws[size:] == 0xA5)
